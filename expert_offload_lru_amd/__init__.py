@@ -1,8 +1,9 @@
 """MI355X offloaded mixture-of-experts layer with an LRU expert cache.
 
-Thin ctypes binding over the C ABI of ``include/moe_offload.h`` (GPU
-library ``libmoe_offload.so``) and ``include/moe_planner.h`` (host slot table,
-also built alone as ``libmoe_planner.so`` without HIP).  The binding only
+Thin ctypes binding over the C ABI of ``include/moe_offload.h`` and
+``include/moe_tokens.h`` (GPU library ``libmoe_offload.so``) and
+``include/moe_planner.h`` (host slot table, also built alone as
+``libmoe_planner.so`` without HIP).  The binding only
 marshals arguments: every step of the layer runs in the native library.
 PyTorch tensors are accepted for device memory and streams.
 
@@ -30,6 +31,8 @@ POOL_SHARED, SHARED_EXPERT, PREFETCH, WAVES_UNION, POLICY_LFU, ADAPTIVE_CAPACITY
 # forward flags
 FWD_RESIDUAL = 0x1
 DECODE_MAX_TOKENS = 32
+# element types of the token and adapter operators
+T_F32, T_F16, T_BF16 = 0, 1, 2
 # timing mask
 TIME_ROUTER, TIME_GATE_UP, TIME_DOWN, TIME_COMBINE, TIME_PREFILL, TIME_FUSED = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 TIME_GATE_UP_EARLY = 0x40
@@ -160,6 +163,18 @@ def _declare_gpu(lib):
     lib.moe_cache_destroy.argtypes = [vp]
     lib.moe_cache_destroy.restype = None
     lib.moe_debug_decode.argtypes = [i, i, vp, i, vp, vp]
+    ld = ctypes.c_int64
+    lib.moe_tokens_workspace.argtypes = [i, i, i]
+    lib.moe_tokens_workspace.restype = sz
+    lib.moe_tokens_dispatch.argtypes = [vp, ld, i, i, i, vp, i, i, vp, ld, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_tokens_dispatch_backward.argtypes = [vp, ld, ld, i, i, i, vp, i, vp, ld, vp]
+    lib.moe_tokens_combine.argtypes = [vp, ld, ld, i, i, i, vp, vp, i, vp, ld, vp, ld, vp]
+    lib.moe_tokens_combine_backward.argtypes = [vp, ld, vp, ld, ld, i, i, i, vp, vp, i, vp, ld, vp, vp]
+    lib.moe_adapters_forward.argtypes = [vp, ld, vp, ld, i, i, i, i, vp, vp, vp, i, vp, i, i, vp, ld, vp]
+    lib.moe_adapters_workspace.argtypes = [i, i, i, i, i]
+    lib.moe_adapters_workspace.restype = sz
+    lib.moe_adapters_backward.argtypes = [vp, ld, vp, ld, vp, ld, i, i, i, i, vp, vp, vp, i, vp, i, i, vp, ld, vp, vp,
+                                          vp, sz, vp]
 
 
 _gpu_lib = None
@@ -469,3 +484,16 @@ class Planner:
             self.close()
         except Exception:
             pass
+
+
+_TOKEN_OPS = ("tokens_dispatch", "tokens_dispatch_backward", "tokens_combine", "tokens_combine_backward",
+              "adapters_forward", "adapters_backward")
+
+
+def __getattr__(name):
+    # the token and adapter operators take torch tensors: torch is imported on their first use
+    if name in _TOKEN_OPS:
+        from . import tokens
+        globals()[name] = getattr(tokens, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

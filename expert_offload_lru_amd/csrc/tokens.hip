@@ -1,0 +1,333 @@
+// Tokens sorted by expert and back (include/moe_tokens.h): a stable counting sort of the picks fused
+// with the copy of the rows, the weighted sum of a token's rows, and its gradients.
+//
+// All of it is bound by memory (at most three flops an element), so every kernel reads each input
+// row once and writes each output row once, in 16-byte pieces, and the small index work rides along.
+#include <algorithm>
+
+#include "elements.hpp"
+#include "token_kernels.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWgPicks = 2048;         // picks a dispatch workgroup ranks at most
+constexpr int kCopies = 8;             // copies of a histogram, by lane: picks of one expert in a
+                                       // wave would otherwise add to one LDS word in turn
+constexpr int kDirectPicks = 32768;    // up to here every workgroup counts all picks itself
+constexpr int kSlicePicks = 8192;      // picks of a histogram slice above
+constexpr int kMaxSlices = 512;
+
+int slices_of(int N) {
+    if (N <= kDirectPicks) return 0;
+    return std::min(kMaxSlices, (N + kSlicePicks - 1) / kSlicePicks);
+}
+int per_slice(int N, int slices) { return (N + slices - 1) / slices; }
+
+// Adds picks p0 .. p1 to the histogram copies.
+__device__ inline void count(const int32_t *ids, int p0, int p1, int E, int *hist) {
+    const int copy = threadIdx.x & (kCopies - 1);
+    for (int p = p0 + (int)threadIdx.x; p < p1; p += kThreads) {
+        const int e = ids[p];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e * kCopies + copy], 1);
+    }
+}
+
+__device__ inline int total_of(const int *hist, int e) {
+    int s = 0;
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) s += hist[e * kCopies + c];
+    return s;
+}
+
+__global__ __launch_bounds__(kThreads) void k_slice_counts(const int32_t *ids, int N, int per, int E, int32_t *counts) {
+    __shared__ int hist[kMaxSegments * kCopies];
+    for (int i = threadIdx.x; i < E * kCopies; i += kThreads) hist[i] = 0;
+    __syncthreads();
+    const int p0 = blockIdx.x * per;
+    count(ids, p0, min(N, p0 + per), E, hist);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads) counts[(size_t)blockIdx.x * E + e] = total_of(hist, e);
+}
+
+// A workgroup takes `tokens` consecutive tokens.  The row of pick p with expert e is
+//   offsets[e] + (valid picks of e before p),
+// so it counts, per expert, all picks and the picks before its own -- from the ids themselves, or for
+// many picks from the slices' counts -- and then ranks its own picks in order, 64 at a time by one
+// wave: the lanes with the same expert are found by one ballot per bit of the id.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int tokens, int lanes_log2, const int32_t *counts,
+                                                       int slices, int per) {
+    __shared__ int hist[kMaxSegments * kCopies];
+    __shared__ int next[kMaxSegments];   // next row of each expert
+    __shared__ int row_of[kWgPicks];
+    __shared__ int wave_sum[kThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int E = a.E, N = a.T * a.k;
+    const int t0 = blockIdx.x * tokens, t1 = min(a.T, t0 + tokens);
+    const int p0 = t0 * a.k, p1 = t1 * a.k;
+
+    for (int i = tid; i < E * kCopies; i += kThreads) hist[i] = 0;
+    __syncthreads();
+    const int slice = counts ? p0 / per : 0;
+    count(a.ids, counts ? slice * per : 0, p0, E, hist);
+    __syncthreads();
+    // four consecutive experts a thread
+    int before[4], total[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * tid + i;
+        before[i] = e < E ? total_of(hist, e) : 0;
+        total[i] = 0;
+        if (counts && e < E) {
+            for (int s = 0; s < slices; ++s) {
+                const int n = counts[(size_t)s * E + e];
+                total[i] += n;
+                before[i] += s < slice ? n : 0;
+            }
+        }
+    }
+    if (!counts) {
+        __syncthreads();
+        count(a.ids, p0, N, E, hist);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total[i] = 4 * tid + i < E ? total_of(hist, 4 * tid + i) : 0;
+    }
+    const int mine = total[0] + total[1] + total[2] + total[3];
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 63) wave_sum[wave] = upto;
+    __syncthreads();
+    int start = upto - mine;
+    for (int w = 0; w < wave; ++w) start += wave_sum[w];
+    const int n_rows = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * tid + i;
+        if (e < E) {
+            next[e] = start + before[i];
+            if (blockIdx.x == 0) a.offsets[e] = start;
+        }
+        start += total[i];
+    }
+    if (blockIdx.x == 0 && tid == 0) a.offsets[E] = n_rows;
+    __syncthreads();
+
+    if (wave == 0) {
+        volatile int *nx = next;
+        for (int p = p0; p < p1; p += 64) {
+            const int q = p + lane;
+            const int e = q < p1 ? a.ids[q] : -1;
+            const bool valid = (unsigned)e < (unsigned)E;
+            unsigned long long same = __ballot(valid);
+            for (int bit = 0; (1 << bit) < E; ++bit) {
+                const bool set = (e >> bit) & 1;
+                const unsigned long long m = __ballot(set);
+                same &= set ? m : ~m;
+            }
+            const int rank = __popcll(same & ((1ull << lane) - 1));
+            int row = -1;
+            if (valid) {
+                const int at = nx[e];
+                row = at + rank;
+                if (rank == 0) nx[e] = at + __popcll(same);
+            }
+            if (q < p1) {
+                row_of[q - p0] = row;
+                if (a.pos) a.pos[q] = row;
+                if (valid) {
+                    a.src[row] = q;
+                    if (a.expert) a.expert[row] = e;
+                }
+            }
+        }
+    }
+    // rows behind the last
+    for (int p = p0 + tid; p < p1; p += kThreads)
+        if (p >= n_rows) {
+            a.src[p] = -1;
+            if (a.expert) a.expert[p] = -1;
+        }
+    if (!a.x) return;
+    __syncthreads();
+
+    const int L = 1 << lanes_log2, group = tid >> lanes_log2, l = tid & (L - 1);
+    const int pieces = (a.H + kVec<T> - 1) / kVec<T>;
+    for (int t = t0 + group; t < t1; t += kThreads >> lanes_log2) {
+        const T *x = static_cast<const T *>(a.x) + (int64_t)t * a.ld_x;
+        for (int c = l; c < pieces; c += L) {
+            const int n = a.H - c * kVec<T>;
+            const uint4 v = load_piece(x + c * kVec<T>, n);
+            for (int j = 0; j < a.k; ++j) {
+                const int row = row_of[(t - t0) * a.k + j];
+                if (row >= 0) store_piece(static_cast<T *>(a.rows) + (int64_t)row * a.ld_rows + c * kVec<T>, v, n);
+            }
+        }
+    }
+}
+
+// L lanes a token (a whole workgroup for wide rows); each lane sums its pieces over the picks in
+// order, eight rows' loads in flight.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_combine_rows(CombineRowsArgs a, int lanes_log2) {
+    const int L = 1 << lanes_log2;
+    const int t = (blockIdx.x << (8 - lanes_log2)) + ((int)threadIdx.x >> lanes_log2);
+    if (t >= a.T) return;
+    const int pieces = (a.H + kVec<T> - 1) / kVec<T>;
+    const T *rows = static_cast<const T *>(a.rows);
+    for (int c = threadIdx.x & (L - 1); c < pieces; c += L) {
+        const int n = a.H - c * kVec<T>;
+        float sum[kVec<T>] = {};
+        if (a.base) unpack<T>(load_piece(static_cast<const T *>(a.base) + (int64_t)t * a.ld_base + c * kVec<T>, n), sum);
+        for (int j0 = 0; j0 < a.k; j0 += 8) {
+            uint4 v[8];
+            float g[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int j = j0 + u;
+                const int row = j < a.k ? a.pos[(int64_t)t * a.k + j] : -1;
+                v[u] = uint4{0, 0, 0, 0};
+                g[u] = 0.f;
+                if (row >= 0 && row < a.n_rows) {
+                    v[u] = load_piece(rows + (int64_t)row * a.ld_rows + c * kVec<T>, n);
+                    g[u] = a.gate ? a.gate[(int64_t)t * a.k + j] : 1.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                float f[kVec<T>];
+                unpack<T>(v[u], f);
+#pragma unroll
+                for (int i = 0; i < kVec<T>; ++i) sum[i] = fmaf(g[u], f[i], sum[i]);
+            }
+        }
+        store_piece(static_cast<T *>(a.out) + (int64_t)t * a.ld_out + c * kVec<T>, pack<T>(sum), n);
+    }
+}
+
+// L lanes a token: d_out's piece is read once and serves every pick's gradient row and dot product.
+// KM: picks held in registers (8 or 16).
+template <typename T, int KM>
+__global__ __launch_bounds__(kThreads) void k_combine_back(CombineBackArgs a, int lanes_log2) {
+    __shared__ float part[kThreads / 64][KM];
+    const int L = 1 << lanes_log2, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int t = (blockIdx.x << (8 - lanes_log2)) + (tid >> lanes_log2);
+    const bool live = t < a.T;
+    const int pieces = live ? (a.H + kVec<T> - 1) / kVec<T> : 0;
+    const T *rows = static_cast<const T *>(a.rows);
+    int row[KM];
+    float gate[KM], dot[KM];
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+        row[j] = live && j < a.k ? a.pos[(int64_t)t * a.k + j] : -1;
+        if (row[j] >= a.n_rows) row[j] = -1;
+        gate[j] = row[j] >= 0 ? a.gate[(int64_t)t * a.k + j] : 0.f;
+        dot[j] = 0.f;
+    }
+    for (int c = tid & (L - 1); c < pieces; c += L) {
+        const int n = a.H - c * kVec<T>;
+        float d[kVec<T>];
+        uint4 v[KM];
+        unpack<T>(load_piece(static_cast<const T *>(a.d_out) + (int64_t)t * a.ld_d_out + c * kVec<T>, n), d);
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            v[j] = uint4{0, 0, 0, 0};
+            if (row[j] >= 0) v[j] = load_piece(rows + (int64_t)row[j] * a.ld_rows + c * kVec<T>, n);
+        }
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            if (row[j] < 0) continue;
+            float f[kVec<T>], s = 0.f;
+            unpack<T>(v[j], f);
+#pragma unroll
+            for (int i = 0; i < kVec<T>; ++i) {
+                s = fmaf(d[i], f[i], s);
+                f[i] = gate[j] * d[i];
+            }
+            dot[j] += s;
+            store_piece(static_cast<T *>(a.d_rows) + (int64_t)row[j] * a.ld_d_rows + c * kVec<T>, pack<T>(f), n);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < KM; ++j)
+        for (int d = min(L, 64) >> 1; d > 0; d >>= 1) dot[j] += __shfl_xor(dot[j], d);
+    if (L <= 64) {
+        if (live && (tid & (L - 1)) == 0)
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (j < a.k) a.d_gate[(int64_t)t * a.k + j] = dot[j];
+        return;
+    }
+    if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < KM; ++j) part[wave][j] = dot[j];
+    __syncthreads();
+    if (live && tid < a.k) a.d_gate[(int64_t)t * a.k + tid] = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+}
+
+// Lanes that share a token: as many as its row has pieces, 8 .. 64, or the whole workgroup of 256.
+int lanes_for(int H, int vec) {
+    const int pieces = (H + vec - 1) / vec;
+    int log2 = 3;
+    while (log2 < 6 && (1 << log2) < pieces) ++log2;
+    return pieces > 64 ? 8 : log2;
+}
+int vec_of(int dtype) { return dtype == T_F32 ? 4 : 8; }
+
+template <typename T>
+hipError_t dispatch(const DispatchArgs &a, int32_t *counts, hipStream_t stream) {
+    const int N = a.T * a.k;
+    const int slices = slices_of(N), per = slices ? per_slice(N, slices) : 1;
+    if (slices) {
+        const hipError_t e = launch(k_slice_counts, dim3(slices), dim3(kThreads), stream, nullptr, nullptr, a.ids, N, per,
+                                    a.E, counts);
+        if (e != hipSuccess) return e;
+    }
+    const int tokens = std::max(1, std::min((a.T + 1023) / 1024, kWgPicks / a.k));
+    const int grid = std::max(1, (a.T + tokens - 1) / tokens);
+    return launch(k_dispatch<T>, dim3(grid), dim3(kThreads), stream, nullptr, nullptr, a, tokens,
+                  lanes_for(a.H, kVec<T>), static_cast<const int32_t *>(slices ? counts : nullptr), slices, per);
+}
+
+}  // namespace
+
+size_t dispatch_workspace(int T, int k, int E) { return (size_t)slices_of(T * k) * E * sizeof(int32_t); }
+
+hipError_t launch_dispatch(int dtype, const DispatchArgs &a, void *workspace, hipStream_t stream) {
+    int32_t *counts = static_cast<int32_t *>(workspace);
+    if (dtype == T_F32) return dispatch<float>(a, counts, stream);
+    if (dtype == T_F16) return dispatch<f16>(a, counts, stream);
+    return dispatch<bf16>(a, counts, stream);
+}
+
+hipError_t launch_combine_rows(int dtype, const CombineRowsArgs &a, hipStream_t stream) {
+    if (a.T == 0) return hipSuccess;
+    const int log2 = lanes_for(a.H, vec_of(dtype)), per = kThreads >> log2;
+    const dim3 grid((a.T + per - 1) / per), block(kThreads);
+    if (dtype == T_F32) return launch(k_combine_rows<float>, grid, block, stream, nullptr, nullptr, a, log2);
+    if (dtype == T_F16) return launch(k_combine_rows<f16>, grid, block, stream, nullptr, nullptr, a, log2);
+    return launch(k_combine_rows<bf16>, grid, block, stream, nullptr, nullptr, a, log2);
+}
+
+template <typename T>
+static hipError_t combine_back(const CombineBackArgs &a, hipStream_t stream) {
+    const int log2 = lanes_for(a.H, kVec<T>), per = kThreads >> log2;
+    const dim3 grid((a.T + per - 1) / per), block(kThreads);
+    return a.k <= 8 ? launch(k_combine_back<T, 8>, grid, block, stream, nullptr, nullptr, a, log2)
+                    : launch(k_combine_back<T, 16>, grid, block, stream, nullptr, nullptr, a, log2);
+}
+
+hipError_t launch_combine_back(int dtype, const CombineBackArgs &a, hipStream_t stream) {
+    if (a.T == 0) return hipSuccess;
+    if (dtype == T_F32) return combine_back<float>(a, stream);
+    if (dtype == T_F16) return combine_back<f16>(a, stream);
+    return combine_back<bf16>(a, stream);
+}
+
+}  // namespace moe

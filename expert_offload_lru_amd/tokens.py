@@ -1,0 +1,198 @@
+"""Token order and adapters: the binding of ``include/moe_tokens.h``.
+
+Every function takes torch tensors on one GPU, checks their shapes and types, and enqueues the
+library's kernels on ``stream`` (default: the current stream of that GPU).  Outputs are tensors that
+the caller holds.  A matrix needs unit stride along its rows (a column slice of a wider matrix will
+do); index, gate, scale, adapter and adapter-gradient tensors are contiguous.  ``MoeError`` with
+``ERR_INVALID`` or ``ERR_UNSUPPORTED`` says what was refused; nothing is enqueued then.
+"""
+import torch
+
+from . import ERR_INVALID, OK, T_BF16, T_F16, T_F32, MoeError, gpu_lib
+
+_TYPES = {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16}
+
+
+def _refuse(msg):
+    raise MoeError(ERR_INVALID, msg)
+
+
+def _matrix(name, t, rows, cols, dtype, device):
+    """Address and row distance of a [rows x cols] matrix."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        _refuse(f"{name} has shape {tuple(t.shape)}, not ({rows}, {cols})")
+    if t.dtype is not dtype:
+        _refuse(f"{name} is {t.dtype}, not {dtype}")
+    if t.device != device:
+        _refuse(f"{name} is on {t.device}, not {device}")
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
+        _refuse(f"{name} is not stored by rows")
+    if rows <= 1:
+        ld = max(ld, cols)
+    if ld < cols:
+        _refuse(f"{name} has rows that overlap")
+    return t.data_ptr(), ld
+
+
+def _dims(name, t, n):
+    if t.dim() != n:
+        _refuse(f"{name} has {t.dim()} dimensions, not {n}")
+    return t.shape
+
+
+def _array(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _type(name, t):
+    if t.device.type != "cuda":
+        _refuse(f"{name} is on {t.device}, not a GPU")
+    if t.dtype not in _TYPES:
+        _refuse(f"{name} is {t.dtype}: float32, float16 or bfloat16 is wanted")
+    return _TYPES[t.dtype]
+
+
+def _call(fn, device, stream, *args):
+    """The library call with `device` current and the stream's handle as last argument."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    else:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    rc = fn(*args, handle)
+    if rc != OK:
+        raise MoeError(rc, gpu_lib().moe_last_error().decode())
+
+
+def _workspace(nbytes, given, device, stream):
+    """A workspace tensor: the caller's, or a new one that belongs to the call's stream."""
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            _refuse(f"workspace must be a contiguous tensor on {device}")
+        return given
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    s = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def tokens_dispatch(x, ids, n_experts, rows, offsets, pos, src, expert, workspace=None, stream=None):
+    """Tokens sorted by expert (moe_tokens_dispatch).
+
+    x [T, H] and ids int32 [T, k] (-1: no pick) give rows [T*k, H] (as x), offsets int32
+    [n_experts+1], pos int32 [T, k], src and expert int32 [T*k]: the valid picks p = t*k + j in the
+    order of (ids[p], p) are rows 0 .. R-1; rows from R on are left as they were.  x = rows = None
+    makes the order alone.
+    """
+    lib = gpu_lib()
+    device = ids.device
+    if device.type != "cuda":
+        _refuse(f"ids is on {device}, not a GPU")
+    T, k = _dims("ids", ids, 2)
+    n = T * k
+    if (x is None) != (rows is None):
+        _refuse("x and rows go together")
+    i32 = torch.int32
+    if x is None:
+        dtype, H, px, ldx, pr, ldr = T_F32, 1, None, 1, None, 1
+    else:
+        dtype, H = _type("x", x), _dims("x", x, 2)[1]
+        px, ldx = _matrix("x", x, T, H, x.dtype, device)
+        pr, ldr = _matrix("rows", rows, n, H, x.dtype, device)
+    p_ids, p_off = _array("ids", ids, (T, k), i32, device), _array("offsets", offsets, (n_experts + 1,), i32, device)
+    p_pos, p_src = _array("pos", pos, (T, k), i32, device), _array("src", src, (n,), i32, device)
+    p_exp = _array("expert", expert, (n,), i32, device)
+    need = lib.moe_tokens_workspace(T, k, n_experts)
+    ws = _workspace(need, workspace, device, stream) if need else None
+    _call(lib.moe_tokens_dispatch, device, stream, px, ldx, dtype, T, H, p_ids, k, n_experts, pr, ldr, p_off, p_pos,
+          p_src, p_exp, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
+
+
+def tokens_dispatch_backward(d_rows, pos, d_x, stream=None):
+    """d_x[t] = sum_j d_rows[pos[t, j]] (moe_tokens_dispatch_backward)."""
+    dtype, device = _type("d_rows", d_rows), d_rows.device
+    (T, k), (R, H) = _dims("pos", pos, 2), _dims("d_rows", d_rows, 2)
+    pr, ldr = _matrix("d_rows", d_rows, R, H, d_rows.dtype, device)
+    px, ldx = _matrix("d_x", d_x, T, H, d_rows.dtype, device)
+    p_pos = _array("pos", pos, (T, k), torch.int32, device)
+    _call(gpu_lib().moe_tokens_dispatch_backward, device, stream, pr, ldr, R, dtype, T, H, p_pos, k, px, ldx)
+
+
+def tokens_combine(rows, pos, gate, out, base=None, stream=None):
+    """out[t] = base[t] + sum_j gate[t, j] rows[pos[t, j]] (moe_tokens_combine); base may be out."""
+    dtype, device = _type("rows", rows), rows.device
+    (T, k), (R, H) = _dims("pos", pos, 2), _dims("rows", rows, 2)
+    pr, ldr = _matrix("rows", rows, R, H, rows.dtype, device)
+    po, ldo = _matrix("out", out, T, H, rows.dtype, device)
+    pb, ldb = (None, H) if base is None else _matrix("base", base, T, H, rows.dtype, device)
+    p_pos = _array("pos", pos, (T, k), torch.int32, device)
+    p_gate = _array("gate", gate, (T, k), torch.float32, device)
+    _call(gpu_lib().moe_tokens_combine, device, stream, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pb, ldb, po, ldo)
+
+
+def tokens_combine_backward(d_out, rows, pos, gate, d_rows, d_gate, stream=None):
+    """d_rows[pos[t, j]] = gate[t, j] d_out[t] and d_gate[t, j] = <d_out[t], rows[pos[t, j]]>
+    (moe_tokens_combine_backward); rows of d_rows that no pick names are left as they were."""
+    dtype, device = _type("rows", rows), rows.device
+    (T, k), (R, H) = _dims("pos", pos, 2), _dims("rows", rows, 2)
+    pd, ldd = _matrix("d_out", d_out, T, H, rows.dtype, device)
+    pr, ldr = _matrix("rows", rows, R, H, rows.dtype, device)
+    pg, ldg = _matrix("d_rows", d_rows, R, H, rows.dtype, device)
+    p_pos = _array("pos", pos, (T, k), torch.int32, device)
+    p_gate = _array("gate", gate, (T, k), torch.float32, device)
+    p_dgate = _array("d_gate", d_gate, (T, k), torch.float32, device)
+    _call(gpu_lib().moe_tokens_combine_backward, device, stream, pd, ldd, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pg,
+          ldg, p_dgate)
+
+
+def _adapter_shapes(a, b, wdtype, device):
+    n, r, inner = _dims("a", a, 3)
+    outer = _dims("b", b, 3)[1]
+    return (n, r, inner, outer, _array("a", a, (n, r, inner), wdtype, device),
+            _array("b", b, (n, outer, r), wdtype, device), _type("a", a))
+
+
+def adapters_forward(x, adapter, a, b, scale, out, base=None, stream=None):
+    """out[i] = base[i] + scale[e] B_e (A_e x[i]) with e = adapter[i] (moe_adapters_forward).
+
+    x [T, inner], adapter int32 [T] (-1: none), a [n, r, inner], b [n, outer, r], scale fp32 [n], out
+    and base [T, outer]; base may be out, and None stands for zeros.  a and b have x's type, or any
+    type beside fp32 activations.
+    """
+    dtype, device, T = _type("x", x), x.device, _dims("x", x, 2)[0]
+    n, r, inner, outer, pa, pb, wtype = _adapter_shapes(a, b, a.dtype, device)
+    px, ldx = _matrix("x", x, T, inner, x.dtype, device)
+    po, ldo = _matrix("out", out, T, outer, x.dtype, device)
+    p_base, ldb = (None, outer) if base is None else _matrix("base", base, T, outer, x.dtype, device)
+    p_ad = _array("adapter", adapter, (T,), torch.int32, device)
+    p_scale = _array("scale", scale, (n,), torch.float32, device)
+    _call(gpu_lib().moe_adapters_forward, device, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
+          wtype, p_scale, n, r, po, ldo)
+
+
+def adapters_backward(d_out, x, adapter, a, b, scale, d_x, d_a, d_b, dx_base=None, workspace=None, stream=None):
+    """Gradients of adapters_forward (moe_adapters_backward): d_x [T, inner] = dx_base + scale A_e^T B_e^T
+    d_out, and the fp32 gradients d_a [n, r, inner] and d_b [n, outer, r] of all adapters.  dx_base may
+    be d_x, and None stands for zeros; a workspace (any contiguous tensor of enough bytes, 16-byte
+    aligned) may be kept by the caller."""
+    lib = gpu_lib()
+    dtype, device, T = _type("x", x), x.device, _dims("x", x, 2)[0]
+    n, r, inner, outer, pa, pb, wtype = _adapter_shapes(a, b, a.dtype, device)
+    px, ldx = _matrix("x", x, T, inner, x.dtype, device)
+    pd, ldd = _matrix("d_out", d_out, T, outer, x.dtype, device)
+    pg, ldg = _matrix("d_x", d_x, T, inner, x.dtype, device)
+    p_base, ldb = (None, inner) if dx_base is None else _matrix("dx_base", dx_base, T, inner, x.dtype, device)
+    p_ad = _array("adapter", adapter, (T,), torch.int32, device)
+    p_scale = _array("scale", scale, (n,), torch.float32, device)
+    p_da = _array("d_a", d_a, (n, r, inner), torch.float32, device)
+    p_db = _array("d_b", d_b, (n, outer, r), torch.float32, device)
+    ws = _workspace(lib.moe_adapters_workspace(T, inner, outer, n, r), workspace, device, stream)
+    _call(lib.moe_adapters_backward, device, stream, pd, ldd, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
+          wtype, p_scale, n, r, pg, ldg, p_da, p_db, ws.data_ptr(), ws.numel() * ws.element_size())

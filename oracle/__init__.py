@@ -15,6 +15,8 @@ lru      two independent LRU slot-pool simulations (linked list, timestamps),
          wave split, a whole-run replay with statistics, prefill plan
 ffn      SwiGLU expert FFN, the MoE layer, a dense brute-force variant
 toy      the toy sticky router and per-pick LRU replay of the explainer page
+tokens   picks in the order of their experts, the weighted way back, low-rank adapters,
+         and the gradients of all three
 report   bus / preflight arithmetic printed on the pages
 
 Parity status: every function is pinned by a test under tests/ that does
