@@ -10,7 +10,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kTileElements = 1 << 30;   // an adapter's matrix in a block kernel: 32-bit offsets
 constexpr int kRowCalls = 256;   // rows of a call that takes a workgroup a row
 
 // n <= 8 elements at p as fp32, zeros behind them.
@@ -78,13 +77,32 @@ __global__ __launch_bounds__(kThreads) void k_adapters_row(AdapterArgs g) {
 }
 
 // ------------------------------------------------------------------ blocks of rows, matrix cores
+//
+// For sizes that 16-byte pieces divide.  All loads and stores of the block kernels are buffer
+// instructions whose lanes with nothing to do carry an offset out of range (a load gives zeros, a store
+// does nothing): without branches around them the compiler keeps them in flight together.
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileThreads = 512;
 constexpr int kTileWaves = kTileThreads / 64;
+constexpr int kTileRows = 16;
+constexpr unsigned kNowhere = 0x80000000u;                   // an offset out of every buffer's range
+constexpr int64_t kBufferBytes = (int64_t)kNowhere - 65536;   // a buffer's size at most
+
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer(const void *p, size_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, p ? (int)bytes : 0, 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(Buffer b, unsigned at) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0));
+}
+__device__ __forceinline__ void store16(Buffer b, unsigned at, u32x4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, b, (int)at, 0, 0);
+}
 
 // The 16x16 products of one lane's chunk of kChunk reduction elements per operand: 16-bit types
 // multiply as they are (v_mfma_f32_16x16x32), fp32 activations in fp32 (four v_mfma_f32_16x16x4,
@@ -114,27 +132,28 @@ struct Mma<float> {
     }
 };
 
-// The chunk at p, n elements of it (zeros behind).  EVEN: n is 0 or less, or the whole chunk, and no
-// code for a part of one is made (it would cost the registers that keep loads in flight).
-template <typename TX, bool EVEN, typename T>
-__device__ __forceinline__ typename Mma<TX>::Frag load_chunk(const T *p, int n) {
-    typedef typename Mma<TX>::Frag Frag;
-    constexpr int C = Mma<TX>::kChunk;
-    if constexpr (sizeof(TX) == 2 || sizeof(T) == 4) {
-        if constexpr (EVEN) return n > 0 ? __builtin_bit_cast(Frag, load_piece(p, C)) : Frag{};
-        return __builtin_bit_cast(Frag, load_piece(p, n));
-    } else {   // four 16-bit weights beside fp32 activations
-        T e[4] = {};
-        if (EVEN ? n > 0 : n >= 4) {
-            __builtin_memcpy(e, p, 8);
-        } else if constexpr (!EVEN) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) e[i] = p[i];
-        }
-        return f32x4{widen(e[0]), widen(e[1]), widen(e[2]), widen(e[3])};
+// A chunk as it is loaded, and as the product takes it (16-bit weights beside fp32 activations are
+// widened there).
+template <typename TX, typename T>
+struct Chunk {
+    static constexpr bool kWide = sizeof(TX) == 4 && sizeof(T) == 2;
+    typename std::conditional<kWide, uint2, u32x4>::type raw;
+    __device__ __forceinline__ void load(Buffer b, unsigned at) {
+        if constexpr (kWide)
+            raw = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(b, (int)at, 0, 0));
+        else
+            raw = load16(b, at);
     }
-}
+    __device__ __forceinline__ typename Mma<TX>::Frag frag() const {
+        if constexpr (kWide) {
+            T e[4];
+            __builtin_memcpy(e, &raw, 8);
+            return f32x4{widen(e[0]), widen(e[1]), widen(e[2]), widen(e[3])};
+        } else {
+            return __builtin_bit_cast(typename Mma<TX>::Frag, raw);
+        }
+    }
+};
 
 // Two parts of v whose sum is v to 16 bits or more; an infinity is all in the first.
 template <typename T>
@@ -144,44 +163,57 @@ __device__ inline void split(float v, T &hi, T &lo) {
     lo = narrow<T>(__builtin_isfinite(rest) ? rest : 0.f);
 }
 
-// Where a lane's 16 rows x NT x MT work sits: lane l has row l%16 of each of the MT sixteens.
+// A lane's place: row l16 of the block, quarter quad of the reduction (or of a piece's 64 bytes).
 struct Lane {
     int l16, quad, wave;
     __device__ Lane()
         : l16(threadIdx.x & 15), quad((threadIdx.x >> 4) & 3), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {}
+    // The same, unknown to the compiler: addresses are computed again from it where they are used, and
+    // not all ahead of the loop over a block's adapters (which spilled 60 registers and more).
+    __device__ __forceinline__ Lane again() const {
+        Lane l = *this;
+        asm volatile("" : "+s"(l.wave), "+v"(l.l16), "+v"(l.quad));
+        return l;
+    }
 };
 
-// The first product of a block of 16 MT rows: v = m w^T.  A wave takes every eighth run of 128 bytes
-// of the rows, two chunks a lane, so that a row's cache line is read by one wave at once.
-template <typename TX, int MT, bool EVEN>
-struct Rows {
+// The first product of a block's rows: v = m w^T.  A wave takes every eighth run of 128 bytes of the
+// rows, two chunks a lane, so that a row's cache line is read by one wave at once, 64 bytes of a row in
+// an instruction.  NT: tiles of 16 ranks at a time.
+template <typename TX, typename TW, int NT>
+struct Shrink {
     typedef Mma<TX> M;
     static constexpr int C = M::kChunk, kRun = 8 * C;
-    const TX *row[MT];   // the lane's rows, from the lane's first chunk on
+    static constexpr int U = NT == 1 ? 4 : NT == 2 ? 2 : 1;   // runs in flight
+    Buffer m, w;
+    unsigned row;   // the lane's row in m, bytes
     int cols;
 
     // part[wave][row][q] = the wave's share of sum_k m[row, k] w[q0 + q, k].  `then` is called once,
     // behind the first loads: what it requests arrives while these are multiplied and joined.
-    template <typename TW, int NT, typename F>
-    __device__ __forceinline__ void shrink(const Lane &l, const TW *w, int q0, int r, float *part, F then) const {
-        const int full = cols / kRun;
-        f32x4 acc[NT][MT] = {};
-        unsigned wr[NT];   // r * cols is under 2^30
+    template <typename F>
+    __device__ __forceinline__ void run(const Lane &lane, int q0, int r, float *part, F then) const {
+        const Lane l = lane.again();
+        f32x4 acc[NT] = {};
+        unsigned wr[NT];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) wr[i] = (unsigned)min(q0 + 16 * i + l.l16, r - 1) * cols + 2 * l.quad * C;
-        auto run = [&](int d, auto count, auto whole, auto first) __attribute__((always_inline)) {
-            constexpr int N = decltype(count)::value;
-            typename M::Frag x[N][MT][2], a[N][NT][2];
+        for (int i = 0; i < NT; ++i) {
+            const int q = q0 + 16 * i + l.l16;
+            wr[i] = q < r ? (unsigned)q * cols : kNowhere / sizeof(TW);
+        }
+        const int runs = (cols + kRun - 1) / kRun;
+        auto batch = [&](int d, auto first) __attribute__((always_inline)) {
+            Chunk<TX, TX> x[U][2];
+            Chunk<TX, TW> a[U][NT][2];
 #pragma unroll
-            for (int u = 0; u < N; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const int k = (d + u * kTileWaves) * kRun + s * C;
-                    const int n = decltype(whole)::value ? C : cols - k - 2 * l.quad * C;
+                    const int k = (d + u * kTileWaves) * kRun + 4 * s * C + l.quad * C;
+                    const bool in = k < cols;
+                    x[u][s].load(m, in ? row + k * (unsigned)sizeof(TX) : kNowhere);
 #pragma unroll
-                    for (int j = 0; j < MT; ++j) x[u][j][s] = load_chunk<TX, EVEN || decltype(whole)::value>(row[j] + k, n);
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) a[u][i][s] = load_chunk<TX, EVEN || decltype(whole)::value>(w + k + wr[i], n);
+                    for (int i = 0; i < NT; ++i) a[u][i][s].load(w, in ? (wr[i] + k) * (unsigned)sizeof(TW) : kNowhere);
                 }
             if constexpr (decltype(first)::value) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -189,44 +221,29 @@ struct Rows {
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int u = 0; u < N; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int j = 0; j < MT; ++j) acc[i][j] = M::mul(a[u][i][s], x[u][j][s], acc[i][j]);
+                    for (int i = 0; i < NT; ++i) acc[i] = M::mul(a[u][i][s].frag(), x[u][s].frag(), acc[i]);
         };
-        constexpr int U = NT == 1 ? 4 / MT : NT == 2 ? 2 : 1;
-        int d = l.wave;
-        if (d + (U - 1) * kTileWaves < full) {
-            run(d, std::integral_constant<int, U>{}, std::true_type{}, std::true_type{});
-            for (d += U * kTileWaves; d + (U - 1) * kTileWaves < full; d += U * kTileWaves)
-                run(d, std::integral_constant<int, U>{}, std::true_type{}, std::false_type{});
-        } else {
-            then();
-        }
-        for (; d < full; d += kTileWaves) run(d, std::integral_constant<int, 1>{}, std::true_type{}, std::false_type{});
-        if (full * kRun < cols && full % kTileWaves == l.wave)
-            run(full, std::integral_constant<int, 1>{}, std::false_type{}, std::false_type{});
+        batch(l.wave, std::true_type{});
+        for (int d = U * kTileWaves; d < runs; d += U * kTileWaves) batch(d + l.wave, std::false_type{});
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j)
-                *reinterpret_cast<f32x4 *>(part + ((l.wave * MT + j) * 16 + l.l16) * (16 * NT) + 16 * i + 4 * l.quad) =
-                    acc[i][j];
+            *reinterpret_cast<f32x4 *>(part + (l.wave * 16 + l.l16) * (16 * NT) + 16 * i + 4 * l.quad) = acc[i];
     }
 };
 
 // v[row][q0 + q] = scale * (sum of the waves' parts), zeros from rank r up to the next multiple of 32.
-template <int NT, int MT, int RP>
-__device__ inline void join_parts(const float *part, float *v, int q0, int r, float scale) {
+template <int NT, int RP>
+__device__ __forceinline__ void join_parts(const float *part, float *v, int q0, int r, float scale) {
     if (NT == 1)
-        for (int i = threadIdx.x; i < 16 * MT * 16; i += kTileThreads) v[i / 16 * RP + 16 + i % 16] = 0.f;
-    for (int i = threadIdx.x; i < 16 * MT * 16 * NT; i += kTileThreads) {
+        for (int i = threadIdx.x; i < 256; i += kTileThreads) v[i / 16 * RP + 16 + i % 16] = 0.f;
+    for (int i = threadIdx.x; i < 256 * NT; i += kTileThreads) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kTileWaves; ++w) s += part[w * 16 * MT * 16 * NT + i];
+        for (int w = 0; w < kTileWaves; ++w) s += part[w * 256 * NT + i];
         const int row = i / (16 * NT), q = q0 + i % (16 * NT);
         v[row * RP + q] = q < r ? s * scale : 0.f;
     }
@@ -239,7 +256,7 @@ struct Left {
     typename Mma<TX>::Frag hi, lo;
 };
 template <typename TX>
-__device__ inline Left<TX> left_of(const float *v, int exponent) {
+__device__ __forceinline__ Left<TX> left_of(const float *v, int exponent) {
     Left<TX> f;
     if constexpr (sizeof(TX) == 4) {
         f.hi = *reinterpret_cast<const f32x4 *>(v);
@@ -258,216 +275,221 @@ __device__ inline Left<TX> left_of(const float *v, int exponent) {
 }
 
 // The second product: out[row, c] = base[row, c] + sum_q v[row][q] w[c, q] for the columns c0 .. c1.
-// A wave takes every eighth group of 64 columns; a lane gets 16 consecutive ones of its row.  hold()
-// requests the base of its first kHeld groups ahead of time.
-template <typename TX, int MT, bool EVEN>
-struct Columns {
+// A wave takes every eighth group of 64 columns, a lane 16 of its row's, in pieces of 16 bytes: the
+// four lanes of a row have 64 bytes of it in each piece, which the memory reads and writes faster than
+// 16 bytes here and there.  kTiles: products of 16x16 that make a piece.  kHeld pieces of base are requested
+// ahead (half of it behind the first product's own loads, half behind that product) with the first two
+// groups' weights, the results replace the base in its registers, and all are stored at the end: a load
+// that waits behind a store waits for the store too.
+template <typename TX, typename TW, int kHeld>
+struct Expand {
     typedef Mma<TX> M;
-    static constexpr int C = M::kChunk, kBlock = 4 * C, kPieces = 16 / kVec<TX>, kHeld = 4 / kPieces / MT;
-    const TX *base[MT];
-    TX *out[MT];
-    uint4 held[kHeld][MT][kPieces];
-    int cols, c0, c1;
+    static constexpr int C = M::kChunk, kBlock = 4 * C, V = kVec<TX>, kPieces = 16 / V, kTiles = V / 4;
+    static constexpr int kRing = kHeld / kPieces, kEarly = (kRing + 1) / 2, kStep = kTileWaves * 64;
+    Buffer base, out, w;
+    unsigned base_row, out_row;   // the lane's row, bytes; kNowhere or above: not its turn
+    int c0, c1;                   // c1: at most the columns of w
+    u32x4 held[kRing][kPieces];
+    Chunk<TX, TW> ahead[2][4];
 
-    __device__ __forceinline__ uint4 base_piece(int j, int c) const {
-        const int left = cols - c;
-        if (!base[j] || left <= 0) return uint4{0, 0, 0, 0};
-        return load_piece(base[j] + c, EVEN ? kVec<TX> : left);
+    __device__ __forceinline__ unsigned at(const Lane &l, unsigned row, int g, int p) const {
+        const int c = g + p * 4 * V + l.quad * V;
+        return c < c1 ? row + c * (unsigned)sizeof(TX) : kNowhere;
     }
-    __device__ __forceinline__ void hold(const Lane &l, const bool (&mine)[MT]) {
+    __device__ __forceinline__ void load_base(const Lane &l, int u, int g) {
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-            const int g = c0 + (l.wave + u * kTileWaves) * 64;
-            if (g < c1)
+        for (int p = 0; p < kPieces; ++p) held[u][p] = load16(base, at(l, base_row, g, p));
+    }
+    __device__ __forceinline__ void load_weights(const Lane &l, Chunk<TX, TW> (&a)[4], int r, int g, int b) const {
+        const int q = b * kBlock + l.quad * C;
 #pragma unroll
-                for (int j = 0; j < MT; ++j)
-#pragma unroll
-                    for (int p = 0; p < kPieces; ++p)
-                        held[u][j][p] = mine[j] ? base_piece(j, g + 16 * l.quad + p * kVec<TX>) : uint4{0, 0, 0, 0};
+        for (int t = 0; t < 4; ++t) {
+            const int c = g + t / kTiles * 4 * V + (l.l16 >> 2) * V + 4 * (t % kTiles) + (l.l16 & 3);
+            a[t].load(w, c < c1 && q < r ? ((unsigned)c * r + q) * (unsigned)sizeof(TW) : kNowhere);
         }
+    }
+    __device__ __forceinline__ void early(const Lane &lane) {
+        const Lane l = lane.again();
+#pragma unroll
+        for (int u = 0; u < kEarly; ++u) load_base(l, u, c0 + l.wave * 64 + u * kStep);
+    }
+    __device__ __forceinline__ void late(const Lane &lane, int r, int g, bool all) {
+        const Lane l = lane.again();
+#pragma unroll
+        for (int u = 0; u < 2 && u < kRing; ++u) load_weights(l, ahead[u], r, g + u * kStep, 0);
+        if (all)
+#pragma unroll
+            for (int u = 0; u < kEarly; ++u) load_base(l, u, g + u * kStep);
+#pragma unroll
+        for (int u = kEarly; u < kRing; ++u) load_base(l, u, g + u * kStep);
     }
     // kBlocks: blocks of ranks whose split values stay in registers
-    template <typename TW, int RP, int kBlocks>
-    __device__ __forceinline__ void expand(const Lane &l, const float *v, const TW *w, int r, const bool (&mine)[MT]) const {
+    template <int RP, int kBlocks>
+    __device__ __forceinline__ void run(const Lane &lane, const float *v, int r) {
+        const Lane l = lane.again();
         const int blocks = (r + kBlock - 1) / kBlock;
-        int exponent[MT];
+        const float *mine = v + l.l16 * RP + l.quad * C;
+        int exponent = 0;
+        if constexpr (std::is_same_v<TX, f16>) {
+            float most = 0.f;
+            for (int b = 0; b < blocks; ++b)
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            exponent[j] = 0;
-            if constexpr (std::is_same_v<TX, f16>) {
-                float most = 0.f;
-                for (int b = 0; b < blocks; ++b)
-#pragma unroll
-                    for (int i = 0; i < C; ++i) {
-                        const float a = fabsf(v[(16 * j + l.l16) * RP + b * kBlock + l.quad * C + i]);
-                        most = a < __builtin_inff() ? fmaxf(most, a) : most;
-                    }
-                most = fmaxf(most, __shfl_xor(most, 16));
-                most = fmaxf(most, __shfl_xor(most, 32));
-                if (most > 0.f) frexpf(most, &exponent[j]);
-            }
+                for (int i = 0; i < C; ++i) {
+                    const float a = fabsf(mine[b * kBlock + i]);
+                    most = a < __builtin_inff() ? fmaxf(most, a) : most;
+                }
+            most = fmaxf(most, __shfl_xor(most, 16));
+            most = fmaxf(most, __shfl_xor(most, 32));
+            if (most > 0.f) frexpf(most, &exponent);
         }
-        Left<TX> left[kBlocks][MT];
+        Left<TX> left[kBlocks];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-            if (b < blocks)
+        for (int b = 0; b < kBlocks; ++b) left[b] = left_of<TX>(mine + b * kBlock, exponent);
+        for (int g0 = c0 + l.wave * 64; g0 < c1; g0 += kRing * kStep) {
+            if (g0 != c0 + l.wave * 64) late(l, r, g0, true);
 #pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    left[b][j] = left_of<TX>(v + (16 * j + l.l16) * RP + b * kBlock + l.quad * C, exponent[j]);
-
-        auto group = [&](int g, const uint4 (&from)[MT][kPieces]) __attribute__((always_inline)) {
-            f32x4 acc[4][MT] = {};
-            auto block = [&](int b, const Left<TX> (&f)[MT]) __attribute__((always_inline)) {
-                typename M::Frag a[4] = {};
-                const int q = b * kBlock + l.quad * C;
-                if (q < r)
+            for (int u = 0; u < kRing; ++u) {
+                const int g = g0 + u * kStep;
+                f32x4 acc[4] = {};
+                auto multiply = [&](const Chunk<TX, TW> (&a)[4], const Left<TX> &f) __attribute__((always_inline)) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const int c = min(g + 16 * (l.l16 >> 2) + 4 * t + (l.l16 & 3), cols - 1);
-                        a[t] = load_chunk<TX, EVEN>(w + ((unsigned)c * r + q), r - q);
+                        if constexpr (sizeof(TX) == 2) acc[t] = M::mul(a[t].frag(), f.lo, acc[t]);
+                        acc[t] = M::mul(a[t].frag(), f.hi, acc[t]);
                     }
+                };
+                multiply(ahead[u & 1], left[0]);
+                if (u + 2 < kRing) load_weights(lane.again(), ahead[u & 1], r, g + 2 * kStep, 0);
+                if constexpr (kBlocks > 1) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int j = 0; j < MT; ++j) {
-                        if constexpr (sizeof(TX) == 2) acc[t][j] = M::mul(a[t], f[j].lo, acc[t][j]);
-                        acc[t][j] = M::mul(a[t], f[j].hi, acc[t][j]);
+                    for (int b = 1; b < kBlocks; ++b)
+                        if (b < blocks) {
+                            Chunk<TX, TW> a[4];
+                            load_weights(l, a, r, g, b);
+                            multiply(a, left[b]);
+                        }
+                    for (int b = kBlocks; b < blocks; ++b) {
+                        Chunk<TX, TW> a[4];
+                        load_weights(l, a, r, g, b);
+                        multiply(a, left_of<TX>(mine + b * kBlock, exponent));
                     }
-            };
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-                if (b < blocks) block(b, left[b]);
-            for (int b = kBlocks; b < blocks; ++b) {
-                Left<TX> f[MT];
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    f[j] = left_of<TX>(v + (16 * j + l.l16) * RP + b * kBlock + l.quad * C, exponent[j]);
-                block(b, f);
-            }
-            const int c = g + 16 * l.quad;
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                if (!mine[j]) continue;
+                }
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
-                    const int left_cols = cols - (c + p * kVec<TX>);
-                    if (left_cols <= 0) continue;
-                    float sum[kVec<TX>];
-                    unpack<TX>(from[j][p], sum);
+                    float sum[V];
+                    unpack<TX>(__builtin_bit_cast(uint4, held[u][p]), sum);
 #pragma unroll
-                    for (int i = 0; i < kVec<TX>; ++i) {
-                        const int at = p * kVec<TX> + i;
-                        float s = acc[at / 4][j][at % 4];
-                        if constexpr (std::is_same_v<TX, f16>) s = ldexpf(s, exponent[j]);
+                    for (int i = 0; i < V; ++i) {
+                        float s = acc[(p * V + i) / 4][i % 4];
+                        if constexpr (std::is_same_v<TX, f16>) s = ldexpf(s, exponent);
                         sum[i] += s;
                     }
-                    store_piece(out[j] + c + p * kVec<TX>, pack<TX>(sum), EVEN ? kVec<TX> : left_cols);
+                    held[u][p] = __builtin_bit_cast(u32x4, pack<TX>(sum));
                 }
+                __builtin_amdgcn_sched_barrier(0);   // one group's products at a time: registers
             }
-        };
+            const Lane o = lane.again();
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-            const int g = c0 + (l.wave + u * kTileWaves) * 64;
-            if (g < c1) group(g, held[u]);
-        }
-        for (int g = c0 + (l.wave + kHeld * kTileWaves) * 64; g < c1; g += kTileWaves * 64) {
-            uint4 from[MT][kPieces];
+            for (int u = 0; u < kRing; ++u)
 #pragma unroll
-            for (int j = 0; j < MT; ++j)
-#pragma unroll
-                for (int p = 0; p < kPieces; ++p) from[j][p] = base_piece(j, g + 16 * l.quad + p * kVec<TX>);
-            group(g, from);
+                for (int p = 0; p < kPieces; ++p) store16(out, at(o, out_row, g0 + u * kStep, p), held[u][p]);
         }
     }
-    // Keeps the compiler from computing every address of a turn ahead of the loop over a block's adapters
-    // (it spilled registers for them): what they start from becomes unknown here.
-    __device__ __forceinline__ void renew(Lane &l, int &r) {
-        asm volatile("" : "+s"(r), "+s"(cols), "+s"(c0), "+v"(l.l16), "+v"(l.quad));
-    }
-    // base (or zeros) to out for the rows without an adapter
-    __device__ __forceinline__ void pass(const Lane &l, const bool (&none)[MT]) const {
-        for (int g = c0 + l.wave * 64; g < c1; g += kTileWaves * 64)
+    // base (or zeros) to out
+    __device__ __forceinline__ void pass(const Lane &l) const {
+        for (int g = c0 + l.wave * 64; g < c1; g += kStep)
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                if (!none[j] || base[j] == out[j]) continue;
-#pragma unroll
-                for (int p = 0; p < kPieces; ++p) {
-                    const int c = g + 16 * l.quad + p * kVec<TX>;
-                    if (c < cols) store_piece(out[j] + c, base_piece(j, c), EVEN ? kVec<TX> : cols - c);
-                }
-            }
+            for (int p = 0; p < kPieces; ++p) store16(out, at(l, out_row, g, p), load16(base, at(l, base_row, g, p)));
     }
 };
 
 // The smallest adapter number left among a block's rows (e < 0: done or none), the same in every
 // lane of every wave; -1 if there is none.
-template <int MT>
-__device__ inline int next_adapter(const int (&e)[MT]) {
-    unsigned now = ~0u;
-#pragma unroll
-    for (int j = 0; j < MT; ++j) now = min(now, (unsigned)e[j]);   // a negative number is a large one
+__device__ __forceinline__ int next_adapter(int e) {
+    unsigned now = (unsigned)e;   // a negative number is a large one
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) now = min(now, (unsigned)__shfl_xor((int)now, d));
     return max(__builtin_amdgcn_readfirstlane((int)now), -1);
 }
 
-// 16 MT rows a workgroup, for each adapter among them: v = x A^T with the reduction split over the
+// Rows row0 .. row0 + 15 of a matrix, as a buffer.
+template <typename T>
+__device__ __forceinline__ Buffer rows_of(const void *p, int64_t ld, int row0, int rows, int cols) {
+    return buffer(p ? static_cast<const T *>(p) + row0 * ld : nullptr,
+                  ((size_t)(min(rows - row0, kTileRows) - 1) * ld + cols) * sizeof(T));
+}
+
+// 16 rows a workgroup, for each adapter among them: v = x A^T with the reduction split over the
 // waves and joined in LDS, then out = base + v B^T, the columns split over the waves.  Bound by
 // memory: x and base are read and out written once, the adapters' matrices come from L2.  Several
-// workgroups may share a block of rows (blockIdx.y), each for its own columns, with v computed by each.
-// NT: tiles of 16 ranks a pass; RM: ranks that v has room for.
-// EVEN: inner, outer and the rank are multiples of a lane's chunk.
-template <typename TX, typename TW, int NT, int RM, int MT, bool EVEN>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(EVEN ? 4 : 2))) void k_adapters_tile(AdapterArgs g,
-                                                                                                   int slice_cols) {
+// workgroups may share a block of rows, each for its own slice of the columns, with v computed by each;
+// and a block's adapters are dealt to `turns` workgroups, the first adapter's behind all others, so that
+// a block with several of them does not end a whole turn after the rest (a workgroup without an adapter
+// ends when it has seen the numbers).
+// Workgroups go to the 8 XCDs in turn by index: a block's workgroups have one index modulo 8, and follow
+// each other there, so that they share its rows in that XCD's cache.
+// RM: ranks that v has room for.
+template <typename TX, typename TW, int NT, int RM>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4))) void k_adapters_tile(
+    AdapterArgs g, int slice_cols, int slices, int turns) {
     constexpr int RP = RM + 4;
-    __shared__ __align__(16) float part[kTileWaves * 16 * MT * 16 * NT];
-    __shared__ __align__(16) float v[16 * MT * RP];
+    __shared__ __align__(16) float part[kTileWaves * 256 * NT];
+    __shared__ __align__(16) float v[16 * RP];
+    const int of = blockIdx.x >> 3, block = of / slices * 8 + (blockIdx.x & 7), turn = turns - 1 - blockIdx.y;
+    const int row0 = block * kTileRows;
+    if (row0 >= g.T) return;
     Lane l;
-    Rows<TX, MT, EVEN> x;
-    Columns<TX, MT, EVEN> y;
+    const int row = row0 + l.l16;
+    const int id = g.adapter[min(row, g.T - 1)];
+    const bool valid = (unsigned)id < (unsigned)g.n;
+    const bool none = row < g.T && !valid;
+    int e = row < g.T && valid ? id : -1;
+    Shrink<TX, TW, NT> x;
+    Expand<TX, TW, NT == 4 && sizeof(TX) == 2 ? 2 : 4> y;
+    x.m = rows_of<TX>(g.x, g.ld_x, row0, g.T, g.inner);
+    x.row = l.l16 * (unsigned)g.ld_x * sizeof(TX);
     x.cols = g.inner;
-    y.cols = g.outer;
-    y.c0 = blockIdx.y * slice_cols;
+    y.base = rows_of<TX>(g.base, g.ld_base, row0, g.T, g.outer);
+    y.out = rows_of<TX>(g.out, g.ld_out, row0, g.T, g.outer);
+    y.c0 = of % slices * slice_cols;
     y.c1 = min(g.outer, y.c0 + slice_cols);
-    int e[MT];
-    bool none[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const int row = (blockIdx.x * MT + j) * 16 + l.l16, at = min(row, g.T - 1);
-        x.row[j] = static_cast<const TX *>(g.x) + at * g.ld_x + 2 * l.quad * Mma<TX>::kChunk;
-        y.base[j] = g.base ? static_cast<const TX *>(g.base) + at * g.ld_base : nullptr;
-        y.out[j] = static_cast<TX *>(g.out) + at * g.ld_out;
-        const int id = g.adapter[at];
-        const bool valid = (unsigned)id < (unsigned)g.n;
-        none[j] = row < g.T && !valid;
-        e[j] = row < g.T && valid ? id : -1;
-    }
+    const unsigned base_row = l.l16 * (unsigned)g.ld_base * sizeof(TX), out_row = l.l16 * (unsigned)g.ld_out * sizeof(TX);
+    int seen = 0;
     for (int now = next_adapter(e); now >= 0; now = next_adapter(e)) {
+        const bool mine = e == now;
+        if (mine) e = -1;
+        if (seen++ % turns != turn) continue;
         int r = g.r;
-        y.renew(l, r);
-        const TW *a = static_cast<const TW *>(g.a) + (size_t)now * r * g.inner;
-        const TW *b = static_cast<const TW *>(g.b) + (size_t)now * r * g.outer;
+        asm volatile("" : "+s"(r));
+        const size_t of_a = (size_t)now * r * g.inner, of_b = (size_t)now * r * g.outer;
+        x.w = buffer(static_cast<const TW *>(g.a) + of_a, (size_t)r * g.inner * sizeof(TW));
+        y.w = buffer(static_cast<const TW *>(g.b) + of_b, (size_t)r * g.outer * sizeof(TW));
+        y.base_row = mine ? base_row : kNowhere;
+        y.out_row = mine ? out_row : kNowhere;
         const float scale = g.scale[now];
-        bool mine[MT];
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            mine[j] = e[j] == now;
-            if (mine[j]) e[j] = -1;
-        }
-        x.template shrink<TW, NT>(l, a, 0, r, part, [&]() __attribute__((always_inline)) { y.hold(l, mine); });
+        const int g0 = y.c0 + l.wave * 64;
+        x.run(l, 0, r, part, [&]() __attribute__((always_inline)) { y.early(l); });
+        __builtin_amdgcn_sched_barrier(0);
+        if (RM <= 16 * NT || NT == 1) y.late(l, r, g0, false);
         __syncthreads();
-        join_parts<NT, MT, RP>(part, v, 0, r, scale);
-        for (int q0 = 16 * NT; q0 < r; q0 += 16 * NT) {
-            __syncthreads();
-            x.template shrink<TW, NT>(l, a, q0, r, part, [] {});
-            __syncthreads();
-            join_parts<NT, MT, RP>(part, v, q0, r, scale);
+        join_parts<NT, RP>(part, v, 0, r, scale);
+        if constexpr (RM > 64) {
+            for (int q0 = 16 * NT; q0 < r; q0 += 16 * NT) {
+                __syncthreads();
+                x.run(l, q0, r, part, []() __attribute__((always_inline)) {});
+                __syncthreads();
+                join_parts<NT, RP>(part, v, q0, r, scale);
+            }
+            y.late(l, r, g0, false);
         }
         __syncthreads();
-        y.template expand<TW, RP, (RM >= 64 ? 64 : 32) / (4 * Mma<TX>::kChunk)>(l, v, b, r, mine);
+        y.template run<RP, (RM >= 64 ? 64 : 32) / (4 * Mma<TX>::kChunk)>(l, v, r);
     }
-    y.pass(l, none);
+    if (turn == 0 && __ballot(none) && !(g.base == g.out && g.ld_base == g.ld_out)) {
+        y.base_row = none ? base_row : kNowhere;
+        y.out_row = none ? out_row : kNowhere;
+        y.pass(l);
+    }
 }
 
 // v and u of a row to memory, and its d_x.
@@ -560,28 +582,38 @@ BackSpace back_space(int T, int n, int r) {
     return s;
 }
 
-template <typename TX, typename TW, int NT, int RM, bool EVEN>
+template <typename TX, typename TW, int NT, int RM>
 hipError_t forward_tile(const AdapterArgs &g, hipStream_t stream) {
-    constexpr int MT = 1;
-    const int tiles = (g.T + 16 * MT - 1) / (16 * MT);
+    const int tiles = (g.T + kTileRows - 1) / kTileRows;
     const int groups = (g.outer + 63) / 64;
     const int slices = std::max(1, std::min(groups / kTileWaves, 512 / tiles));
-    const int cols = (groups + slices - 1) / slices * 64;
-    return launch(k_adapters_tile<TX, TW, NT, RM, MT, EVEN>, dim3(tiles, (g.outer + cols - 1) / cols), dim3(kTileThreads), stream,
-                  nullptr, nullptr, g, cols);
+    const int cols = (groups + slices - 1) / slices * 64, used = (g.outer + cols - 1) / cols;
+    const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / (tiles * slices))));
+    return launch(k_adapters_tile<TX, TW, NT, RM>, dim3((tiles + 7) / 8 * 8 * used, turns), dim3(kTileThreads), stream,
+                  nullptr, nullptr, g, cols, used, turns);
+}
+
+// Whether a matrix can be read by the block kernels: rows of whole, aligned 16-byte pieces, sixteen of
+// them within a buffer.
+bool piecewise(const void *p, int64_t ld, int cols, size_t size) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && cols * size % 16 == 0 &&
+           (15 * ld + cols) * (int64_t)size < kBufferBytes;
+}
+bool piecewise_adapters(const void *a, const void *b, int inner, int outer, int r, int chunk, size_t size) {
+    return (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) % (chunk * size) == 0 && r % chunk == 0 &&
+           inner % chunk == 0 && outer % chunk == 0 && (int64_t)r * std::max(inner, outer) * (int64_t)size < kBufferBytes;
 }
 
 template <typename TX, typename TW>
 hipError_t forward(const AdapterArgs &g, hipStream_t stream) {
-    if (g.T > kRowCalls && (int64_t)g.r * std::max(g.inner, g.outer) < kTileElements) {
-        constexpr int C = Mma<TX>::kChunk;
-        if (g.inner % C || g.outer % kVec<TX> || g.r % C)
-            return g.r <= 64 ? forward_tile<TX, TW, 4, 64, false>(g, stream)
-                             : forward_tile<TX, TW, 4, kMaxRank, false>(g, stream);
-        if (g.r <= 16) return forward_tile<TX, TW, 1, 32, true>(g, stream);
-        if (g.r <= 32) return forward_tile<TX, TW, 2, 32, true>(g, stream);
-        if (g.r <= 64) return forward_tile<TX, TW, 4, 64, true>(g, stream);
-        return forward_tile<TX, TW, 4, kMaxRank, true>(g, stream);
+    constexpr size_t z = sizeof(TX);
+    if (g.T > kRowCalls && piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.out, g.ld_out, g.outer, z) &&
+        (!g.base || piecewise(g.base, g.ld_base, g.outer, z)) &&
+        piecewise_adapters(g.a, g.b, g.inner, g.outer, g.r, Mma<TX>::kChunk, sizeof(TW))) {
+        if (g.r <= 16) return forward_tile<TX, TW, 1, 32>(g, stream);
+        if (g.r <= 32) return forward_tile<TX, TW, 2, 32>(g, stream);
+        if (g.r <= 64) return forward_tile<TX, TW, 4, 64>(g, stream);
+        return forward_tile<TX, TW, 4, kMaxRank>(g, stream);
     }
     return launch(k_adapters_row<TX, TW>, dim3(g.T), dim3(kThreads), stream, nullptr, nullptr, g);
 }
