@@ -566,19 +566,398 @@ __global__ __launch_bounds__(kThreads) void k_back_weights(AdapterBackArgs g, co
     }
 }
 
-// Workspace of a backward call.
-struct BackSpace {
-    size_t offsets, order, sort, v, u, bytes;
+// ------------------------------------------------------------------ gradients, blocks of rows
+//
+// d_x is the forward's two products with the matrices transposed, so a call first lays them out that
+// way (ranks padded to a multiple of 8); v and u go to memory on the way, and the weights' gradients
+// are products over the rows of one adapter at a time, in the order of a counting sort.
+
+// at[e][c][q] = a[e][q][c], bt[e][q][o] = b[e][o][q], zeros in the padding; and where inner is padded,
+// ap[e][q][c] = a[e][q][c].  32 ranks by 64 columns a workgroup.
+template <typename TW>
+__global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW *b, TW *at, TW *bt, TW *ap, int inner,
+                                                          int outer, int ip, int op, int r, int rp) {
+    __shared__ TW tile[32][65];
+    const int tiles_a = (ip + 63) / 64, e = blockIdx.z, q0 = blockIdx.y * 32;
+    const bool is_b = (int)blockIdx.x >= tiles_a;
+    const int c0 = (is_b ? blockIdx.x - tiles_a : blockIdx.x) * 64;
+    const int cols = is_b ? outer : inner, padded = is_b ? op : ip;
+    const size_t ea = (size_t)e * r * inner, eb = (size_t)e * r * outer;
+    for (int i = threadIdx.x; i < 32 * 64; i += kThreads) {
+        const int q = is_b ? i % 32 : i / 64, c = is_b ? i / 32 : i % 64;
+        TW v = narrow<TW>(0.f);
+        if (q0 + q < r && c0 + c < cols)
+            v = is_b ? b[eb + (size_t)(c0 + c) * r + q0 + q] : a[ea + (size_t)(q0 + q) * inner + c0 + c];
+        tile[q][c] = v;
+        if (!is_b && ap && q0 + q < r && c0 + c < padded) ap[((size_t)e * r + q0 + q) * ip + c0 + c] = v;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * 64; i += kThreads) {
+        const int q = is_b ? i / 64 : i % 32, c = is_b ? i % 64 : i / 32;
+        if (q0 + q >= rp || c0 + c >= padded) continue;
+        if (is_b)
+            bt[((size_t)e * rp + q0 + q) * op + c0 + c] = tile[q][c];
+        else
+            at[((size_t)e * ip + c0 + c) * rp + q0 + q] = tile[q][c];
+    }
+}
+
+// Up to three matrices copied row by row to another row distance and width: zeros behind the narrower
+// source (and for a missing one).
+struct Reshape {
+    const void *from[3];
+    void *to[3];
+    int64_t ld_from[3], ld_to[3];
+    int cols_from[3], cols_to[3];
 };
-BackSpace back_space(int T, int n, int r) {
-    auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+template <typename TX>
+__global__ __launch_bounds__(kThreads) void k_back_reshape(Reshape g, int rows) {
+    const int m = blockIdx.y;
+    for (int row = blockIdx.x * 4 + ((int)threadIdx.x >> 6); row < rows; row += gridDim.x * 4) {
+        const TX *from = static_cast<const TX *>(g.from[m]) + row * g.ld_from[m];
+        TX *to = static_cast<TX *>(g.to[m]) + row * g.ld_to[m];
+        for (int c = (threadIdx.x & 63) * kVec<TX>; c < g.cols_to[m]; c += 64 * kVec<TX>) {
+            const uint4 v = g.from[m] && c < g.cols_from[m] ? load_piece(from + c, g.cols_from[m] - c) : uint4{0, 0, 0, 0};
+            store_piece(to + c, v, g.cols_to[m] - c);
+        }
+    }
+}
+
+// What the block kernels of a backward call read and write: as AdapterBackArgs, or padded copies.
+struct BackBlocks {
+    const void *x, *d_out, *dx_base;
+    void *d_x;
+    int64_t ld_x, ld_d_out, ld_dx_base, ld_d_x;
+    const void *a, *at, *bt;          // [n x r x ip], [n x ip x rp], [n x rp x op]
+    const int32_t *adapter;
+    const float *scale;
+    float *v, *u;                     // [T x r]: scale * (A x), scale * (B^T d_out)
+    int T, ip, op, n, r, rp;
+};
+
+// d_x = dx_base + u A of 16 rows a workgroup, and v and u; built as k_adapters_tile.
+template <typename TX, typename TW, int NT, int RM>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4))) void k_back_tile(
+    BackBlocks g, int slice_cols, int slices, int turns) {
+    constexpr int RP = RM + 4;
+    __shared__ __align__(16) float part[kTileWaves * 256 * NT];
+    __shared__ __align__(16) float v[16 * RP], u[16 * RP];
+    const int of = blockIdx.x >> 3, block = of / slices * 8 + (blockIdx.x & 7), turn = turns - 1 - blockIdx.y;
+    const int row0 = block * kTileRows, slice = of % slices;
+    if (row0 >= g.T) return;
+    Lane l;
+    const int row = row0 + l.l16;
+    const int id = g.adapter[min(row, g.T - 1)];
+    const bool valid = (unsigned)id < (unsigned)g.n;
+    const bool none = row < g.T && !valid;
+    int e = row < g.T && valid ? id : -1;
+    Shrink<TX, TW, NT> x, dy;
+    Expand<TX, TW, sizeof(TX) == 2 && (NT > 1 || std::is_same_v<TX, f16>) ? 2 : 4> y;
+    x.m = rows_of<TX>(g.x, g.ld_x, row0, g.T, g.ip);
+    x.row = l.l16 * (unsigned)g.ld_x * sizeof(TX);
+    x.cols = g.ip;
+    dy.m = rows_of<TX>(g.d_out, g.ld_d_out, row0, g.T, g.op);
+    dy.row = l.l16 * (unsigned)g.ld_d_out * sizeof(TX);
+    dy.cols = g.op;
+    y.base = rows_of<TX>(g.dx_base, g.ld_dx_base, row0, g.T, g.ip);
+    y.out = rows_of<TX>(g.d_x, g.ld_d_x, row0, g.T, g.ip);
+    y.c0 = slice * slice_cols;
+    y.c1 = min(g.ip, y.c0 + slice_cols);
+    const unsigned base_row = l.l16 * (unsigned)g.ld_dx_base * sizeof(TX), out_row = l.l16 * (unsigned)g.ld_d_x * sizeof(TX);
+    int seen = 0;
+    for (int now = next_adapter(e); now >= 0; now = next_adapter(e)) {
+        const bool mine = e == now;
+        if (mine) e = -1;
+        if (seen++ % turns != turn) continue;
+        const unsigned rows = (unsigned)__ballot(mine) & 0xFFFFu;
+        int r = g.r;
+        asm volatile("" : "+s"(r));
+        x.w = buffer(static_cast<const TW *>(g.a) + (size_t)now * r * g.ip, (size_t)r * g.ip * sizeof(TW));
+        dy.w = buffer(static_cast<const TW *>(g.bt) + (size_t)now * g.rp * g.op, (size_t)g.rp * g.op * sizeof(TW));
+        y.w = buffer(static_cast<const TW *>(g.at) + (size_t)now * g.rp * g.ip, (size_t)g.rp * g.ip * sizeof(TW));
+        y.base_row = mine ? base_row : kNowhere;
+        y.out_row = mine ? out_row : kNowhere;
+        const float scale = g.scale[now];
+        const int g0 = y.c0 + l.wave * 64;
+        if (slice == 0)
+            for (int q0 = 0; q0 < r; q0 += 16 * NT) {
+                x.run(l, q0, r, part, []() __attribute__((always_inline)) {});
+                __syncthreads();
+                join_parts<NT, RP>(part, v, q0, r, scale);
+                __syncthreads();
+            }
+        for (int q0 = 0; q0 < r; q0 += 16 * NT) {
+            if (q0) __syncthreads();
+            dy.run(l, q0, r, part, []() __attribute__((always_inline)) {});
+            __syncthreads();
+            join_parts<NT, RP>(part, u, q0, r, scale);
+        }
+        y.early(l);
+        y.late(l, g.rp, g0, false);
+        __syncthreads();
+        if (slice == 0)
+            for (int i = threadIdx.x; i < 16 * r; i += kTileThreads) {
+                const int k = i / r, q = i - k * r;
+                if ((rows >> k) & 1) {
+                    g.v[(size_t)(row0 + k) * r + q] = v[k * RP + q];
+                    g.u[(size_t)(row0 + k) * r + q] = u[k * RP + q];
+                }
+            }
+        y.template run<RP, (RM >= 64 ? 64 : 32) / (4 * Mma<TX>::kChunk)>(l, u, g.rp);
+        __syncthreads();
+    }
+    if (turn == 0 && __ballot(none) && !(g.dx_base == g.d_x && g.ld_dx_base == g.ld_d_x)) {
+        y.base_row = none ? base_row : kNowhere;
+        y.out_row = none ? out_row : kNowhere;
+        y.pass(l);
+    }
+}
+
+// An adapter's rows, in their sorted order, are cut into pieces of `rows`; pieces are numbered through.
+struct Piece {
+    int e, first, begin, end, count;   // adapter, its first piece, the piece's rows, its pieces
+};
+constexpr int kPieceCols = 128;
+
+// Piece p, found by every workgroup from the offsets (four adapters a thread); e < 0: there is none.
+__device__ inline Piece find_piece(const int32_t *offsets, int n, int rows, int p) {
+    __shared__ int wave_sum[kThreads / 64];
+    __shared__ Piece found;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (threadIdx.x == 0) found.e = -1;
+    int count[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * threadIdx.x + i;
+        count[i] = e < n ? (offsets[e + 1] - offsets[e] + rows - 1) / rows : 0;
+        mine += count[i];
+    }
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 63) wave_sum[wave] = upto;
+    __syncthreads();
+    int start = upto - mine;
+    for (int w = 0; w < wave; ++w) start += wave_sum[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (p >= start && p < start + count[i]) {
+            const int e = 4 * threadIdx.x + i;
+            found.e = e;
+            found.first = start;
+            found.begin = offsets[e] + (p - start) * rows;
+            found.end = min(offsets[e + 1], found.begin + rows);
+            found.count = count[i];
+        }
+        start += count[i];
+    }
+    __syncthreads();
+    return found;
+}
+
+struct BackWeights {
+    const void *x, *d_out;
+    int64_t ld_x, ld_d_out;
+    const int32_t *offsets, *order;
+    const float *v, *u;
+    float *partial;      // [piece][r][ip + op]
+    float *d_a, *d_b;
+    int inner, outer, ip, op, n, r, piece_rows;
+};
+
+__device__ __forceinline__ void store_grad(const BackWeights &g, int e, bool is_b, int q, int c, float s) {
+    if (is_b)
+        g.d_b[((size_t)e * g.outer + c) * g.r + q] = s;
+    else
+        g.d_a[((size_t)e * g.r + q) * g.inner + c] = s;
+}
+
+// d_a and d_b of one piece: 128 columns and 16 NT ranks a workgroup, 32 rows a wave at a time.
+// left[q][col] = sum over rows of (u or v)[row][q] (x or d_out)[row][col], the rows being the reduction:
+// a lane loads 16 bytes of 8 rows, and for bf16 turns them into the eight columns' operands, pairs of
+// rows a dword (v_perm), with u and v in two parts of 16 bits together; other types multiply in fp32,
+// whose operand is one element.
+template <typename TX, int NT>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NT == 4 && sizeof(TX) == 4 ? 1 : 2))) void k_back_pieces(BackWeights g) {
+    constexpr bool kPairs = std::is_same_v<TX, bf16>;
+    constexpr int kLoads = sizeof(TX) == 4 ? 2 : 1;   // of 16 bytes for a lane's 8 columns of a row
+    __shared__ __align__(16) f32x4 part[kThreads / 64][8][64];
+    const Piece p = find_piece(g.offsets, g.n, g.piece_rows, blockIdx.y);
+    if (p.e < 0) return;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4, wave = threadIdx.x >> 6;
+    const int tiles_a = (g.ip + kPieceCols - 1) / kPieceCols;
+    const bool is_b = (int)blockIdx.x >= tiles_a;
+    const int c0 = (is_b ? blockIdx.x - tiles_a : blockIdx.x) * kPieceCols, cols = is_b ? g.op : g.ip;
+    const int q0 = blockIdx.z * 16 * NT;
+    const TX *m = static_cast<const TX *>(is_b ? g.d_out : g.x);
+    const int64_t ld = is_b ? g.ld_d_out : g.ld_x;
+    const float *left = is_b ? g.v : g.u;
+    // the lane's first column of a load; beyond the matrix its last piece (the results are dropped)
+    int at[kLoads], rank[NT];
+#pragma unroll
+    for (int h = 0; h < kLoads; ++h) at[h] = min(c0 + h * 64 + l16 * kVec<TX>, cols - kVec<TX>);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) rank[i] = min(q0 + 16 * i + l16, g.r - 1);
+    f32x4 acc[NT][8] = {};
+    for (int b = p.begin + wave * 32; b < p.end; b += 32 * (kThreads / 64)) {
+        uint4 x[8][kLoads];
+        float f[NT][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // rows 8 quad + j of the 32 (bf16: a lane's chunk of the reduction), or 4 j + quad
+            const int i = b + (kPairs ? 8 * quad + j : 4 * j + quad);
+            const int row = g.order[min(i, p.end - 1)];
+#pragma unroll
+            for (int h = 0; h < kLoads; ++h) x[j][h] = load_piece(m + row * ld + at[h], kVec<TX>);
+#pragma unroll
+            for (int k = 0; k < NT; ++k) f[k][j] = left[(size_t)row * g.r + rank[k]];
+        }
+        if (b + 32 > p.end) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (b + (kPairs ? 8 * quad + j : 4 * j + quad) >= p.end) {
+#pragma unroll
+                    for (int h = 0; h < kLoads; ++h) x[j][h] = uint4{0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < NT; ++k) f[k][j] = 0.f;
+                }
+        }
+        if constexpr (kPairs) {
+            bf16x8 hi[NT], lo[NT];
+#pragma unroll
+            for (int k = 0; k < NT; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    bf16 h, w;
+                    split(f[k][j], h, w);
+                    hi[k][j] = h;
+                    lo[k][j] = w;
+                }
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                u32x4 pairs;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const u32x4 r0 = __builtin_bit_cast(u32x4, x[2 * d][0]), r1 = __builtin_bit_cast(u32x4, x[2 * d + 1][0]);
+                    pairs[d] = __builtin_amdgcn_perm(r1[t / 2], r0[t / 2], t % 2 ? 0x07060302u : 0x05040100u);
+                }
+                const bf16x8 right = __builtin_bit_cast(bf16x8, pairs);
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    acc[k][t] = Mma<bf16>::mul(lo[k], right, acc[k][t]);
+                    acc[k][t] = Mma<bf16>::mul(hi[k], right, acc[k][t]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float w[8];
+#pragma unroll
+                for (int h = 0; h < kLoads; ++h) {
+                    float e[kVec<TX>];
+                    unpack<TX>(x[j][h], e);
+#pragma unroll
+                    for (int i = 0; i < kVec<TX>; ++i) w[h * kVec<TX> + i] = e[i];
+                }
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int k = 0; k < NT; ++k)
+                        acc[k][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[k][j], w[t], acc[k][t], 0, 0, 0);
+            }
+        }
+    }
+    // the waves' sums, joined in order; each wave writes two of the eight column tiles
+    const int real = is_b ? g.outer : g.inner;
+    const size_t width = g.ip + g.op;
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+        if (k) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 8; ++t) part[wave][t][lane] = acc[k][t];
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int t = 2 * wave + s;
+            const int c = c0 + (kLoads == 2 ? 64 * (t / 4) + 4 * l16 + t % 4 : 8 * l16 + t);
+            f32x4 sum = part[0][t][lane];
+#pragma unroll
+            for (int w = 1; w < kThreads / 64; ++w) sum += part[w][t][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int q = q0 + 16 * k + 4 * quad + i;
+                if (q >= g.r || c >= real) continue;
+                if (p.count == 1)
+                    store_grad(g, p.e, is_b, q, c, sum[i]);
+                else
+                    g.partial[((size_t)blockIdx.y * g.r + q) * width + (is_b ? g.ip : 0) + c] = sum[i];
+            }
+        }
+    }
+}
+
+// The sum of an adapter's pieces, in order, or zeros where it has no rows.
+__global__ __launch_bounds__(kThreads) void k_back_join(BackWeights g) {
+    const int e = blockIdx.z, q = blockIdx.y, c0 = blockIdx.x * kThreads + threadIdx.x;
+    // pieces of the adapters before, and of this one
+    __shared__ int sums[kThreads / 64];
+    int before = 0;
+    for (int i = threadIdx.x; i < e; i += kThreads) before += (g.offsets[i + 1] - g.offsets[i] + g.piece_rows - 1) / g.piece_rows;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d);
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = before;
+    __syncthreads();
+    const int first = sums[0] + sums[1] + sums[2] + sums[3];
+    const int count = (g.offsets[e + 1] - g.offsets[e] + g.piece_rows - 1) / g.piece_rows;
+    if (count == 1 || c0 >= g.inner + g.outer) return;
+    const bool is_b = c0 >= g.inner;
+    const int c = is_b ? c0 - g.inner : c0;
+    const size_t width = g.ip + g.op, at = (is_b ? g.ip : 0) + c;
+    float s = 0.f;
+    for (int p = 0; p < count; ++p) s += g.partial[((size_t)(first + p) * g.r + q) * width + at];
+    store_grad(g, e, is_b, q, c, s);
+}
+
+// Sizes of a backward call and where its workspace holds what (element sizes as for fp32: the entry
+// point does not ask for the types).
+struct BackSpace {
+    int ip, op, rp, piece_rows, max_pieces;
+    bool padded;   // rows are copied to whole pieces of 8 elements
+    size_t offsets, order, sort, v, u, at, bt, ap, partial, x, d_out, d_x, bytes;
+};
+BackSpace back_space(int T, int inner, int outer, int n, int r) {
     BackSpace s;
-    s.offsets = 0;
-    s.order = up((size_t)(n + 1) * 4);
-    s.sort = s.order + up((size_t)T * 4);
-    s.v = s.sort + up(dispatch_workspace(T, 1, n));
-    s.u = s.v + up((size_t)T * r * 4);
-    s.bytes = s.u + up((size_t)T * r * 4);
+    s.ip = (inner + 7) / 8 * 8;
+    s.op = (outer + 7) / 8 * 8;
+    s.rp = (r + 7) / 8 * 8;
+    s.padded = s.ip != inner || s.op != outer;
+    // pieces such that their workgroups are about two and a half rounds of the chip's CUs
+    const int64_t tiles = (s.ip + kPieceCols - 1) / kPieceCols + (s.op + kPieceCols - 1) / kPieceCols;
+    s.piece_rows = (int)std::min<int64_t>(1 << 24, std::max<int64_t>(128, (T * tiles / 640 + 127) / 128 * 128));
+    s.max_pieces = T / s.piece_rows + std::min(n, T);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) & ~(size_t)255;
+        return here;
+    };
+    const size_t row = T, adapters = n;
+    s.offsets = take((adapters + 1) * 4);
+    s.order = take(row * 4);
+    s.sort = take(dispatch_workspace(T, 1, n));
+    s.v = take(row * r * 4);
+    s.u = take(row * r * 4);
+    s.at = take(adapters * s.ip * s.rp * 4);
+    s.bt = take(adapters * s.op * s.rp * 4);
+    s.partial = take((size_t)s.max_pieces * r * (s.ip + s.op) * 4);
+    s.ap = take(s.padded ? adapters * r * s.ip * 4 : 0);
+    s.x = take(s.padded ? row * s.ip * 4 : 0);
+    s.d_out = take(s.padded ? row * s.op * 4 : 0);
+    s.d_x = take(s.padded ? row * s.ip * 4 : 0);
+    s.bytes = at;
     return s;
 }
 
@@ -618,9 +997,19 @@ hipError_t forward(const AdapterArgs &g, hipStream_t stream) {
     return launch(k_adapters_row<TX, TW>, dim3(g.T), dim3(kThreads), stream, nullptr, nullptr, g);
 }
 
+template <typename TX, typename TW, int NT, int RM>
+hipError_t back_tile(const BackBlocks &g, hipStream_t stream) {
+    const int tiles = (g.T + kTileRows - 1) / kTileRows, groups = (g.ip + 63) / 64;
+    const int slices = std::max(1, std::min(groups / kTileWaves, 512 / tiles));
+    const int cols = (groups + slices - 1) / slices * 64, used = (g.ip + cols - 1) / cols;
+    const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / (tiles * slices))));
+    return launch(k_back_tile<TX, TW, NT, RM>, dim3((tiles + 7) / 8 * 8 * used, turns), dim3(kTileThreads), stream,
+                  nullptr, nullptr, g, cols, used, turns);
+}
+
 template <typename TX, typename TW>
 hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStream_t stream) {
-    const BackSpace s = back_space(g.T, g.n, g.r);
+    const BackSpace s = back_space(g.T, g.inner, g.outer, g.n, g.r);
     char *ws = static_cast<char *>(workspace);
     int32_t *offsets = reinterpret_cast<int32_t *>(ws + s.offsets), *order = reinterpret_cast<int32_t *>(ws + s.order);
     float *v = reinterpret_cast<float *>(ws + s.v), *u = reinterpret_cast<float *>(ws + s.u);
@@ -633,20 +1022,71 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
     d.k = 1;
     d.E = g.n;
     hipError_t err = launch_dispatch(dtype, d, ws + s.sort, stream);
-    if (err == hipSuccess && g.T > 0)
-        err = launch(k_back_row<TX, TW>, dim3(g.T), dim3(kThreads), stream, nullptr, nullptr, g, v, u);
-    if (err == hipSuccess) {
+    if (err != hipSuccess) return err;
+
+    constexpr size_t z = sizeof(TX);
+    const bool blocks =
+        g.T > 0 && (int64_t)s.rp * std::max(s.ip, s.op) * (int64_t)sizeof(TW) < kBufferBytes &&
+        (15 + 1) * (int64_t)std::max(s.ip, s.op) * (int64_t)z < kBufferBytes &&
+        (s.padded || (piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.d_out, g.ld_d_out, g.outer, z) &&
+                      piecewise(g.d_x, g.ld_d_x, g.inner, z) && reinterpret_cast<uintptr_t>(g.a) % 16 == 0 &&
+                      (!g.dx_base || piecewise(g.dx_base, g.ld_dx_base, g.inner, z))));
+    if (!blocks) {
+        if (g.T > 0) err = launch(k_back_row<TX, TW>, dim3(g.T), dim3(kThreads), stream, nullptr, nullptr, g, v, u);
+        if (err != hipSuccess) return err;
         const dim3 grid((g.inner + 63) / 64 + (g.outer + 63) / 64, (g.r + 15) / 16, g.n);
-        err = launch(k_back_weights<TX>, grid, dim3(kThreads), stream, nullptr, nullptr, g,
-                     static_cast<const int32_t *>(offsets), static_cast<const int32_t *>(order),
-                     static_cast<const float *>(v), static_cast<const float *>(u));
+        return launch(k_back_weights<TX>, grid, dim3(kThreads), stream, nullptr, nullptr, g,
+                      static_cast<const int32_t *>(offsets), static_cast<const int32_t *>(order),
+                      static_cast<const float *>(v), static_cast<const float *>(u));
     }
-    return err;
+
+    TW *at = reinterpret_cast<TW *>(ws + s.at), *bt = reinterpret_cast<TW *>(ws + s.bt);
+    TW *ap = s.padded ? reinterpret_cast<TW *>(ws + s.ap) : nullptr;
+    err = launch(k_back_layout<TW>, dim3((s.ip + 63) / 64 + (s.op + 63) / 64, (s.rp + 31) / 32, g.n), dim3(kThreads), stream,
+                 nullptr, nullptr, static_cast<const TW *>(g.a), static_cast<const TW *>(g.b), at, bt, ap, g.inner, g.outer,
+                 s.ip, s.op, g.r, s.rp);
+    if (err != hipSuccess) return err;
+    BackBlocks b{g.x, g.d_out, g.dx_base, g.d_x, g.ld_x, g.ld_d_out, g.ld_dx_base, g.ld_d_x, g.a, at, bt,
+                 g.adapter, g.scale, v, u, g.T, s.ip, s.op, g.n, g.r, s.rp};
+    const int copies = std::min((g.T + 3) / 4, 2048);
+    if (s.padded) {
+        Reshape m{{g.x, g.d_out, g.dx_base}, {ws + s.x, ws + s.d_out, ws + s.d_x}, {g.ld_x, g.ld_d_out, g.ld_dx_base},
+                  {s.ip, s.op, s.ip}, {g.inner, g.outer, g.inner}, {s.ip, s.op, s.ip}};
+        err = launch(k_back_reshape<TX>, dim3(copies, 3), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
+        if (err != hipSuccess) return err;
+        b.x = ws + s.x;
+        b.d_out = ws + s.d_out;
+        b.dx_base = b.d_x = ws + s.d_x;
+        b.ld_x = b.ld_dx_base = b.ld_d_x = s.ip;
+        b.ld_d_out = s.op;
+        b.a = ap;
+    }
+    err = g.r <= 16   ? back_tile<TX, TW, 1, 32>(b, stream)
+          : g.r <= 32 ? back_tile<TX, TW, 2, 32>(b, stream)
+          : g.r <= 64 ? back_tile<TX, TW, 4, 64>(b, stream)
+                      : back_tile<TX, TW, 4, kMaxRank>(b, stream);
+    if (err != hipSuccess) return err;
+    if (s.padded) {
+        Reshape m{{b.d_x}, {g.d_x}, {s.ip}, {g.ld_d_x}, {g.inner}, {g.inner}};
+        err = launch(k_back_reshape<TX>, dim3(copies, 1), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
+        if (err != hipSuccess) return err;
+    }
+    const BackWeights w{b.x, b.d_out, b.ld_x, b.ld_d_out, offsets, order, v, u, reinterpret_cast<float *>(ws + s.partial),
+                        g.d_a, g.d_b, g.inner, g.outer, s.ip, s.op, g.n, g.r, s.piece_rows};
+    const int nt = g.r <= 16 ? 1 : g.r <= 32 ? 2 : 4;
+    const dim3 grid((s.ip + kPieceCols - 1) / kPieceCols + (s.op + kPieceCols - 1) / kPieceCols, s.max_pieces,
+                    (g.r + 16 * nt - 1) / (16 * nt));
+    err = nt == 1   ? launch(k_back_pieces<TX, 1>, grid, dim3(kThreads), stream, nullptr, nullptr, w)
+          : nt == 2 ? launch(k_back_pieces<TX, 2>, grid, dim3(kThreads), stream, nullptr, nullptr, w)
+                    : launch(k_back_pieces<TX, 4>, grid, dim3(kThreads), stream, nullptr, nullptr, w);
+    if (err != hipSuccess) return err;
+    return launch(k_back_join, dim3((g.inner + g.outer + kThreads - 1) / kThreads, g.r, g.n), dim3(kThreads), stream,
+                  nullptr, nullptr, w);
 }
 
 }  // namespace
 
-size_t adapters_workspace(int T, int, int, int n, int r) { return back_space(T, n, r).bytes; }
+size_t adapters_workspace(int T, int inner, int outer, int n, int r) { return back_space(T, inner, outer, n, r).bytes; }
 
 hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &g, hipStream_t stream) {
     if (g.T == 0) return hipSuccess;
