@@ -12,12 +12,13 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWgPicks = 2048;         // picks a dispatch workgroup ranks at most
-constexpr int kCopies = 8;             // copies of a histogram, by lane: picks of one expert in a
-                                       // wave would otherwise add to one LDS word in turn
-constexpr int kDirectPicks = 32768;    // up to here every workgroup counts all picks itself
-constexpr int kSlicePicks = 8192;      // picks of a histogram slice above
-constexpr int kMaxSlices = 512;
+constexpr int kWgPicks = 512;         // picks a dispatch workgroup ranks at most
+constexpr int kCopies = 8;            // copies of a histogram, by lane: picks of one expert in a wave
+                                      // would otherwise add to one LDS word in turn
+constexpr int kDirectPicks = 4096;    // up to here every workgroup counts all picks itself
+constexpr int kSlicePicks = 2048;     // picks of a histogram slice above, at least
+constexpr int kMaxSlices = 64;
+constexpr int kWgTarget = 1024;       // workgroups of a dispatch that copies rows: four a CU
 
 int slices_of(int N) {
     if (N <= kDirectPicks) return 0;
@@ -25,12 +26,26 @@ int slices_of(int N) {
 }
 int per_slice(int N, int slices) { return (N + slices - 1) / slices; }
 
-// Adds picks p0 .. p1 to the histogram copies.
+// Adds picks p0 .. p1 to the histogram copies, eight picks a thread in flight.
 __device__ inline void count(const int32_t *ids, int p0, int p1, int E, int *hist) {
     const int copy = threadIdx.x & (kCopies - 1);
-    for (int p = p0 + (int)threadIdx.x; p < p1; p += kThreads) {
-        const int e = ids[p];
+    auto add = [&](int e) {
         if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e * kCopies + copy], 1);
+    };
+    int p = p0 + 4 * (int)threadIdx.x;
+    for (; p + 4 * kThreads + 4 <= p1; p += 8 * kThreads) {
+        int e[8];
+        __builtin_memcpy(e, ids + p, 16);
+        __builtin_memcpy(e + 4, ids + p + 4 * kThreads, 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) add(e[i]);
+    }
+    for (; p < p1; p += 4 * kThreads) {
+        int e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = p + i < p1 ? ids[p + i] : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add(e[i]);
     }
 }
 
@@ -55,12 +70,14 @@ __global__ __launch_bounds__(kThreads) void k_slice_counts(const int32_t *ids, i
 //   offsets[e] + (valid picks of e before p),
 // so it counts, per expert, all picks and the picks before its own -- from the ids themselves, or for
 // many picks from the slices' counts -- and then ranks its own picks in order, 64 at a time by one
-// wave: the lanes with the same expert are found by one ballot per bit of the id.
-template <typename T>
+// wave: the lanes with the same expert are found by one ballot per bit of the id.  The rows follow:
+// the first four tokens' pieces are requested before all that.  EM: experts there is room for.
+template <typename T, int EM>
 __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int tokens, int lanes_log2, const int32_t *counts,
                                                        int slices, int per) {
-    __shared__ int hist[kMaxSegments * kCopies];
-    __shared__ int next[kMaxSegments];   // next row of each expert
+    __shared__ int hist[EM * kCopies];
+    __shared__ int next[EM];   // picks before the workgroup's, then the next row, of each expert
+    __shared__ int all[EM];    // picks of each expert
     __shared__ int row_of[kWgPicks];
     __shared__ int wave_sum[kThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -68,34 +85,50 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int token
     const int t0 = blockIdx.x * tokens, t1 = min(a.T, t0 + tokens);
     const int p0 = t0 * a.k, p1 = t1 * a.k;
 
+    const int L = 1 << lanes_log2, groups = kThreads >> lanes_log2, l = tid & (L - 1);
+    const int first = t0 + (tid >> lanes_log2), pieces = (a.H + kVec<T> - 1) / kVec<T>;
+    const T *x = static_cast<const T *>(a.x);
+    auto request = [&](uint4 (&v)[4], int t, int c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (t + u * groups < t1) v[u] = load_piece(x + (int64_t)(t + u * groups) * a.ld_x + c * kVec<T>, a.H - c * kVec<T>);
+    };
+    uint4 ahead[4];
+    if (x && l < pieces) request(ahead, first, l);
+
     for (int i = tid; i < E * kCopies; i += kThreads) hist[i] = 0;
     __syncthreads();
     const int slice = counts ? p0 / per : 0;
     count(a.ids, counts ? slice * per : 0, p0, E, hist);
     __syncthreads();
-    // four consecutive experts a thread
-    int before[4], total[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = 4 * tid + i;
-        before[i] = e < E ? total_of(hist, e) : 0;
-        total[i] = 0;
-        if (counts && e < E) {
+    for (int e = tid; e < E; e += kThreads) {
+        int before = total_of(hist, e), sum = 0;
+        if (counts) {
+#pragma unroll 8
             for (int s = 0; s < slices; ++s) {
                 const int n = counts[(size_t)s * E + e];
-                total[i] += n;
-                before[i] += s < slice ? n : 0;
+                sum += n;
+                before += s < slice ? n : 0;
             }
         }
+        next[e] = before;
+        all[e] = sum;
     }
     if (!counts) {
         __syncthreads();
         count(a.ids, p0, N, E, hist);
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) total[i] = 4 * tid + i < E ? total_of(hist, 4 * tid + i) : 0;
+        for (int e = tid; e < E; e += kThreads) all[e] = total_of(hist, e);
     }
-    const int mine = total[0] + total[1] + total[2] + total[3];
+    __syncthreads();
+    // the experts' first rows: consecutive experts a thread
+    constexpr int EP = EM / kThreads;
+    int total[EP], mine = 0;
+#pragma unroll
+    for (int i = 0; i < EP; ++i) {
+        total[i] = EP * tid + i < E ? all[EP * tid + i] : 0;
+        mine += total[i];
+    }
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -108,10 +141,10 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int token
     for (int w = 0; w < wave; ++w) start += wave_sum[w];
     const int n_rows = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = 4 * tid + i;
+    for (int i = 0; i < EP; ++i) {
+        const int e = EP * tid + i;
         if (e < E) {
-            next[e] = start + before[i];
+            next[e] += start;
             if (blockIdx.x == 0) a.offsets[e] = start;
         }
         start += total[i];
@@ -154,19 +187,26 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int token
             a.src[p] = -1;
             if (a.expert) a.expert[p] = -1;
         }
-    if (!a.x) return;
+    if (!x) return;
     __syncthreads();
 
-    const int L = 1 << lanes_log2, group = tid >> lanes_log2, l = tid & (L - 1);
-    const int pieces = (a.H + kVec<T> - 1) / kVec<T>;
-    for (int t = t0 + group; t < t1; t += kThreads >> lanes_log2) {
-        const T *x = static_cast<const T *>(a.x) + (int64_t)t * a.ld_x;
-        for (int c = l; c < pieces; c += L) {
-            const int n = a.H - c * kVec<T>;
-            const uint4 v = load_piece(x + c * kVec<T>, n);
-            for (int j = 0; j < a.k; ++j) {
-                const int row = row_of[(t - t0) * a.k + j];
-                if (row >= 0) store_piece(static_cast<T *>(a.rows) + (int64_t)row * a.ld_rows + c * kVec<T>, v, n);
+    for (int c = l; c < pieces; c += L) {
+        const int n = a.H - c * kVec<T>;
+        T *rows = static_cast<T *>(a.rows) + c * kVec<T>;
+        for (int t = first; t < t1; t += 4 * groups) {
+            uint4 v[4];
+            if (c == l && t == first)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[u] = ahead[u];
+            else
+                request(v, t, c);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (t + u * groups >= t1) break;
+                for (int j = 0; j < a.k; ++j) {
+                    const int row = row_of[(t + u * groups - t0) * a.k + j];
+                    if (row >= 0) store_piece(rows + (int64_t)row * a.ld_rows, v[u], n);
+                }
             }
         }
     }
@@ -184,7 +224,8 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(CombineRowsArgs a, in
     for (int c = threadIdx.x & (L - 1); c < pieces; c += L) {
         const int n = a.H - c * kVec<T>;
         float sum[kVec<T>] = {};
-        if (a.base) unpack<T>(load_piece(static_cast<const T *>(a.base) + (int64_t)t * a.ld_base + c * kVec<T>, n), sum);
+        uint4 base = {0, 0, 0, 0};
+        if (a.base) base = load_piece(static_cast<const T *>(a.base) + (int64_t)t * a.ld_base + c * kVec<T>, n);
         for (int j0 = 0; j0 < a.k; j0 += 8) {
             uint4 v[8];
             float g[8];
@@ -207,6 +248,10 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(CombineRowsArgs a, in
                 for (int i = 0; i < kVec<T>; ++i) sum[i] = fmaf(g[u], f[i], sum[i]);
             }
         }
+        float f[kVec<T>];
+        unpack<T>(base, f);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) sum[i] += f[i];
         store_piece(static_cast<T *>(a.out) + (int64_t)t * a.ld_out + c * kVec<T>, pack<T>(sum), n);
     }
 }
@@ -289,10 +334,14 @@ hipError_t dispatch(const DispatchArgs &a, int32_t *counts, hipStream_t stream) 
                                     a.E, counts);
         if (e != hipSuccess) return e;
     }
-    const int tokens = std::max(1, std::min((a.T + 1023) / 1024, kWgPicks / a.k));
-    const int grid = std::max(1, (a.T + tokens - 1) / tokens);
-    return launch(k_dispatch<T>, dim3(grid), dim3(kThreads), stream, nullptr, nullptr, a, tokens,
-                  lanes_for(a.H, kVec<T>), static_cast<const int32_t *>(slices ? counts : nullptr), slices, per);
+    // without rows to copy, as many tokens a workgroup as it can rank
+    const int tokens = std::max(1, a.x ? std::min((a.T + kWgTarget - 1) / kWgTarget, kWgPicks / a.k) : kWgPicks / a.k);
+    const dim3 grid(std::max(1, (a.T + tokens - 1) / tokens)), block(kThreads);
+    const int32_t *from = slices ? counts : nullptr;
+    const int lanes = lanes_for(a.H, kVec<T>);
+    return a.E <= 256 ? launch(k_dispatch<T, 256>, grid, block, stream, nullptr, nullptr, a, tokens, lanes, from, slices, per)
+                      : launch(k_dispatch<T, kMaxSegments>, grid, block, stream, nullptr, nullptr, a, tokens, lanes, from,
+                               slices, per);
 }
 
 }  // namespace
