@@ -12,57 +12,66 @@ from . import ERR_INVALID, OK, T_BF16, T_F16, T_F32, MoeError, gpu_lib
 
 _TYPES = {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16}
 
+# torch.cuda.current_device() and .current_stream().cuda_stream without their Python layers (about 2 us a call)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda gpu: torch.cuda.current_stream(gpu).cuda_stream))
+
 
 def _refuse(msg):
     raise MoeError(ERR_INVALID, msg)
 
 
-def _matrix(name, t, rows, cols, dtype, device):
+# A call of few rows takes the GPU a few microseconds, so the checks are one comparison of what should
+# be with what is for each tensor, and the words for what is wrong are found only then.
+
+def _matrix(name, t, rows, cols, dtype, gpu):
     """Address and row distance of a [rows x cols] matrix."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        _refuse(f"{name} has shape {tuple(t.shape)}, not ({rows}, {cols})")
-    if t.dtype is not dtype:
-        _refuse(f"{name} is {t.dtype}, not {dtype}")
-    if t.device != device:
-        _refuse(f"{name} is on {t.device}, not {device}")
-    ld, unit = t.stride()
-    if cols > 1 and unit != 1:
-        _refuse(f"{name} is not stored by rows")
-    if rows <= 1:
-        ld = max(ld, cols)
-    if ld < cols:
-        _refuse(f"{name} has rows that overlap")
-    return t.data_ptr(), ld
+    if t.shape == (rows, cols) and t.dtype is dtype and t.get_device() == gpu:
+        ld, unit = t.stride()
+        if unit == 1 and ld >= cols:
+            return t.data_ptr(), ld
+        if cols > 1 and unit != 1:
+            _refuse(f"{name} is not stored by rows")
+        if ld < cols and rows > 1:
+            _refuse(f"{name} has rows that overlap")
+        return t.data_ptr(), max(ld, cols)
+    _refuse(f"{name} must be a {dtype} tensor of shape {(rows, cols)} on GPU {gpu}, got {t.dtype} {tuple(t.shape)} "
+            f"on {t.device}")
+
+
+def _array(name, t, shape, dtype, gpu):
+    if t.shape == shape and t.dtype is dtype and t.get_device() == gpu and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {gpu}, "
+            f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _dims(name, t, n):
-    if t.dim() != n:
-        _refuse(f"{name} has {t.dim()} dimensions, not {n}")
-    return t.shape
-
-
-def _array(name, t, shape, dtype, device):
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
-                f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    shape = t.shape
+    if len(shape) != n:
+        _refuse(f"{name} has {len(shape)} dimensions, not {n}")
+    return shape
 
 
 def _type(name, t):
-    if t.device.type != "cuda":
+    """Type code and GPU of a tensor of values."""
+    gpu = t.get_device()
+    if gpu < 0:
         _refuse(f"{name} is on {t.device}, not a GPU")
-    if t.dtype not in _TYPES:
+    code = _TYPES.get(t.dtype)
+    if code is None:
         _refuse(f"{name} is {t.dtype}: float32, float16 or bfloat16 is wanted")
-    return _TYPES[t.dtype]
+    return code, gpu
 
 
-def _call(fn, device, stream, *args):
-    """The library call with `device` current and the stream's handle as last argument."""
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _call(fn, device, stream, *args)
+def _call(fn, gpu, stream, *args):
+    """The library call with `gpu` current and the stream's handle as last argument."""
+    if _current_device() != gpu:
+        with torch.cuda.device(gpu):
+            return _call(fn, gpu, stream, *args)
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = _current_stream(gpu)
     else:
         handle = stream if isinstance(stream, int) else stream.cuda_stream
     rc = fn(*args, handle)
@@ -70,12 +79,13 @@ def _call(fn, device, stream, *args):
         raise MoeError(rc, gpu_lib().moe_last_error().decode())
 
 
-def _workspace(nbytes, given, device, stream):
+def _workspace(nbytes, given, gpu, stream):
     """A workspace tensor: the caller's, or a new one that belongs to the call's stream."""
     if given is not None:
-        if given.device != device or not given.is_contiguous():
-            _refuse(f"workspace must be a contiguous tensor on {device}")
+        if given.get_device() != gpu or not given.is_contiguous():
+            _refuse(f"workspace must be a contiguous tensor on GPU {gpu}")
         return given
+    device = torch.device("cuda", gpu)
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     s = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
@@ -92,9 +102,9 @@ def tokens_dispatch(x, ids, n_experts, rows, offsets, pos, src, expert, workspac
     makes the order alone.
     """
     lib = gpu_lib()
-    device = ids.device
-    if device.type != "cuda":
-        _refuse(f"ids is on {device}, not a GPU")
+    gpu = ids.get_device()
+    if gpu < 0:
+        _refuse(f"ids is on {ids.device}, not a GPU")
     T, k = _dims("ids", ids, 2)
     n = T * k
     if (x is None) != (rows is None):
@@ -103,60 +113,60 @@ def tokens_dispatch(x, ids, n_experts, rows, offsets, pos, src, expert, workspac
     if x is None:
         dtype, H, px, ldx, pr, ldr = T_F32, 1, None, 1, None, 1
     else:
-        dtype, H = _type("x", x), _dims("x", x, 2)[1]
-        px, ldx = _matrix("x", x, T, H, x.dtype, device)
-        pr, ldr = _matrix("rows", rows, n, H, x.dtype, device)
-    p_ids, p_off = _array("ids", ids, (T, k), i32, device), _array("offsets", offsets, (n_experts + 1,), i32, device)
-    p_pos, p_src = _array("pos", pos, (T, k), i32, device), _array("src", src, (n,), i32, device)
-    p_exp = _array("expert", expert, (n,), i32, device)
+        dtype, H = _type("x", x)[0], _dims("x", x, 2)[1]
+        px, ldx = _matrix("x", x, T, H, x.dtype, gpu)
+        pr, ldr = _matrix("rows", rows, n, H, x.dtype, gpu)
+    p_ids, p_off = _array("ids", ids, (T, k), i32, gpu), _array("offsets", offsets, (n_experts + 1,), i32, gpu)
+    p_pos, p_src = _array("pos", pos, (T, k), i32, gpu), _array("src", src, (n,), i32, gpu)
+    p_exp = _array("expert", expert, (n,), i32, gpu)
     need = lib.moe_tokens_workspace(T, k, n_experts)
-    ws = _workspace(need, workspace, device, stream) if need else None
-    _call(lib.moe_tokens_dispatch, device, stream, px, ldx, dtype, T, H, p_ids, k, n_experts, pr, ldr, p_off, p_pos,
+    ws = _workspace(need, workspace, gpu, stream) if need else None
+    _call(lib.moe_tokens_dispatch, gpu, stream, px, ldx, dtype, T, H, p_ids, k, n_experts, pr, ldr, p_off, p_pos,
           p_src, p_exp, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
 
 
 def tokens_dispatch_backward(d_rows, pos, d_x, stream=None):
     """d_x[t] = sum_j d_rows[pos[t, j]] (moe_tokens_dispatch_backward)."""
-    dtype, device = _type("d_rows", d_rows), d_rows.device
+    dtype, gpu = _type("d_rows", d_rows)
     (T, k), (R, H) = _dims("pos", pos, 2), _dims("d_rows", d_rows, 2)
-    pr, ldr = _matrix("d_rows", d_rows, R, H, d_rows.dtype, device)
-    px, ldx = _matrix("d_x", d_x, T, H, d_rows.dtype, device)
-    p_pos = _array("pos", pos, (T, k), torch.int32, device)
-    _call(gpu_lib().moe_tokens_dispatch_backward, device, stream, pr, ldr, R, dtype, T, H, p_pos, k, px, ldx)
+    pr, ldr = _matrix("d_rows", d_rows, R, H, d_rows.dtype, gpu)
+    px, ldx = _matrix("d_x", d_x, T, H, d_rows.dtype, gpu)
+    p_pos = _array("pos", pos, (T, k), torch.int32, gpu)
+    _call(gpu_lib().moe_tokens_dispatch_backward, gpu, stream, pr, ldr, R, dtype, T, H, p_pos, k, px, ldx)
 
 
 def tokens_combine(rows, pos, gate, out, base=None, stream=None):
     """out[t] = base[t] + sum_j gate[t, j] rows[pos[t, j]] (moe_tokens_combine); base may be out."""
-    dtype, device = _type("rows", rows), rows.device
+    dtype, gpu = _type("rows", rows)
     (T, k), (R, H) = _dims("pos", pos, 2), _dims("rows", rows, 2)
-    pr, ldr = _matrix("rows", rows, R, H, rows.dtype, device)
-    po, ldo = _matrix("out", out, T, H, rows.dtype, device)
-    pb, ldb = (None, H) if base is None else _matrix("base", base, T, H, rows.dtype, device)
-    p_pos = _array("pos", pos, (T, k), torch.int32, device)
-    p_gate = _array("gate", gate, (T, k), torch.float32, device)
-    _call(gpu_lib().moe_tokens_combine, device, stream, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pb, ldb, po, ldo)
+    pr, ldr = _matrix("rows", rows, R, H, rows.dtype, gpu)
+    po, ldo = _matrix("out", out, T, H, rows.dtype, gpu)
+    pb, ldb = (None, H) if base is None else _matrix("base", base, T, H, rows.dtype, gpu)
+    p_pos = _array("pos", pos, (T, k), torch.int32, gpu)
+    p_gate = _array("gate", gate, (T, k), torch.float32, gpu)
+    _call(gpu_lib().moe_tokens_combine, gpu, stream, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pb, ldb, po, ldo)
 
 
 def tokens_combine_backward(d_out, rows, pos, gate, d_rows, d_gate, stream=None):
     """d_rows[pos[t, j]] = gate[t, j] d_out[t] and d_gate[t, j] = <d_out[t], rows[pos[t, j]]>
     (moe_tokens_combine_backward); rows of d_rows that no pick names are left as they were."""
-    dtype, device = _type("rows", rows), rows.device
+    dtype, gpu = _type("rows", rows)
     (T, k), (R, H) = _dims("pos", pos, 2), _dims("rows", rows, 2)
-    pd, ldd = _matrix("d_out", d_out, T, H, rows.dtype, device)
-    pr, ldr = _matrix("rows", rows, R, H, rows.dtype, device)
-    pg, ldg = _matrix("d_rows", d_rows, R, H, rows.dtype, device)
-    p_pos = _array("pos", pos, (T, k), torch.int32, device)
-    p_gate = _array("gate", gate, (T, k), torch.float32, device)
-    p_dgate = _array("d_gate", d_gate, (T, k), torch.float32, device)
-    _call(gpu_lib().moe_tokens_combine_backward, device, stream, pd, ldd, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pg,
+    pd, ldd = _matrix("d_out", d_out, T, H, rows.dtype, gpu)
+    pr, ldr = _matrix("rows", rows, R, H, rows.dtype, gpu)
+    pg, ldg = _matrix("d_rows", d_rows, R, H, rows.dtype, gpu)
+    p_pos = _array("pos", pos, (T, k), torch.int32, gpu)
+    p_gate = _array("gate", gate, (T, k), torch.float32, gpu)
+    p_dgate = _array("d_gate", d_gate, (T, k), torch.float32, gpu)
+    _call(gpu_lib().moe_tokens_combine_backward, gpu, stream, pd, ldd, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pg,
           ldg, p_dgate)
 
 
-def _adapter_shapes(a, b, wdtype, device):
+def _adapter_shapes(a, b, gpu):
     n, r, inner = _dims("a", a, 3)
     outer = _dims("b", b, 3)[1]
-    return (n, r, inner, outer, _array("a", a, (n, r, inner), wdtype, device),
-            _array("b", b, (n, outer, r), wdtype, device), _type("a", a))
+    return (n, r, inner, outer, _array("a", a, (n, r, inner), a.dtype, gpu), _array("b", b, (n, outer, r), a.dtype, gpu),
+            _type("a", a)[0])
 
 
 def adapters_forward(x, adapter, a, b, scale, out, base=None, stream=None):
@@ -166,14 +176,14 @@ def adapters_forward(x, adapter, a, b, scale, out, base=None, stream=None):
     and base [T, outer]; base may be out, and None stands for zeros.  a and b have x's type, or any
     type beside fp32 activations.
     """
-    dtype, device, T = _type("x", x), x.device, _dims("x", x, 2)[0]
-    n, r, inner, outer, pa, pb, wtype = _adapter_shapes(a, b, a.dtype, device)
-    px, ldx = _matrix("x", x, T, inner, x.dtype, device)
-    po, ldo = _matrix("out", out, T, outer, x.dtype, device)
-    p_base, ldb = (None, outer) if base is None else _matrix("base", base, T, outer, x.dtype, device)
-    p_ad = _array("adapter", adapter, (T,), torch.int32, device)
-    p_scale = _array("scale", scale, (n,), torch.float32, device)
-    _call(gpu_lib().moe_adapters_forward, device, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
+    (dtype, gpu), T = _type("x", x), _dims("x", x, 2)[0]
+    n, r, inner, outer, pa, pb, wtype = _adapter_shapes(a, b, gpu)
+    px, ldx = _matrix("x", x, T, inner, x.dtype, gpu)
+    po, ldo = _matrix("out", out, T, outer, x.dtype, gpu)
+    p_base, ldb = (None, outer) if base is None else _matrix("base", base, T, outer, x.dtype, gpu)
+    p_ad = _array("adapter", adapter, (T,), torch.int32, gpu)
+    p_scale = _array("scale", scale, (n,), torch.float32, gpu)
+    _call(gpu_lib().moe_adapters_forward, gpu, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
           wtype, p_scale, n, r, po, ldo)
 
 
@@ -183,16 +193,16 @@ def adapters_backward(d_out, x, adapter, a, b, scale, d_x, d_a, d_b, dx_base=Non
     be d_x, and None stands for zeros; a workspace (any contiguous tensor of enough bytes, 16-byte
     aligned) may be kept by the caller."""
     lib = gpu_lib()
-    dtype, device, T = _type("x", x), x.device, _dims("x", x, 2)[0]
-    n, r, inner, outer, pa, pb, wtype = _adapter_shapes(a, b, a.dtype, device)
-    px, ldx = _matrix("x", x, T, inner, x.dtype, device)
-    pd, ldd = _matrix("d_out", d_out, T, outer, x.dtype, device)
-    pg, ldg = _matrix("d_x", d_x, T, inner, x.dtype, device)
-    p_base, ldb = (None, inner) if dx_base is None else _matrix("dx_base", dx_base, T, inner, x.dtype, device)
-    p_ad = _array("adapter", adapter, (T,), torch.int32, device)
-    p_scale = _array("scale", scale, (n,), torch.float32, device)
-    p_da = _array("d_a", d_a, (n, r, inner), torch.float32, device)
-    p_db = _array("d_b", d_b, (n, outer, r), torch.float32, device)
-    ws = _workspace(lib.moe_adapters_workspace(T, inner, outer, n, r), workspace, device, stream)
-    _call(lib.moe_adapters_backward, device, stream, pd, ldd, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
+    (dtype, gpu), T = _type("x", x), _dims("x", x, 2)[0]
+    n, r, inner, outer, pa, pb, wtype = _adapter_shapes(a, b, gpu)
+    px, ldx = _matrix("x", x, T, inner, x.dtype, gpu)
+    pd, ldd = _matrix("d_out", d_out, T, outer, x.dtype, gpu)
+    pg, ldg = _matrix("d_x", d_x, T, inner, x.dtype, gpu)
+    p_base, ldb = (None, inner) if dx_base is None else _matrix("dx_base", dx_base, T, inner, x.dtype, gpu)
+    p_ad = _array("adapter", adapter, (T,), torch.int32, gpu)
+    p_scale = _array("scale", scale, (n,), torch.float32, gpu)
+    p_da = _array("d_a", d_a, (n, r, inner), torch.float32, gpu)
+    p_db = _array("d_b", d_b, (n, outer, r), torch.float32, gpu)
+    ws = _workspace(lib.moe_adapters_workspace(T, inner, outer, n, r), workspace, gpu, stream)
+    _call(lib.moe_adapters_backward, gpu, stream, pd, ldd, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
           wtype, p_scale, n, r, pg, ldg, p_da, p_db, ws.data_ptr(), ws.numel() * ws.element_size())
