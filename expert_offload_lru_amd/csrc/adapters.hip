@@ -10,24 +10,28 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowCalls = 256;   // rows of a call that takes a workgroup a row
+constexpr int kRowCalls = 256;    // rows of a call that takes a workgroup a row
+constexpr int kRowTarget = 512;   // workgroups of such a call: two a CU
 
-// n <= 8 elements at p as fp32, zeros behind them.
+// Eight elements at p (n of them there, zeros behind), as loaded and as fp32.
 template <typename T>
-__device__ inline void load8(const T *p, int n, float (&f)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        unpack<T>(load_piece(p, n), f);
-    } else {
-        float lo[4], hi[4];
-        unpack<T>(load_piece(p, n), lo);
-        unpack<T>(load_piece(p + 4, n - 4), hi);
+struct Eight {
+    static constexpr int kPieces = sizeof(T) / 2;
+    uint4 raw[kPieces];
+    __device__ __forceinline__ void load(const T *p, int n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = lo[i];
-            f[4 + i] = hi[i];
+        for (int i = 0; i < kPieces; ++i) raw[i] = load_piece(p + i * kVec<T>, n - i * kVec<T>);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            float e[kVec<T>];
+            unpack<T>(raw[i], e);
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) f[i * kVec<T> + k] = e[k];
         }
     }
-}
+};
 
 __device__ inline float wave_total(float v) {
 #pragma unroll
@@ -35,44 +39,88 @@ __device__ inline float wave_total(float v) {
     return v;
 }
 
-// v[q] = <a's row q, x> for q < r: a wave per row of a.
+// v[q] = <a's row q, x> for q < r: four rows of a at a time a wave, their loads in flight together.
 template <typename TX, typename TW>
 __device__ inline void shrink_row(const TX *x, const TW *a, int inner, int r, float *v) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int q = wave; q < r; q += kThreads / 64) {
-        float s = 0.f;
+    for (int q0 = wave * 4; q0 < r; q0 += kThreads / 64 * 4) {
+        float s[4] = {};
+#pragma unroll 2
         for (int c = lane * 8; c < inner; c += 512) {
-            float fx[8], fa[8];
-            load8(x + c, inner - c, fx);
-            load8(a + (size_t)q * inner + c, inner - c, fa);
+            Eight<TX> ex;
+            Eight<TW> ea[4];
+            ex.load(x + c, inner - c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(fx[i], fa[i], s);
+            for (int i = 0; i < 4; ++i) ea[i].load(a + (size_t)min(q0 + i, r - 1) * inner + c, inner - c);
+            float fx[8];
+            ex.get(fx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float fa[8];
+                ea[i].get(fa);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) s[i] = fmaf(fx[k], fa[k], s[i]);
+            }
         }
-        s = wave_total(s);
-        if (lane == 0) v[q] = s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = wave_total(s[i]);
+            if (lane == 0 && q0 + i < r) v[q0 + i] = s[i];
+        }
     }
 }
 
+// A workgroup a row and slice of the columns: v by dot products (each slice makes its own), then a
+// thread a column.  For calls of few rows, whose time is the chain of loads: the first column's share
+// of b and base is requested before v is made.
 template <typename TX, typename TW>
-__global__ __launch_bounds__(kThreads) void k_adapters_row(AdapterArgs g) {
-    __shared__ float v[kMaxRank];
+__global__ __launch_bounds__(kThreads) void k_adapters_row(AdapterArgs g, int slice_cols) {
+    __shared__ __align__(16) float v[kMaxRank];
     const int row = blockIdx.x, e = g.adapter[row];
+    const int o0 = blockIdx.y * slice_cols + threadIdx.x, o1 = min(g.outer, (int)(blockIdx.y + 1) * slice_cols);
     const bool has = (unsigned)e < (unsigned)g.n;
-    if (has)
+    const TX *base = g.base ? static_cast<const TX *>(g.base) + row * g.ld_base : nullptr;
+    TX *out = static_cast<TX *>(g.out) + row * g.ld_out;
+    const TW *b = static_cast<const TW *>(g.b) + (has ? (size_t)e * g.outer * g.r : 0);
+    Eight<TW> ahead[2];
+    float scale = 0.f, from = 0.f;
+    if (o0 < o1) {
+        if (has)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ahead[i].load(b + (size_t)o0 * g.r + 8 * i, g.r - 8 * i);
+        if (base) from = widen(base[o0]);
+    }
+    if (has) {
+        scale = g.scale[e];
         shrink_row(static_cast<const TX *>(g.x) + row * g.ld_x, static_cast<const TW *>(g.a) + (size_t)e * g.r * g.inner,
                    g.inner, g.r, v);
+        if (threadIdx.x >= (unsigned)g.r && threadIdx.x < ((g.r + 7) & ~7u)) v[threadIdx.x] = 0.f;
+    }
     __syncthreads();
-    const float scale = has ? g.scale[e] : 0.f;
-    const TX *base = static_cast<const TX *>(g.base);
-    TX *out = static_cast<TX *>(g.out) + row * g.ld_out;
-    for (int o = threadIdx.x; o < g.outer; o += kThreads) {
+    auto dot = [&](const Eight<TW> &eb, int q, float s) __attribute__((always_inline)) {
+        float f[8];
+        eb.get(f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(f[k], v[q + k], s);
+        return s;
+    };
+    for (int o = o0; o < o1; o += kThreads) {
         float s = 0.f;
         if (has) {
-            const TW *b = static_cast<const TW *>(g.b) + ((size_t)e * g.outer + o) * g.r;
-            for (int q = 0; q < g.r; ++q) s = fmaf(widen(b[q]), v[q], s);
+            if (o != o0)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) ahead[i].load(b + (size_t)o * g.r + 8 * i, g.r - 8 * i);
+            s = dot(ahead[0], 0, 0.f);
+            if (g.r > 8) s = dot(ahead[1], 8, s);
+            for (int q = 16; q < g.r; q += 8) {
+                Eight<TW> eb;
+                eb.load(b + (size_t)o * g.r + q, g.r - q);
+                s = dot(eb, q, s);
+            }
             s *= scale;
         }
-        out[o] = base ? narrow<TX>(widen(base[row * g.ld_base + o]) + s) : narrow<TX>(s);
+        const float add = o == o0 ? from : base ? widen(base[o]) : 0.f;
+        out[o] = narrow<TX>(add + s);
     }
 }
 
@@ -635,15 +683,16 @@ struct BackBlocks {
     int T, ip, op, n, r, rp;
 };
 
-// d_x = dx_base + u A of 16 rows a workgroup, and v and u; built as k_adapters_tile.
+// d_x = dx_base + u A of 16 rows a workgroup, and u; built as k_adapters_tile.  v is the work of one more
+// workgroup a block (the last slice), which shares nothing with the others but the adapters' numbers.
 template <typename TX, typename TW, int NT, int RM>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4))) void k_back_tile(
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(std::is_same_v<TX, f16> && NT == 4 ? 2 : 4))) void k_back_tile(
     BackBlocks g, int slice_cols, int slices, int turns) {
     constexpr int RP = RM + 4;
     __shared__ __align__(16) float part[kTileWaves * 256 * NT];
-    __shared__ __align__(16) float v[16 * RP], u[16 * RP];
-    const int of = blockIdx.x >> 3, block = of / slices * 8 + (blockIdx.x & 7), turn = turns - 1 - blockIdx.y;
-    const int row0 = block * kTileRows, slice = of % slices;
+    __shared__ __align__(16) float u[16 * RP];
+    const int of = blockIdx.x >> 3, block = of / (slices + 1) * 8 + (blockIdx.x & 7), turn = turns - 1 - blockIdx.y;
+    const int row0 = block * kTileRows, slice = of % (slices + 1);
     if (row0 >= g.T) return;
     Lane l;
     const int row = row0 + l.l16;
@@ -652,7 +701,7 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
     const bool none = row < g.T && !valid;
     int e = row < g.T && valid ? id : -1;
     Shrink<TX, TW, NT> x, dy;
-    Expand<TX, TW, sizeof(TX) == 2 && (NT > 1 || std::is_same_v<TX, f16>) ? 2 : 4> y;
+    Expand<TX, TW, sizeof(TX) == 2 ? 2 : 4> y;
     x.m = rows_of<TX>(g.x, g.ld_x, row0, g.T, g.ip);
     x.row = l.l16 * (unsigned)g.ld_x * sizeof(TX);
     x.cols = g.ip;
@@ -679,13 +728,23 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
         y.out_row = mine ? out_row : kNowhere;
         const float scale = g.scale[now];
         const int g0 = y.c0 + l.wave * 64;
-        if (slice == 0)
+        auto keep = [&](float *to) __attribute__((always_inline)) {
+            for (int i = threadIdx.x; i < 16 * r; i += kTileThreads) {
+                const int k = i / r, q = i - k * r;
+                if ((rows >> k) & 1) to[(size_t)(row0 + k) * r + q] = u[k * RP + q];
+            }
+        };
+        if (slice == slices) {
             for (int q0 = 0; q0 < r; q0 += 16 * NT) {
                 x.run(l, q0, r, part, []() __attribute__((always_inline)) {});
                 __syncthreads();
-                join_parts<NT, RP>(part, v, q0, r, scale);
+                join_parts<NT, RP>(part, u, q0, r, scale);
                 __syncthreads();
             }
+            keep(g.v);
+            __syncthreads();
+            continue;
+        }
         for (int q0 = 0; q0 < r; q0 += 16 * NT) {
             if (q0) __syncthreads();
             dy.run(l, q0, r, part, []() __attribute__((always_inline)) {});
@@ -695,18 +754,11 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4)
         y.early(l);
         y.late(l, g.rp, g0, false);
         __syncthreads();
-        if (slice == 0)
-            for (int i = threadIdx.x; i < 16 * r; i += kTileThreads) {
-                const int k = i / r, q = i - k * r;
-                if ((rows >> k) & 1) {
-                    g.v[(size_t)(row0 + k) * r + q] = v[k * RP + q];
-                    g.u[(size_t)(row0 + k) * r + q] = u[k * RP + q];
-                }
-            }
+        if (slice == 0) keep(g.u);
         y.template run<RP, (RM >= 64 ? 64 : 32) / (4 * Mma<TX>::kChunk)>(l, u, g.rp);
         __syncthreads();
     }
-    if (turn == 0 && __ballot(none) && !(g.dx_base == g.d_x && g.ld_dx_base == g.ld_d_x)) {
+    if (turn == 0 && slice < slices && __ballot(none) && !(g.dx_base == g.d_x && g.ld_dx_base == g.ld_d_x)) {
         y.base_row = none ? base_row : kNowhere;
         y.out_row = none ? out_row : kNowhere;
         y.pass(l);
@@ -758,14 +810,19 @@ __device__ inline Piece find_piece(const int32_t *offsets, int n, int rows, int 
     return found;
 }
 
+// Calls of up to this many rows: an adapter is one piece, its rows are found by the workgroups themselves,
+// and there is neither a sort nor a join.
+constexpr int kSmallBack = 512;
+
 struct BackWeights {
+    const int32_t *adapter;
     const void *x, *d_out;
     int64_t ld_x, ld_d_out;
     const int32_t *offsets, *order;
     const float *v, *u;
     float *partial;      // [piece][r][ip + op]
     float *d_a, *d_b;
-    int inner, outer, ip, op, n, r, piece_rows;
+    int T, inner, outer, ip, op, n, r, piece_rows;
 };
 
 __device__ __forceinline__ void store_grad(const BackWeights &g, int e, bool is_b, int q, int c, float s) {
@@ -780,13 +837,34 @@ __device__ __forceinline__ void store_grad(const BackWeights &g, int e, bool is_
 // a lane loads 16 bytes of 8 rows, and for bf16 turns them into the eight columns' operands, pairs of
 // rows a dword (v_perm), with u and v in two parts of 16 bits together; other types multiply in fp32,
 // whose operand is one element.
-template <typename TX, int NT>
+template <typename TX, int NT, bool SMALL>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NT == 4 && sizeof(TX) == 4 ? 1 : 2))) void k_back_pieces(BackWeights g) {
     constexpr bool kPairs = std::is_same_v<TX, bf16>;
     constexpr int kLoads = sizeof(TX) == 4 ? 2 : 1;   // of 16 bytes for a lane's 8 columns of a row
     __shared__ __align__(16) f32x4 part[kThreads / 64][8][64];
-    const Piece p = find_piece(g.offsets, g.n, g.piece_rows, blockIdx.y);
-    if (p.e < 0) return;
+    Piece p;
+    const int32_t *order;
+    if constexpr (SMALL) {
+        __shared__ int32_t list[kSmallBack];
+        __shared__ int found;
+        if (threadIdx.x < 64) {
+            int at = 0;
+            for (int i = threadIdx.x; i - (int)threadIdx.x < g.T; i += 64) {
+                const bool is = i < g.T && g.adapter[i] == (int)blockIdx.y;
+                const unsigned long long m = __ballot(is);
+                if (is) list[at + __popcll(m & ((1ull << threadIdx.x) - 1))] = i;
+                at += __popcll(m);
+            }
+            if (threadIdx.x == 0) found = at;
+        }
+        __syncthreads();
+        p = Piece{(int)blockIdx.y, 0, 0, found, 1};
+        order = list;
+    } else {
+        p = find_piece(g.offsets, g.n, g.piece_rows, blockIdx.y);
+        if (p.e < 0) return;
+        order = g.order;
+    }
     const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4, wave = threadIdx.x >> 6;
     const int tiles_a = (g.ip + kPieceCols - 1) / kPieceCols;
     const bool is_b = (int)blockIdx.x >= tiles_a;
@@ -809,7 +887,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NT == 
         for (int j = 0; j < 8; ++j) {
             // rows 8 quad + j of the 32 (bf16: a lane's chunk of the reduction), or 4 j + quad
             const int i = b + (kPairs ? 8 * quad + j : 4 * j + quad);
-            const int row = g.order[min(i, p.end - 1)];
+            const int row = order[min(i, p.end - 1)];
 #pragma unroll
             for (int h = 0; h < kLoads; ++h) x[j][h] = load_piece(m + row * ld + at[h], kVec<TX>);
 #pragma unroll
@@ -994,7 +1072,10 @@ hipError_t forward(const AdapterArgs &g, hipStream_t stream) {
         if (g.r <= 64) return forward_tile<TX, TW, 4, 64>(g, stream);
         return forward_tile<TX, TW, 4, kMaxRank>(g, stream);
     }
-    return launch(k_adapters_row<TX, TW>, dim3(g.T), dim3(kThreads), stream, nullptr, nullptr, g);
+    const int groups = (g.outer + kThreads - 1) / kThreads;
+    const int slices = std::max(1, std::min(groups, kRowTarget / g.T)), cols = (groups + slices - 1) / slices * kThreads;
+    return launch(k_adapters_row<TX, TW>, dim3(g.T, (g.outer + cols - 1) / cols), dim3(kThreads), stream, nullptr, nullptr,
+                  g, cols);
 }
 
 template <typename TX, typename TW, int NT, int RM>
@@ -1003,8 +1084,8 @@ hipError_t back_tile(const BackBlocks &g, hipStream_t stream) {
     const int slices = std::max(1, std::min(groups / kTileWaves, 512 / tiles));
     const int cols = (groups + slices - 1) / slices * 64, used = (g.ip + cols - 1) / cols;
     const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / (tiles * slices))));
-    return launch(k_back_tile<TX, TW, NT, RM>, dim3((tiles + 7) / 8 * 8 * used, turns), dim3(kTileThreads), stream,
-                  nullptr, nullptr, g, cols, used, turns);
+    return launch(k_back_tile<TX, TW, NT, RM>, dim3((tiles + 7) / 8 * 8 * (used + 1), turns), dim3(kTileThreads),
+                  stream, nullptr, nullptr, g, cols, used, turns);
 }
 
 template <typename TX, typename TW>
@@ -1013,17 +1094,6 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
     char *ws = static_cast<char *>(workspace);
     int32_t *offsets = reinterpret_cast<int32_t *>(ws + s.offsets), *order = reinterpret_cast<int32_t *>(ws + s.order);
     float *v = reinterpret_cast<float *>(ws + s.v), *u = reinterpret_cast<float *>(ws + s.u);
-    DispatchArgs d{};
-    d.ids = g.adapter;
-    d.offsets = offsets;
-    d.src = order;
-    d.T = g.T;
-    d.H = 1;
-    d.k = 1;
-    d.E = g.n;
-    hipError_t err = launch_dispatch(dtype, d, ws + s.sort, stream);
-    if (err != hipSuccess) return err;
-
     constexpr size_t z = sizeof(TX);
     const bool blocks =
         g.T > 0 && (int64_t)s.rp * std::max(s.ip, s.op) * (int64_t)sizeof(TW) < kBufferBytes &&
@@ -1031,6 +1101,20 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
         (s.padded || (piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.d_out, g.ld_d_out, g.outer, z) &&
                       piecewise(g.d_x, g.ld_d_x, g.inner, z) && reinterpret_cast<uintptr_t>(g.a) % 16 == 0 &&
                       (!g.dx_base || piecewise(g.dx_base, g.ld_dx_base, g.inner, z))));
+    const bool small = blocks && g.T <= kSmallBack;
+    hipError_t err = hipSuccess;
+    if (!small) {
+        DispatchArgs d{};
+        d.ids = g.adapter;
+        d.offsets = offsets;
+        d.src = order;
+        d.T = g.T;
+        d.H = 1;
+        d.k = 1;
+        d.E = g.n;
+        err = launch_dispatch(dtype, d, ws + s.sort, stream);
+        if (err != hipSuccess) return err;
+    }
     if (!blocks) {
         if (g.T > 0) err = launch(k_back_row<TX, TW>, dim3(g.T), dim3(kThreads), stream, nullptr, nullptr, g, v, u);
         if (err != hipSuccess) return err;
@@ -1071,14 +1155,19 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
         err = launch(k_back_reshape<TX>, dim3(copies, 1), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
         if (err != hipSuccess) return err;
     }
-    const BackWeights w{b.x, b.d_out, b.ld_x, b.ld_d_out, offsets, order, v, u, reinterpret_cast<float *>(ws + s.partial),
-                        g.d_a, g.d_b, g.inner, g.outer, s.ip, s.op, g.n, g.r, s.piece_rows};
+    const BackWeights w{g.adapter, b.x, b.d_out, b.ld_x, b.ld_d_out, offsets, order, v, u, reinterpret_cast<float *>(ws + s.partial),
+                        g.d_a, g.d_b, g.T, g.inner, g.outer, s.ip, s.op, g.n, g.r, s.piece_rows};
     const int nt = g.r <= 16 ? 1 : g.r <= 32 ? 2 : 4;
-    const dim3 grid((s.ip + kPieceCols - 1) / kPieceCols + (s.op + kPieceCols - 1) / kPieceCols, s.max_pieces,
+    const dim3 grid((s.ip + kPieceCols - 1) / kPieceCols + (s.op + kPieceCols - 1) / kPieceCols, small ? g.n : s.max_pieces,
                     (g.r + 16 * nt - 1) / (16 * nt));
-    err = nt == 1   ? launch(k_back_pieces<TX, 1>, grid, dim3(kThreads), stream, nullptr, nullptr, w)
-          : nt == 2 ? launch(k_back_pieces<TX, 2>, grid, dim3(kThreads), stream, nullptr, nullptr, w)
-                    : launch(k_back_pieces<TX, 4>, grid, dim3(kThreads), stream, nullptr, nullptr, w);
+    auto pieces = [&](auto sm) {
+        constexpr bool SMALL = decltype(sm)::value;
+        return nt == 1   ? launch(k_back_pieces<TX, 1, SMALL>, grid, dim3(kThreads), stream, nullptr, nullptr, w)
+               : nt == 2 ? launch(k_back_pieces<TX, 2, SMALL>, grid, dim3(kThreads), stream, nullptr, nullptr, w)
+                         : launch(k_back_pieces<TX, 4, SMALL>, grid, dim3(kThreads), stream, nullptr, nullptr, w);
+    };
+    if (small) return pieces(std::true_type{});
+    err = pieces(std::false_type{});
     if (err != hipSuccess) return err;
     return launch(k_back_join, dim3((g.inner + g.outer + kThreads - 1) / kThreads, g.r, g.n), dim3(kThreads), stream,
                   nullptr, nullptr, w);
