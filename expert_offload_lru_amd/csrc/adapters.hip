@@ -10,7 +10,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowCalls = 256;    // rows of a call that takes a workgroup a row
+constexpr int kRowCalls = 512;    // rows of a call that takes a workgroup a row
+constexpr int kTallRows = 4096;   // rows from which blocks are 32 rows high
 constexpr int kRowTarget = 512;   // workgroups of such a call: two a CU
 
 // Eight elements at p (n of them there, zeros behind), as loaded and as fp32.
@@ -137,7 +138,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileThreads = 512;
 constexpr int kTileWaves = kTileThreads / 64;
-constexpr int kTileRows = 16;
+constexpr int kMostRows = 64;   // rows of a block
 constexpr unsigned kNowhere = 0x80000000u;                   // an offset out of every buffer's range
 constexpr int64_t kBufferBytes = (int64_t)kNowhere - 65536;   // a buffer's size at most
 
@@ -225,24 +226,22 @@ struct Lane {
     }
 };
 
-// The first product of a block's rows: v = m w^T.  A wave takes every eighth run of 128 bytes of the
-// rows, two chunks a lane, so that a row's cache line is read by one wave at once, 64 bytes of a row in
-// an instruction.  NT: tiles of 16 ranks at a time.
-template <typename TX, typename TW, int NT>
+// The first product of a block of 16 MT rows: v = m w^T.  The waves take runs of 128 bytes of the
+// rows in turn, two chunks a lane, 64 bytes of a row in an instruction.  NT: tiles of 16 ranks at a time.
+// More rows a block read w from L2 less often, which is what bounds this beside m.
+template <typename TX, typename TW, int NT, int MT, int WAVES>
 struct Shrink {
     typedef Mma<TX> M;
     static constexpr int C = M::kChunk, kRun = 8 * C;
-    static constexpr int U = NT == 1 ? 4 : NT == 2 ? 2 : 1;   // runs in flight
+    static constexpr int U = NT * MT == 1 ? 2 : NT * MT == 2 ? 2 : 1;   // runs in flight
     Buffer m, w;
-    unsigned row;   // the lane's row in m, bytes
+    unsigned row, step;   // the lane's first row in m, and 16 rows, in bytes
     int cols;
 
-    // part[wave][row][q] = the wave's share of sum_k m[row, k] w[q0 + q, k].  `then` is called once,
-    // behind the first loads: what it requests arrives while these are multiplied and joined.
-    template <typename F>
-    __device__ __forceinline__ void run(const Lane &lane, int q0, int r, float *part, F then) const {
+    // part[wave][row][q] = the wave's share of sum_k m[row, k] w[q0 + q, k]
+    __device__ __forceinline__ void run(const Lane &lane, int q0, int r, float *part) const {
         const Lane l = lane.again();
-        f32x4 acc[NT] = {};
+        f32x4 acc[NT][MT] = {};
         unsigned wr[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -250,50 +249,155 @@ struct Shrink {
             wr[i] = q < r ? (unsigned)q * cols : kNowhere / sizeof(TW);
         }
         const int runs = (cols + kRun - 1) / kRun;
-        auto batch = [&](int d, auto first) __attribute__((always_inline)) {
-            Chunk<TX, TX> x[U][2];
+        for (int d = l.wave; d < runs; d += U * WAVES) {
+            Chunk<TX, TX> x[U][MT][2];
             Chunk<TX, TW> a[U][NT][2];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const int k = (d + u * kTileWaves) * kRun + 4 * s * C + l.quad * C;
+                    const int k = (d + u * WAVES) * kRun + 4 * s * C + l.quad * C;
                     const bool in = k < cols;
-                    x[u][s].load(m, in ? row + k * (unsigned)sizeof(TX) : kNowhere);
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) x[u][j][s].load(m, in ? row + j * step + k * (unsigned)sizeof(TX) : kNowhere);
 #pragma unroll
                     for (int i = 0; i < NT; ++i) a[u][i][s].load(w, in ? (wr[i] + k) * (unsigned)sizeof(TW) : kNowhere);
                 }
-            if constexpr (decltype(first)::value) {
-                __builtin_amdgcn_sched_barrier(0);
-                then();
-                __builtin_amdgcn_sched_barrier(0);
-            }
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) acc[i] = M::mul(a[u][i][s].frag(), x[u][s].frag(), acc[i]);
-        };
-        batch(l.wave, std::true_type{});
-        for (int d = U * kTileWaves; d < runs; d += U * kTileWaves) batch(d + l.wave, std::false_type{});
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int j = 0; j < MT; ++j) acc[i][j] = M::mul(a[u][i][s].frag(), x[u][j][s].frag(), acc[i][j]);
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-            *reinterpret_cast<f32x4 *>(part + (l.wave * 16 + l.l16) * (16 * NT) + 16 * i + 4 * l.quad) = acc[i];
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                *reinterpret_cast<f32x4 *>(part + ((l.wave * MT + j) * 16 + l.l16) * (16 * NT) + 16 * i + 4 * l.quad) =
+                    acc[i][j];
     }
 };
 
-// v[row][q0 + q] = scale * (sum of the waves' parts), zeros from rank r up to the next multiple of 32.
-template <int NT, int RP>
-__device__ __forceinline__ void join_parts(const float *part, float *v, int q0, int r, float scale) {
-    if (NT == 1)
-        for (int i = threadIdx.x; i < 256; i += kTileThreads) v[i / 16 * RP + 16 + i % 16] = 0.f;
-    for (int i = threadIdx.x; i < 256 * NT; i += kTileThreads) {
-        float s = 0.f;
+// The adapters of a lane's rows (e < 0: done or none): the smallest number left in the block, the same in
+// every lane of every wave; -1 if there is none.
+template <int MT>
+__device__ __forceinline__ int next_adapter(const int (&e)[MT]) {
+    unsigned now = ~0u;
 #pragma unroll
-        for (int w = 0; w < kTileWaves; ++w) s += part[w * 256 * NT + i];
-        const int row = i / (16 * NT), q = q0 + i % (16 * NT);
-        v[row * RP + q] = q < r ? s * scale : 0.f;
+    for (int j = 0; j < MT; ++j) now = min(now, (unsigned)e[j]);   // a negative number is a large one
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) now = min(now, (unsigned)__shfl_xor((int)now, d));
+    return max(__builtin_amdgcn_readfirstlane((int)now), -1);
+}
+template <int MT>
+__device__ __forceinline__ void adapters_of(const int32_t *adapter, int row, int T, int n, int (&e)[MT]) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        const int id = adapter[min(row + 16 * j, T - 1)];
+        e[j] = row + 16 * j < T && (unsigned)id < (unsigned)n ? id : -1;
+    }
+}
+
+// Rows row0 .. row0 + count - 1 of a matrix (as many as there are), as a buffer.
+template <typename T>
+__device__ __forceinline__ Buffer rows_of(const void *p, int64_t ld, int row0, int count, int rows, int cols) {
+    return buffer(p ? static_cast<const T *>(p) + row0 * ld : nullptr,
+                  ((size_t)(min(rows - row0, count) - 1) * ld + cols) * sizeof(T));
+}
+
+// v = scale (m w^T) for rows with their own adapters' w: the forward's x and A; the backward's x and A,
+// and d_out and B transposed.
+struct ShrinkJob {
+    const void *m, *w;    // [T x cols]; [n][at least r x cols], w_step elements from one adapter to the next
+    int64_t ld, w_step;
+    float *v;             // [T x vr], zeros from rank r on
+    int cols;
+};
+struct ShrinkArgs {
+    ShrinkJob job[2];
+    const int32_t *adapter;
+    const float *scale;
+    int T, n, r, vr;
+};
+
+// 16 MT rows a workgroup, for each adapter among them: the reduction split over the waves and joined in
+// LDS.  So that a block with several adapters does not end a whole turn after the rest:
+//  - with few blocks, a block's adapters are dealt to the workgroups of blockIdx.y, the first adapter's
+//    behind all others (one without an adapter ends when it has seen the numbers);
+//  - with many blocks (a full grid of such workgroups would cost more than it saves), the first `helpers`
+//    workgroups look through kHelped blocks each and do their second adapters; the others leave those out.
+constexpr int kHelped = 8;
+template <typename TX, typename TW, int NT, int MT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4))) void k_shrink(ShrinkArgs g, int helpers) {
+    constexpr int kPart = 256 * NT * MT;
+    __shared__ __align__(16) float part[WAVES * kPart];
+    const ShrinkJob &job = g.job[blockIdx.z];
+    const Lane l;
+    Shrink<TX, TW, NT, MT, WAVES> x;
+    x.row = l.l16 * (unsigned)job.ld * sizeof(TX);
+    x.step = 16 * (unsigned)job.ld * sizeof(TX);
+    x.cols = job.cols;
+    // the rows of e's adapter `now`, which are taken out of e
+    auto take = [&](int (&e)[MT], int now) {
+        unsigned long long rows = 0;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            rows |= (__ballot(e[j] == now) & 0xFFFFull) << (16 * j);
+            if (e[j] == now) e[j] = -1;
+        }
+        return rows;
+    };
+    auto product = [&](int row0, int now, unsigned long long rows) __attribute__((always_inline)) {
+        int r = g.r;
+        asm volatile("" : "+s"(r));
+        x.m = rows_of<TX>(job.m, job.ld, row0, 16 * MT, g.T, job.cols);
+        x.w = buffer(static_cast<const TW *>(job.w) + now * job.w_step, (size_t)r * job.cols * sizeof(TW));
+        const float scale = g.scale[now];
+        for (int q0 = 0; q0 < g.vr; q0 += 16 * NT) {
+            x.run(l, q0, r, part);
+            __syncthreads();
+            for (int i = threadIdx.x; i < kPart; i += 64 * WAVES) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) s += part[w * kPart + i];
+                const int k = i / (16 * NT), q = q0 + i % (16 * NT);
+                if (q < g.vr && (rows >> k) & 1) job.v[(size_t)(row0 + k) * g.vr + q] = q < r ? s * scale : 0.f;
+            }
+            __syncthreads();
+        }
+    };
+    const int turns = gridDim.y, turn = turns - 1 - blockIdx.y;
+    const bool helper = (int)blockIdx.x < helpers;
+    int row0 = (helper ? blockIdx.x * kHelped : blockIdx.x - helpers) * 16 * MT, e[MT];
+    if (helper) {
+        int ahead[kHelped][MT];
+#pragma unroll
+        for (int i = 0; i < kHelped; ++i) adapters_of(g.adapter, row0 + i * 16 * MT + l.l16, g.T, g.n, ahead[i]);
+#pragma unroll 1
+        for (int i = 0; i < kHelped; ++i, row0 += 16 * MT) {
+            if (row0 >= g.T) return;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                e[j] = ahead[0][j];
+#pragma unroll
+                for (int k = 1; k < kHelped; ++k) e[j] = i == k ? ahead[k][j] : e[j];
+            }
+            take(e, next_adapter(e));
+            const int now = next_adapter(e);
+            if (now >= 0) product(row0, now, take(e, now));
+        }
+        return;
+    }
+    adapters_of(g.adapter, row0 + l.l16, g.T, g.n, e);
+    int seen = 0;
+    for (int now = next_adapter(e); now >= 0; now = next_adapter(e)) {
+        const unsigned long long rows = take(e, now);
+        const int k = seen++;
+        if (helpers ? k == 1 : k % turns != turn) continue;
+        product(row0, now, rows);
     }
 }
 
@@ -301,242 +405,200 @@ __device__ __forceinline__ void join_parts(const float *part, float *v, int q0, 
 // v may exceed, after a power of two per row.
 template <typename TX>
 struct Left {
+    static constexpr int C = Mma<TX>::kChunk;
+    float raw[C];
     typename Mma<TX>::Frag hi, lo;
-};
-template <typename TX>
-__device__ __forceinline__ Left<TX> left_of(const float *v, int exponent) {
-    Left<TX> f;
-    if constexpr (sizeof(TX) == 4) {
-        f.hi = *reinterpret_cast<const f32x4 *>(v);
-        f.lo = f.hi;
-    } else {
+    __device__ __forceinline__ void load(Buffer v, unsigned at) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = std::is_same_v<TX, f16> ? ldexpf(v[i], -exponent) : v[i];
-            TX hi, lo;
-            split(x, hi, lo);
-            f.hi[i] = hi;
-            f.lo[i] = lo;
+        for (int i = 0; i < C; i += 4) {
+            const f32x4 f = __builtin_bit_cast(f32x4, load16(v, at + 4 * i));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) raw[i + k] = f[k];
         }
     }
-    return f;
-}
-
-// The second product: out[row, c] = base[row, c] + sum_q v[row][q] w[c, q] for the columns c0 .. c1.
-// A wave takes every eighth group of 64 columns, a lane 16 of its row's, in pieces of 16 bytes: the
-// four lanes of a row have 64 bytes of it in each piece, which the memory reads and writes faster than
-// 16 bytes here and there.  kTiles: products of 16x16 that make a piece.  kHeld pieces of base are requested
-// ahead (half of it behind the first product's own loads, half behind that product) with the first two
-// groups' weights, the results replace the base in its registers, and all are stored at the end: a load
-// that waits behind a store waits for the store too.
-template <typename TX, typename TW, int kHeld>
-struct Expand {
-    typedef Mma<TX> M;
-    static constexpr int C = M::kChunk, kBlock = 4 * C, V = kVec<TX>, kPieces = 16 / V, kTiles = V / 4;
-    static constexpr int kRing = kHeld / kPieces, kEarly = (kRing + 1) / 2, kStep = kTileWaves * 64;
-    Buffer base, out, w;
-    unsigned base_row, out_row;   // the lane's row, bytes; kNowhere or above: not its turn
-    int c0, c1;                   // c1: at most the columns of w
-    u32x4 held[kRing][kPieces];
-    Chunk<TX, TW> ahead[2][4];
-
-    __device__ __forceinline__ unsigned at(const Lane &l, unsigned row, int g, int p) const {
-        const int c = g + p * 4 * V + l.quad * V;
-        return c < c1 ? row + c * (unsigned)sizeof(TX) : kNowhere;
-    }
-    __device__ __forceinline__ void load_base(const Lane &l, int u, int g) {
+    __device__ __forceinline__ float most(float m) const {
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) held[u][p] = load16(base, at(l, base_row, g, p));
+        for (int i = 0; i < C; ++i) {
+            const float a = fabsf(raw[i]);
+            m = a < __builtin_inff() ? fmaxf(m, a) : m;
+        }
+        return m;
     }
-    __device__ __forceinline__ void load_weights(const Lane &l, Chunk<TX, TW> (&a)[4], int r, int g, int b) const {
+    __device__ __forceinline__ void part(int exponent) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if constexpr (sizeof(TX) == 4) {
+                hi[i] = raw[i];
+            } else {
+                TX a, b;
+                split(std::is_same_v<TX, f16> ? ldexpf(raw[i], -exponent) : raw[i], a, b);
+                hi[i] = a;
+                lo[i] = b;
+            }
+        }
+    }
+};
+
+// out = base + v w^T, w a row's own adapter's: the forward's B, the backward's A transposed.
+struct ExpandArgs {
+    const void *base, *w;   // [T x cols] or null; [n x cols x wr]
+    void *out;
+    const float *v;         // [T x vr]
+    const int32_t *adapter;
+    int64_t ld_base, ld_out;
+    int T, cols, n, wr, vr, groups;   // groups: of 64 columns, that a wave takes
+};
+
+// 16 MT rows and a few groups of 64 columns a wave, without a barrier: bound by reading base and writing
+// out, and by reading w from L2, the less often the more rows; v, split once a wave, is there too.  A lane
+// gets 16 columns of its row in pieces of 16 bytes: the four lanes of a row have 64 bytes of it in each
+// piece.  kTiles: products of 16x16 that make a piece.  For a block with several adapters each one's
+// product is made in turn and the rows keep their own.  Workgroups go to the 8 XCDs in turn by index:
+// those of a block have one index modulo 8, and follow each other there.  KB: blocks of ranks whose operand
+// stays in registers.
+template <typename TX, typename TW, int KB, int MT>
+__global__ __launch_bounds__(kThreads) void k_expand(ExpandArgs g, int col_wgs) {
+    typedef Mma<TX> M;
+    constexpr int C = M::kChunk, kBlock = 4 * C, V = kVec<TX>, kPieces = 16 / V, kTiles = V / 4;
+    const Lane l;
+    const int of = blockIdx.x >> 3, row0 = (of / col_wgs * 8 + (blockIdx.x & 7)) * 16 * MT;
+    if (row0 >= g.T) return;
+    int e[MT];
+    adapters_of(g.adapter, row0 + l.l16, g.T, g.n, e);
+    const Buffer base = rows_of<TX>(g.base, g.ld_base, row0, 16 * MT, g.T, g.cols);
+    const Buffer out = rows_of<TX>(g.out, g.ld_out, row0, 16 * MT, g.T, g.cols);
+    const Buffer v = rows_of<float>(g.v, g.vr, row0, 16 * MT, g.T, g.vr);
+    unsigned base_row[MT], out_row[MT];   // a row behind the last: nowhere
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        const bool in = row0 + 16 * j + l.l16 < g.T;
+        base_row[j] = in ? (16 * j + l.l16) * (unsigned)g.ld_base * sizeof(TX) : kNowhere;
+        out_row[j] = in ? (16 * j + l.l16) * (unsigned)g.ld_out * sizeof(TX) : kNowhere;
+    }
+    const int blocks = (g.vr + kBlock - 1) / kBlock;
+    const int first = next_adapter(e);
+    int todo[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) todo[j] = e[j] == first ? -1 : e[j];
+    const bool several = next_adapter(todo) >= 0;
+
+    auto left_at = [&](int b, int j) {
+        const int q = b * kBlock + l.quad * C;
+        return e[j] >= 0 && q < g.vr ? ((16 * j + l.l16) * g.vr + q) * 4u : kNowhere;   // 0 for a row without an adapter
+    };
+    Left<TX> left[KB][MT];
+    int exponent[MT] = {};
+    if (first >= 0) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) left[b][j].load(v, left_at(b, j));
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            if constexpr (std::is_same_v<TX, f16>) {
+                float most = 0.f;
+#pragma unroll
+                for (int b = 0; b < KB; ++b) most = left[b][j].most(most);
+                for (int b = KB; b < blocks; ++b) {
+                    Left<TX> f;
+                    f.load(v, left_at(b, j));
+                    most = f.most(most);
+                }
+                most = fmaxf(most, __shfl_xor(most, 16));
+                most = fmaxf(most, __shfl_xor(most, 32));
+                if (most > 0.f) frexpf(most, &exponent[j]);
+            }
+#pragma unroll
+            for (int b = 0; b < KB; ++b) left[b][j].part(exponent[j]);
+        }
+    }
+    auto weights = [&](int now) {
+        return buffer(static_cast<const TW *>(g.w) + (size_t)now * g.cols * g.wr, (size_t)g.cols * g.wr * sizeof(TW));
+    };
+    auto load_weights = [&](Chunk<TX, TW> (&a)[4], Buffer w, int c0, int b) __attribute__((always_inline)) {
         const int q = b * kBlock + l.quad * C;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int c = g + t / kTiles * 4 * V + (l.l16 >> 2) * V + 4 * (t % kTiles) + (l.l16 & 3);
-            a[t].load(w, c < c1 && q < r ? ((unsigned)c * r + q) * (unsigned)sizeof(TW) : kNowhere);
+            const int c = c0 + t / kTiles * 4 * V + (l.l16 >> 2) * V + 4 * (t % kTiles) + (l.l16 & 3);
+            a[t].load(w, c < g.cols && q < g.wr ? ((unsigned)c * g.wr + q) * (unsigned)sizeof(TW) : kNowhere);
         }
-    }
-    __device__ __forceinline__ void early(const Lane &lane) {
-        const Lane l = lane.again();
+    };
+    auto multiply = [&](f32x4 (&acc)[4], const Chunk<TX, TW> (&a)[4], const Left<TX> &f) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < kEarly; ++u) load_base(l, u, c0 + l.wave * 64 + u * kStep);
-    }
-    __device__ __forceinline__ void late(const Lane &lane, int r, int g, bool all) {
-        const Lane l = lane.again();
-#pragma unroll
-        for (int u = 0; u < 2 && u < kRing; ++u) load_weights(l, ahead[u], r, g + u * kStep, 0);
-        if (all)
-#pragma unroll
-            for (int u = 0; u < kEarly; ++u) load_base(l, u, g + u * kStep);
-#pragma unroll
-        for (int u = kEarly; u < kRing; ++u) load_base(l, u, g + u * kStep);
-    }
-    // kBlocks: blocks of ranks whose split values stay in registers
-    template <int RP, int kBlocks>
-    __device__ __forceinline__ void run(const Lane &lane, const float *v, int r) {
-        const Lane l = lane.again();
-        const int blocks = (r + kBlock - 1) / kBlock;
-        const float *mine = v + l.l16 * RP + l.quad * C;
-        int exponent = 0;
-        if constexpr (std::is_same_v<TX, f16>) {
-            float most = 0.f;
-            for (int b = 0; b < blocks; ++b)
-#pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    const float a = fabsf(mine[b * kBlock + i]);
-                    most = a < __builtin_inff() ? fmaxf(most, a) : most;
-                }
-            most = fmaxf(most, __shfl_xor(most, 16));
-            most = fmaxf(most, __shfl_xor(most, 32));
-            if (most > 0.f) frexpf(most, &exponent);
+        for (int t = 0; t < 4; ++t) {
+            if constexpr (sizeof(TX) == 2) acc[t] = M::mul(a[t].frag(), f.lo, acc[t]);
+            acc[t] = M::mul(a[t].frag(), f.hi, acc[t]);
         }
-        Left<TX> left[kBlocks];
+    };
+    const int g0 = ((of % col_wgs) * (kThreads / 64) + l.wave) * g.groups, g1 = min(g0 + g.groups, (g.cols + 63) / 64);
+    auto or_nowhere = [](unsigned row, unsigned c) { return (row | c) >= kNowhere ? kNowhere : row + c; };
+    auto column = [&](int k, int p) {
+        const int c = k * 64 + p * 4 * V + l.quad * V;
+        return c < g.cols ? c * (unsigned)sizeof(TX) : kNowhere;
+    };
+    // the products of one adapter's w with every row
+    auto product = [&](f32x4 (&acc)[MT][4], Buffer w, int k) __attribute__((always_inline)) {
+        Chunk<TX, TW> a[KB][4];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) left[b] = left_of<TX>(mine + b * kBlock, exponent);
-        for (int g0 = c0 + l.wave * 64; g0 < c1; g0 += kRing * kStep) {
-            if (g0 != c0 + l.wave * 64) late(l, r, g0, true);
+        for (int b = 0; b < KB; ++b) load_weights(a[b], w, k * 64, b);
 #pragma unroll
-            for (int u = 0; u < kRing; ++u) {
-                const int g = g0 + u * kStep;
-                f32x4 acc[4] = {};
-                auto multiply = [&](const Chunk<TX, TW> (&a)[4], const Left<TX> &f) __attribute__((always_inline)) {
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        if constexpr (sizeof(TX) == 2) acc[t] = M::mul(a[t].frag(), f.lo, acc[t]);
-                        acc[t] = M::mul(a[t].frag(), f.hi, acc[t]);
-                    }
-                };
-                multiply(ahead[u & 1], left[0]);
-                if (u + 2 < kRing) load_weights(lane.again(), ahead[u & 1], r, g + 2 * kStep, 0);
-                if constexpr (kBlocks > 1) {
+            for (int j = 0; j < MT; ++j) multiply(acc[j], a[b], left[b][j]);
+        for (int b = KB; b < blocks; ++b) {
+            Chunk<TX, TW> o[4];
+            load_weights(o, w, k * 64, b);
 #pragma unroll
-                    for (int b = 1; b < kBlocks; ++b)
-                        if (b < blocks) {
-                            Chunk<TX, TW> a[4];
-                            load_weights(l, a, r, g, b);
-                            multiply(a, left[b]);
-                        }
-                    for (int b = kBlocks; b < blocks; ++b) {
-                        Chunk<TX, TW> a[4];
-                        load_weights(l, a, r, g, b);
-                        multiply(a, left_of<TX>(mine + b * kBlock, exponent));
-                    }
-                }
-#pragma unroll
-                for (int p = 0; p < kPieces; ++p) {
-                    float sum[V];
-                    unpack<TX>(__builtin_bit_cast(uint4, held[u][p]), sum);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        float s = acc[(p * V + i) / 4][i % 4];
-                        if constexpr (std::is_same_v<TX, f16>) s = ldexpf(s, exponent);
-                        sum[i] += s;
-                    }
-                    held[u][p] = __builtin_bit_cast(u32x4, pack<TX>(sum));
-                }
-                __builtin_amdgcn_sched_barrier(0);   // one group's products at a time: registers
+            for (int j = 0; j < MT; ++j) {
+                Left<TX> f;
+                f.load(v, left_at(b, j));
+                f.part(exponent[j]);
+                multiply(acc[j], o, f);
             }
-            const Lane o = lane.again();
-#pragma unroll
-            for (int u = 0; u < kRing; ++u)
-#pragma unroll
-                for (int p = 0; p < kPieces; ++p) store16(out, at(o, out_row, g0 + u * kStep, p), held[u][p]);
         }
-    }
-    // base (or zeros) to out
-    __device__ __forceinline__ void pass(const Lane &l) const {
-        for (int g = c0 + l.wave * 64; g < c1; g += kStep)
+    };
+    const Buffer w = weights(max(first, 0));
+    for (int k = g0; k < g1; ++k) {
+        u32x4 held[MT][kPieces];
 #pragma unroll
-            for (int p = 0; p < kPieces; ++p) store16(out, at(l, out_row, g, p), load16(base, at(l, base_row, g, p)));
-    }
-};
-
-// The smallest adapter number left among a block's rows (e < 0: done or none), the same in every
-// lane of every wave; -1 if there is none.
-__device__ __forceinline__ int next_adapter(int e) {
-    unsigned now = (unsigned)e;   // a negative number is a large one
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) now = min(now, (unsigned)__shfl_xor((int)now, d));
-    return max(__builtin_amdgcn_readfirstlane((int)now), -1);
-}
-
-// Rows row0 .. row0 + 15 of a matrix, as a buffer.
-template <typename T>
-__device__ __forceinline__ Buffer rows_of(const void *p, int64_t ld, int row0, int rows, int cols) {
-    return buffer(p ? static_cast<const T *>(p) + row0 * ld : nullptr,
-                  ((size_t)(min(rows - row0, kTileRows) - 1) * ld + cols) * sizeof(T));
-}
-
-// 16 rows a workgroup, for each adapter among them: v = x A^T with the reduction split over the
-// waves and joined in LDS, then out = base + v B^T, the columns split over the waves.  Bound by
-// memory: x and base are read and out written once, the adapters' matrices come from L2.  Several
-// workgroups may share a block of rows, each for its own slice of the columns, with v computed by each;
-// and a block's adapters are dealt to `turns` workgroups, the first adapter's behind all others, so that
-// a block with several of them does not end a whole turn after the rest (a workgroup without an adapter
-// ends when it has seen the numbers).
-// Workgroups go to the 8 XCDs in turn by index: a block's workgroups have one index modulo 8, and follow
-// each other there, so that they share its rows in that XCD's cache.
-// RM: ranks that v has room for.
-template <typename TX, typename TW, int NT, int RM>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4))) void k_adapters_tile(
-    AdapterArgs g, int slice_cols, int slices, int turns) {
-    constexpr int RP = RM + 4;
-    __shared__ __align__(16) float part[kTileWaves * 256 * NT];
-    __shared__ __align__(16) float v[16 * RP];
-    const int of = blockIdx.x >> 3, block = of / slices * 8 + (blockIdx.x & 7), turn = turns - 1 - blockIdx.y;
-    const int row0 = block * kTileRows;
-    if (row0 >= g.T) return;
-    Lane l;
-    const int row = row0 + l.l16;
-    const int id = g.adapter[min(row, g.T - 1)];
-    const bool valid = (unsigned)id < (unsigned)g.n;
-    const bool none = row < g.T && !valid;
-    int e = row < g.T && valid ? id : -1;
-    Shrink<TX, TW, NT> x;
-    Expand<TX, TW, NT == 4 && sizeof(TX) == 2 ? 2 : 4> y;
-    x.m = rows_of<TX>(g.x, g.ld_x, row0, g.T, g.inner);
-    x.row = l.l16 * (unsigned)g.ld_x * sizeof(TX);
-    x.cols = g.inner;
-    y.base = rows_of<TX>(g.base, g.ld_base, row0, g.T, g.outer);
-    y.out = rows_of<TX>(g.out, g.ld_out, row0, g.T, g.outer);
-    y.c0 = of % slices * slice_cols;
-    y.c1 = min(g.outer, y.c0 + slice_cols);
-    const unsigned base_row = l.l16 * (unsigned)g.ld_base * sizeof(TX), out_row = l.l16 * (unsigned)g.ld_out * sizeof(TX);
-    int seen = 0;
-    for (int now = next_adapter(e); now >= 0; now = next_adapter(e)) {
-        const bool mine = e == now;
-        if (mine) e = -1;
-        if (seen++ % turns != turn) continue;
-        int r = g.r;
-        asm volatile("" : "+s"(r));
-        const size_t of_a = (size_t)now * r * g.inner, of_b = (size_t)now * r * g.outer;
-        x.w = buffer(static_cast<const TW *>(g.a) + of_a, (size_t)r * g.inner * sizeof(TW));
-        y.w = buffer(static_cast<const TW *>(g.b) + of_b, (size_t)r * g.outer * sizeof(TW));
-        y.base_row = mine ? base_row : kNowhere;
-        y.out_row = mine ? out_row : kNowhere;
-        const float scale = g.scale[now];
-        const int g0 = y.c0 + l.wave * 64;
-        x.run(l, 0, r, part, [&]() __attribute__((always_inline)) { y.early(l); });
-        __builtin_amdgcn_sched_barrier(0);
-        if (RM <= 16 * NT || NT == 1) y.late(l, r, g0, false);
-        __syncthreads();
-        join_parts<NT, RP>(part, v, 0, r, scale);
-        if constexpr (RM > 64) {
-            for (int q0 = 16 * NT; q0 < r; q0 += 16 * NT) {
-                __syncthreads();
-                x.run(l, q0, r, part, []() __attribute__((always_inline)) {});
-                __syncthreads();
-                join_parts<NT, RP>(part, v, q0, r, scale);
+            for (int p = 0; p < kPieces; ++p) held[j][p] = load16(base, or_nowhere(base_row[j], column(k, p)));
+        f32x4 res[MT][4] = {};
+        if (first >= 0) {
+            product(res, w, k);
+            if (several) {
+                int left_over[MT];
+#pragma unroll
+                for (int j = 0; j < MT; ++j) left_over[j] = todo[j];
+                for (int now = next_adapter(left_over); now >= 0; now = next_adapter(left_over)) {
+                    f32x4 acc[MT][4] = {};
+                    product(acc, weights(now), k);
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) res[j][t][i] = e[j] == now ? acc[j][t][i] : res[j][t][i];
+                        if (left_over[j] == now) left_over[j] = -1;
+                    }
+                }
             }
-            y.late(l, r, g0, false);
         }
-        __syncthreads();
-        y.template run<RP, (RM >= 64 ? 64 : 32) / (4 * Mma<TX>::kChunk)>(l, v, r);
-    }
-    if (turn == 0 && __ballot(none) && !(g.base == g.out && g.ld_base == g.ld_out)) {
-        y.base_row = none ? base_row : kNowhere;
-        y.out_row = none ? out_row : kNowhere;
-        y.pass(l);
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                float sum[V];
+                unpack<TX>(__builtin_bit_cast(uint4, held[j][p]), sum);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float s = res[j][(p * V + i) / 4][i % 4];
+                    if constexpr (std::is_same_v<TX, f16>) s = ldexpf(s, exponent[j]);
+                    sum[i] += e[j] >= 0 ? s : 0.f;
+                }
+                store16(out, or_nowhere(out_row[j], column(k, p)), __builtin_bit_cast(u32x4, pack<TX>(sum)));
+            }
     }
 }
 
@@ -631,8 +693,9 @@ __global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW 
     const int c0 = (is_b ? blockIdx.x - tiles_a : blockIdx.x) * 64;
     const int cols = is_b ? outer : inner, padded = is_b ? op : ip;
     const size_t ea = (size_t)e * r * inner, eb = (size_t)e * r * outer;
-    for (int i = threadIdx.x; i < 32 * 64; i += kThreads) {
-        const int q = is_b ? i % 32 : i / 64, c = is_b ? i / 32 : i % 64;
+#pragma unroll
+    for (int k = 0; k < 32 * 64 / kThreads; ++k) {
+        const int i = threadIdx.x + k * kThreads, q = is_b ? i % 32 : i / 64, c = is_b ? i / 32 : i % 64;
         TW v = narrow<TW>(0.f);
         if (q0 + q < r && c0 + c < cols)
             v = is_b ? b[eb + (size_t)(c0 + c) * r + q0 + q] : a[ea + (size_t)(q0 + q) * inner + c0 + c];
@@ -640,8 +703,9 @@ __global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW 
         if (!is_b && ap && q0 + q < r && c0 + c < padded) ap[((size_t)e * r + q0 + q) * ip + c0 + c] = v;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 32 * 64; i += kThreads) {
-        const int q = is_b ? i / 64 : i % 32, c = is_b ? i % 64 : i / 32;
+#pragma unroll
+    for (int k = 0; k < 32 * 64 / kThreads; ++k) {
+        const int i = threadIdx.x + k * kThreads, q = is_b ? i / 64 : i % 32, c = is_b ? i % 64 : i / 32;
         if (q0 + q >= rp || c0 + c >= padded) continue;
         if (is_b)
             bt[((size_t)e * rp + q0 + q) * op + c0 + c] = tile[q][c];
@@ -659,7 +723,7 @@ struct Reshape {
     int cols_from[3], cols_to[3];
 };
 template <typename TX>
-__global__ __launch_bounds__(kThreads) void k_back_reshape(Reshape g, int rows) {
+__global__ __launch_bounds__(kThreads) void k_reshape(Reshape g, int rows) {
     const int m = blockIdx.y;
     for (int row = blockIdx.x * 4 + ((int)threadIdx.x >> 6); row < rows; row += gridDim.x * 4) {
         const TX *from = static_cast<const TX *>(g.from[m]) + row * g.ld_from[m];
@@ -668,100 +732,6 @@ __global__ __launch_bounds__(kThreads) void k_back_reshape(Reshape g, int rows) 
             const uint4 v = g.from[m] && c < g.cols_from[m] ? load_piece(from + c, g.cols_from[m] - c) : uint4{0, 0, 0, 0};
             store_piece(to + c, v, g.cols_to[m] - c);
         }
-    }
-}
-
-// What the block kernels of a backward call read and write: as AdapterBackArgs, or padded copies.
-struct BackBlocks {
-    const void *x, *d_out, *dx_base;
-    void *d_x;
-    int64_t ld_x, ld_d_out, ld_dx_base, ld_d_x;
-    const void *a, *at, *bt;          // [n x r x ip], [n x ip x rp], [n x rp x op]
-    const int32_t *adapter;
-    const float *scale;
-    float *v, *u;                     // [T x r]: scale * (A x), scale * (B^T d_out)
-    int T, ip, op, n, r, rp;
-};
-
-// d_x = dx_base + u A of 16 rows a workgroup, and u; built as k_adapters_tile.  v is the work of one more
-// workgroup a block (the last slice), which shares nothing with the others but the adapters' numbers.
-template <typename TX, typename TW, int NT, int RM>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(std::is_same_v<TX, f16> && NT == 4 ? 2 : 4))) void k_back_tile(
-    BackBlocks g, int slice_cols, int slices, int turns) {
-    constexpr int RP = RM + 4;
-    __shared__ __align__(16) float part[kTileWaves * 256 * NT];
-    __shared__ __align__(16) float u[16 * RP];
-    const int of = blockIdx.x >> 3, block = of / (slices + 1) * 8 + (blockIdx.x & 7), turn = turns - 1 - blockIdx.y;
-    const int row0 = block * kTileRows, slice = of % (slices + 1);
-    if (row0 >= g.T) return;
-    Lane l;
-    const int row = row0 + l.l16;
-    const int id = g.adapter[min(row, g.T - 1)];
-    const bool valid = (unsigned)id < (unsigned)g.n;
-    const bool none = row < g.T && !valid;
-    int e = row < g.T && valid ? id : -1;
-    Shrink<TX, TW, NT> x, dy;
-    Expand<TX, TW, sizeof(TX) == 2 ? 2 : 4> y;
-    x.m = rows_of<TX>(g.x, g.ld_x, row0, g.T, g.ip);
-    x.row = l.l16 * (unsigned)g.ld_x * sizeof(TX);
-    x.cols = g.ip;
-    dy.m = rows_of<TX>(g.d_out, g.ld_d_out, row0, g.T, g.op);
-    dy.row = l.l16 * (unsigned)g.ld_d_out * sizeof(TX);
-    dy.cols = g.op;
-    y.base = rows_of<TX>(g.dx_base, g.ld_dx_base, row0, g.T, g.ip);
-    y.out = rows_of<TX>(g.d_x, g.ld_d_x, row0, g.T, g.ip);
-    y.c0 = slice * slice_cols;
-    y.c1 = min(g.ip, y.c0 + slice_cols);
-    const unsigned base_row = l.l16 * (unsigned)g.ld_dx_base * sizeof(TX), out_row = l.l16 * (unsigned)g.ld_d_x * sizeof(TX);
-    int seen = 0;
-    for (int now = next_adapter(e); now >= 0; now = next_adapter(e)) {
-        const bool mine = e == now;
-        if (mine) e = -1;
-        if (seen++ % turns != turn) continue;
-        const unsigned rows = (unsigned)__ballot(mine) & 0xFFFFu;
-        int r = g.r;
-        asm volatile("" : "+s"(r));
-        x.w = buffer(static_cast<const TW *>(g.a) + (size_t)now * r * g.ip, (size_t)r * g.ip * sizeof(TW));
-        dy.w = buffer(static_cast<const TW *>(g.bt) + (size_t)now * g.rp * g.op, (size_t)g.rp * g.op * sizeof(TW));
-        y.w = buffer(static_cast<const TW *>(g.at) + (size_t)now * g.rp * g.ip, (size_t)g.rp * g.ip * sizeof(TW));
-        y.base_row = mine ? base_row : kNowhere;
-        y.out_row = mine ? out_row : kNowhere;
-        const float scale = g.scale[now];
-        const int g0 = y.c0 + l.wave * 64;
-        auto keep = [&](float *to) __attribute__((always_inline)) {
-            for (int i = threadIdx.x; i < 16 * r; i += kTileThreads) {
-                const int k = i / r, q = i - k * r;
-                if ((rows >> k) & 1) to[(size_t)(row0 + k) * r + q] = u[k * RP + q];
-            }
-        };
-        if (slice == slices) {
-            for (int q0 = 0; q0 < r; q0 += 16 * NT) {
-                x.run(l, q0, r, part, []() __attribute__((always_inline)) {});
-                __syncthreads();
-                join_parts<NT, RP>(part, u, q0, r, scale);
-                __syncthreads();
-            }
-            keep(g.v);
-            __syncthreads();
-            continue;
-        }
-        for (int q0 = 0; q0 < r; q0 += 16 * NT) {
-            if (q0) __syncthreads();
-            dy.run(l, q0, r, part, []() __attribute__((always_inline)) {});
-            __syncthreads();
-            join_parts<NT, RP>(part, u, q0, r, scale);
-        }
-        y.early(l);
-        y.late(l, g.rp, g0, false);
-        __syncthreads();
-        if (slice == 0) keep(g.u);
-        y.template run<RP, (RM >= 64 ? 64 : 32) / (4 * Mma<TX>::kChunk)>(l, u, g.rp);
-        __syncthreads();
-    }
-    if (turn == 0 && slice < slices && __ballot(none) && !(g.dx_base == g.d_x && g.ld_dx_base == g.ld_d_x)) {
-        y.base_row = none ? base_row : kNowhere;
-        y.out_row = none ? out_row : kNowhere;
-        y.pass(l);
     }
 }
 
@@ -822,7 +792,7 @@ struct BackWeights {
     const float *v, *u;
     float *partial;      // [piece][r][ip + op]
     float *d_a, *d_b;
-    int T, inner, outer, ip, op, n, r, piece_rows;
+    int T, inner, outer, ip, op, n, r, vr, piece_rows;
 };
 
 __device__ __forceinline__ void store_grad(const BackWeights &g, int e, bool is_b, int q, int c, float s) {
@@ -891,7 +861,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NT == 
 #pragma unroll
             for (int h = 0; h < kLoads; ++h) x[j][h] = load_piece(m + row * ld + at[h], kVec<TX>);
 #pragma unroll
-            for (int k = 0; k < NT; ++k) f[k][j] = left[(size_t)row * g.r + rank[k]];
+            for (int k = 0; k < NT; ++k) f[k][j] = left[(size_t)row * g.vr + rank[k]];
         }
         if (b + 32 > p.end) {
 #pragma unroll
@@ -995,6 +965,7 @@ __global__ __launch_bounds__(kThreads) void k_back_join(BackWeights g) {
     const int c = is_b ? c0 - g.inner : c0;
     const size_t width = g.ip + g.op, at = (is_b ? g.ip : 0) + c;
     float s = 0.f;
+#pragma unroll 4
     for (int p = 0; p < count; ++p) s += g.partial[((size_t)(first + p) * g.r + q) * width + at];
     store_grad(g, e, is_b, q, c, s);
 }
@@ -1026,8 +997,8 @@ BackSpace back_space(int T, int inner, int outer, int n, int r) {
     s.offsets = take((adapters + 1) * 4);
     s.order = take(row * 4);
     s.sort = take(dispatch_workspace(T, 1, n));
-    s.v = take(row * r * 4);
-    s.u = take(row * r * 4);
+    s.v = take(row * s.rp * 4);
+    s.u = take(row * s.rp * 4);
     s.at = take(adapters * s.ip * s.rp * 4);
     s.bt = take(adapters * s.op * s.rp * 4);
     s.partial = take((size_t)s.max_pieces * r * (s.ip + s.op) * 4);
@@ -1039,53 +1010,95 @@ BackSpace back_space(int T, int inner, int outer, int n, int r) {
     return s;
 }
 
-template <typename TX, typename TW, int NT, int RM>
-hipError_t forward_tile(const AdapterArgs &g, hipStream_t stream) {
-    const int tiles = (g.T + kTileRows - 1) / kTileRows;
-    const int groups = (g.outer + 63) / 64;
-    const int slices = std::max(1, std::min(groups / kTileWaves, 512 / tiles));
-    const int cols = (groups + slices - 1) / slices * 64, used = (g.outer + cols - 1) / cols;
-    const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / (tiles * slices))));
-    return launch(k_adapters_tile<TX, TW, NT, RM>, dim3((tiles + 7) / 8 * 8 * used, turns), dim3(kTileThreads), stream,
-                  nullptr, nullptr, g, cols, used, turns);
+// A forward call of blocks holds v and, where the rank is no multiple of 8, b with its rows padded.
+struct ForwardSpace {
+    int rp;
+    size_t v, b, bytes;
+};
+ForwardSpace forward_space(int T, int outer, int n, int r) {
+    ForwardSpace s{};
+    if (T <= kRowCalls) return s;
+    s.rp = (r + 7) / 8 * 8;
+    s.b = ((size_t)T * s.rp * 4 + 255) & ~(size_t)255;
+    s.bytes = s.b + (s.rp == r ? 0 : (size_t)n * outer * s.rp * 4);
+    return s;
 }
 
-// Whether a matrix can be read by the block kernels: rows of whole, aligned 16-byte pieces, sixteen of
+// Whether a matrix can be read by the block kernels: rows of whole, aligned 16-byte pieces, a block of
 // them within a buffer.
 bool piecewise(const void *p, int64_t ld, int cols, size_t size) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && cols * size % 16 == 0 &&
-           (15 * ld + cols) * (int64_t)size < kBufferBytes;
+           ((kMostRows - 1) * ld + cols) * (int64_t)size < kBufferBytes;
 }
-bool piecewise_adapters(const void *a, const void *b, int inner, int outer, int r, int chunk, size_t size) {
-    return (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) % (chunk * size) == 0 && r % chunk == 0 &&
-           inner % chunk == 0 && outer % chunk == 0 && (int64_t)r * std::max(inner, outer) * (int64_t)size < kBufferBytes;
+// Whether an adapter's matrices, their ranks padded to rp, fit a buffer, and its rows are whole pieces.
+bool piecewise_adapter(const void *a, int64_t inner, int64_t outer, int64_t rp, size_t size) {
+    return reinterpret_cast<uintptr_t>(a) % 16 == 0 && inner % 8 == 0 && outer % 8 == 0 &&
+           rp * std::max(inner, outer) * (int64_t)size < kBufferBytes;
+}
+
+template <typename TX, typename TW, int MT, int WAVES>
+hipError_t shrink(const ShrinkArgs &g, int jobs, hipStream_t stream) {
+    const int tiles = (g.T + 16 * MT - 1) / (16 * MT);
+    const bool many = tiles >= 256 && g.n > 1;
+    const int helpers = many ? (tiles + kHelped - 1) / kHelped : 0;
+    const int turns = many ? 1 : std::min(g.n, std::max(2, std::min(16, 1024 / tiles)));
+    const dim3 grid(helpers + tiles, turns, jobs), block(64 * WAVES);
+    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, WAVES>, grid, block, stream, nullptr, nullptr, g, helpers);
+    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, WAVES>, grid, block, stream, nullptr, nullptr, g, helpers);
+    return launch(k_shrink<TX, TW, 4, MT, WAVES>, grid, block, stream, nullptr, nullptr, g, helpers);
+}
+
+template <typename TX, typename TW, int MT>
+hipError_t expand(ExpandArgs g, hipStream_t stream) {
+    const int tiles = (g.T + 16 * MT - 1) / (16 * MT), groups = (g.cols + 63) / 64;
+    // a wave takes more groups (v is read and split once) as long as there are 16 waves a CU
+    g.groups = (int)std::max<int64_t>(1, std::min<int64_t>(8, (int64_t)tiles * groups / 4096));
+    const int col_wgs = (groups + 4 * g.groups - 1) / (4 * g.groups);
+    const dim3 grid((tiles + 7) / 8 * 8 * col_wgs), block(kThreads);
+    constexpr int kBlock = 4 * Mma<TX>::kChunk;
+    if (g.wr <= kBlock) return launch(k_expand<TX, TW, 1, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
+    if constexpr (kBlock < 32)
+        if (g.wr > 2 * kBlock) return launch(k_expand<TX, TW, 4, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
+    return launch(k_expand<TX, TW, 2, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
+}
+
+// Both products of a call.  A block of 32 rows instead of 16 halves the reads of the adapters' matrices
+// from L2, and the number of workgroups: worth it from rank 17 (shrink) on, with enough rows.
+template <typename TX, typename TW>
+hipError_t products(const ShrinkArgs &sa, int jobs, const ExpandArgs &ea, hipStream_t stream) {
+    const bool tall = sa.r > 16 && sa.T >= kTallRows;
+    const hipError_t err = !tall          ? shrink<TX, TW, 1, 8>(sa, jobs, stream)
+                           : sa.r <= 32 ? shrink<TX, TW, 2, 8>(sa, jobs, stream)
+                                        : shrink<TX, TW, 2, 16>(sa, jobs, stream);
+    if (err != hipSuccess) return err;
+    return tall ? expand<TX, TW, 2>(ea, stream) : expand<TX, TW, 1>(ea, stream);
 }
 
 template <typename TX, typename TW>
-hipError_t forward(const AdapterArgs &g, hipStream_t stream) {
+hipError_t forward(const AdapterArgs &g, void *workspace, hipStream_t stream) {
     constexpr size_t z = sizeof(TX);
-    if (g.T > kRowCalls && piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.out, g.ld_out, g.outer, z) &&
-        (!g.base || piecewise(g.base, g.ld_base, g.outer, z)) &&
-        piecewise_adapters(g.a, g.b, g.inner, g.outer, g.r, Mma<TX>::kChunk, sizeof(TW))) {
-        if (g.r <= 16) return forward_tile<TX, TW, 1, 32>(g, stream);
-        if (g.r <= 32) return forward_tile<TX, TW, 2, 32>(g, stream);
-        if (g.r <= 64) return forward_tile<TX, TW, 4, 64>(g, stream);
-        return forward_tile<TX, TW, 4, kMaxRank>(g, stream);
+    const ForwardSpace s = forward_space(g.T, g.outer, g.n, g.r);
+    if (s.bytes && piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.out, g.ld_out, g.outer, z) &&
+        (!g.base || piecewise(g.base, g.ld_base, g.outer, z)) && reinterpret_cast<uintptr_t>(g.b) % 16 == 0 &&
+        piecewise_adapter(g.a, g.inner, g.outer, s.rp, sizeof(TW))) {
+        float *v = reinterpret_cast<float *>(static_cast<char *>(workspace) + s.v);
+        const void *b = g.b;
+        hipError_t err = hipSuccess;
+        if (s.rp != g.r) {
+            Reshape m{{g.b}, {static_cast<char *>(workspace) + s.b}, {g.r}, {s.rp}, {g.r}, {s.rp}};
+            b = m.to[0];
+            const int rows = g.n * g.outer;
+            err = launch(k_reshape<TW>, dim3(std::min((rows + 3) / 4, 2048), 1), dim3(kThreads), stream, nullptr, nullptr,
+                         m, rows);
+        }
+        const ShrinkArgs sa{{{g.x, g.a, g.ld_x, (int64_t)g.r * g.inner, v, g.inner}}, g.adapter, g.scale, g.T, g.n, g.r, s.rp};
+        const ExpandArgs ea{g.base, b, g.out, v, g.adapter, g.ld_base, g.ld_out, g.T, g.outer, g.n, s.rp, s.rp, 0};
+        return err == hipSuccess ? products<TX, TW>(sa, 1, ea, stream) : err;
     }
     const int groups = (g.outer + kThreads - 1) / kThreads;
     const int slices = std::max(1, std::min(groups, kRowTarget / g.T)), cols = (groups + slices - 1) / slices * kThreads;
     return launch(k_adapters_row<TX, TW>, dim3(g.T, (g.outer + cols - 1) / cols), dim3(kThreads), stream, nullptr, nullptr,
                   g, cols);
-}
-
-template <typename TX, typename TW, int NT, int RM>
-hipError_t back_tile(const BackBlocks &g, hipStream_t stream) {
-    const int tiles = (g.T + kTileRows - 1) / kTileRows, groups = (g.ip + 63) / 64;
-    const int slices = std::max(1, std::min(groups / kTileWaves, 512 / tiles));
-    const int cols = (groups + slices - 1) / slices * 64, used = (g.ip + cols - 1) / cols;
-    const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / (tiles * slices))));
-    return launch(k_back_tile<TX, TW, NT, RM>, dim3((tiles + 7) / 8 * 8 * (used + 1), turns), dim3(kTileThreads),
-                  stream, nullptr, nullptr, g, cols, used, turns);
 }
 
 template <typename TX, typename TW>
@@ -1096,10 +1109,9 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
     float *v = reinterpret_cast<float *>(ws + s.v), *u = reinterpret_cast<float *>(ws + s.u);
     constexpr size_t z = sizeof(TX);
     const bool blocks =
-        g.T > 0 && (int64_t)s.rp * std::max(s.ip, s.op) * (int64_t)sizeof(TW) < kBufferBytes &&
-        (15 + 1) * (int64_t)std::max(s.ip, s.op) * (int64_t)z < kBufferBytes &&
+        g.T > 0 && piecewise_adapter(s.padded ? workspace : g.a, s.ip, s.op, s.rp, sizeof(TW)) &&
         (s.padded || (piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.d_out, g.ld_d_out, g.outer, z) &&
-                      piecewise(g.d_x, g.ld_d_x, g.inner, z) && reinterpret_cast<uintptr_t>(g.a) % 16 == 0 &&
+                      piecewise(g.d_x, g.ld_d_x, g.inner, z) &&
                       (!g.dx_base || piecewise(g.dx_base, g.ld_dx_base, g.inner, z))));
     const bool small = blocks && g.T <= kSmallBack;
     hipError_t err = hipSuccess;
@@ -1130,33 +1142,34 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
                  nullptr, nullptr, static_cast<const TW *>(g.a), static_cast<const TW *>(g.b), at, bt, ap, g.inner, g.outer,
                  s.ip, s.op, g.r, s.rp);
     if (err != hipSuccess) return err;
-    BackBlocks b{g.x, g.d_out, g.dx_base, g.d_x, g.ld_x, g.ld_d_out, g.ld_dx_base, g.ld_d_x, g.a, at, bt,
-                 g.adapter, g.scale, v, u, g.T, s.ip, s.op, g.n, g.r, s.rp};
+    // what the block kernels read and write: the caller's matrices, or padded copies
+    const void *x = g.x, *d_out = g.d_out, *dx_base = g.dx_base, *am = g.a;
+    void *d_x = g.d_x;
+    int64_t ld_x = g.ld_x, ld_d_out = g.ld_d_out, ld_dx_base = g.ld_dx_base, ld_d_x = g.ld_d_x;
     const int copies = std::min((g.T + 3) / 4, 2048);
     if (s.padded) {
         Reshape m{{g.x, g.d_out, g.dx_base}, {ws + s.x, ws + s.d_out, ws + s.d_x}, {g.ld_x, g.ld_d_out, g.ld_dx_base},
                   {s.ip, s.op, s.ip}, {g.inner, g.outer, g.inner}, {s.ip, s.op, s.ip}};
-        err = launch(k_back_reshape<TX>, dim3(copies, 3), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
+        err = launch(k_reshape<TX>, dim3(copies, 3), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
         if (err != hipSuccess) return err;
-        b.x = ws + s.x;
-        b.d_out = ws + s.d_out;
-        b.dx_base = b.d_x = ws + s.d_x;
-        b.ld_x = b.ld_dx_base = b.ld_d_x = s.ip;
-        b.ld_d_out = s.op;
-        b.a = ap;
+        x = ws + s.x;
+        d_out = ws + s.d_out;
+        dx_base = d_x = ws + s.d_x;
+        ld_x = ld_dx_base = ld_d_x = s.ip;
+        ld_d_out = s.op;
+        am = ap;
     }
-    err = g.r <= 16   ? back_tile<TX, TW, 1, 32>(b, stream)
-          : g.r <= 32 ? back_tile<TX, TW, 2, 32>(b, stream)
-          : g.r <= 64 ? back_tile<TX, TW, 4, 64>(b, stream)
-                      : back_tile<TX, TW, 4, kMaxRank>(b, stream);
+    const ShrinkArgs sa{{{x, am, ld_x, (int64_t)g.r * s.ip, v, s.ip}, {d_out, bt, ld_d_out, (int64_t)s.rp * s.op, u, s.op}},
+                        g.adapter, g.scale, g.T, g.n, g.r, s.rp};
+    err = products<TX, TW>(sa, 2, {dx_base, at, d_x, u, g.adapter, ld_dx_base, ld_d_x, g.T, s.ip, g.n, s.rp, s.rp, 0}, stream);
     if (err != hipSuccess) return err;
     if (s.padded) {
-        Reshape m{{b.d_x}, {g.d_x}, {s.ip}, {g.ld_d_x}, {g.inner}, {g.inner}};
-        err = launch(k_back_reshape<TX>, dim3(copies, 1), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
+        Reshape m{{d_x}, {g.d_x}, {s.ip}, {g.ld_d_x}, {g.inner}, {g.inner}};
+        err = launch(k_reshape<TX>, dim3(copies, 1), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
         if (err != hipSuccess) return err;
     }
-    const BackWeights w{g.adapter, b.x, b.d_out, b.ld_x, b.ld_d_out, offsets, order, v, u, reinterpret_cast<float *>(ws + s.partial),
-                        g.d_a, g.d_b, g.T, g.inner, g.outer, s.ip, s.op, g.n, g.r, s.piece_rows};
+    const BackWeights w{g.adapter, x, d_out, ld_x, ld_d_out, offsets, order, v, u, reinterpret_cast<float *>(ws + s.partial),
+                        g.d_a, g.d_b, g.T, g.inner, g.outer, s.ip, s.op, g.n, g.r, s.rp, s.piece_rows};
     const int nt = g.r <= 16 ? 1 : g.r <= 32 ? 2 : 4;
     const dim3 grid((s.ip + kPieceCols - 1) / kPieceCols + (s.op + kPieceCols - 1) / kPieceCols, small ? g.n : s.max_pieces,
                     (g.r + 16 * nt - 1) / (16 * nt));
@@ -1175,15 +1188,16 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
 
 }  // namespace
 
+size_t adapters_forward_workspace(int T, int outer, int n, int r) { return forward_space(T, outer, n, r).bytes; }
 size_t adapters_workspace(int T, int inner, int outer, int n, int r) { return back_space(T, inner, outer, n, r).bytes; }
 
-hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &g, hipStream_t stream) {
+hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &g, void *workspace, hipStream_t stream) {
     if (g.T == 0) return hipSuccess;
-    if (dtype == T_F16) return forward<f16, f16>(g, stream);
-    if (dtype == T_BF16) return forward<bf16, bf16>(g, stream);
-    if (wtype == T_F16) return forward<float, f16>(g, stream);
-    if (wtype == T_BF16) return forward<float, bf16>(g, stream);
-    return forward<float, float>(g, stream);
+    if (dtype == T_F16) return forward<f16, f16>(g, workspace, stream);
+    if (dtype == T_BF16) return forward<bf16, bf16>(g, workspace, stream);
+    if (wtype == T_F16) return forward<float, f16>(g, workspace, stream);
+    if (wtype == T_BF16) return forward<float, bf16>(g, workspace, stream);
+    return forward<float, float>(g, workspace, stream);
 }
 
 hipError_t launch_adapters_back(int dtype, int wtype, const AdapterBackArgs &g, void *workspace, hipStream_t stream) {

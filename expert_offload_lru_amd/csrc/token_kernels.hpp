@@ -54,7 +54,8 @@ struct AdapterArgs {
     const float *scale;
     int T, inner, outer, n, r;
 };
-hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &a, hipStream_t stream);
+size_t adapters_forward_workspace(int T, int outer, int n, int r);
+hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &a, void *workspace, hipStream_t stream);
 
 struct AdapterBackArgs {
     const void *d_out, *x, *dx_base;

@@ -193,9 +193,15 @@ int moe_tokens_combine_backward(const void *d_out, int64_t ld_d_out, const void 
     return finish(launch_combine_back(dtype, a, static_cast<hipStream_t>(stream)));
 }
 
+size_t moe_adapters_forward_workspace(int n_rows, int inner, int outer, int n_adapters, int rank) {
+    if (check_adapters(MOE_T_F32, MOE_T_F32, n_rows, inner, outer, n_adapters, rank) != MOE_OK) return 0;
+    return adapters_forward_workspace(n_rows, outer, n_adapters, rank);
+}
+
 int moe_adapters_forward(const void *x, int64_t ld_x, const void *base, int64_t ld_base, int dtype, int n_rows, int inner,
                          int outer, const int32_t *adapter, const void *a, const void *b, int wtype, const float *scale,
-                         int n_adapters, int rank, void *out, int64_t ld_out, void *stream) {
+                         int n_adapters, int rank, void *out, int64_t ld_out, void *workspace, size_t workspace_bytes,
+                         void *stream) {
     MOE_TRY(check_adapters(dtype, wtype, n_rows, inner, outer, n_adapters, rank));
     if (n_rows == 0) return MOE_OK;
     if (!x || !adapter || !a || !b || !scale || !out) return invalid("a tensor is NULL");
@@ -204,13 +210,16 @@ int moe_adapters_forward(const void *x, int64_t ld_x, const void *base, int64_t 
     MOE_TRY(check_ld("out", out, ld_out, outer));
     const size_t z = elem_size(dtype), zw = elem_size(wtype);
     const bool in_place = base == out && ld_base == ld_out;
-    MOE_TRY(check_overlap({matrix("out", out, n_rows, outer, ld_out, z)},
+    const size_t need = adapters_forward_workspace(n_rows, outer, n_adapters, rank);
+    if (need && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16))
+        return invalid("the workspace is too small or not aligned");
+    MOE_TRY(check_overlap({matrix("out", out, n_rows, outer, ld_out, z), array("workspace", workspace, need, 1)},
                           {matrix("x", x, n_rows, inner, ld_x, z),
                            matrix("base", in_place ? nullptr : base, n_rows, outer, ld_base, z),
                            array("adapter", adapter, n_rows), array("a", a, (int64_t)n_adapters * rank * inner, zw),
                            array("b", b, (int64_t)n_adapters * rank * outer, zw), array("scale", scale, n_adapters)}));
     AdapterArgs g{x, base, out, ld_x, ld_base, ld_out, adapter, a, b, scale, n_rows, inner, outer, n_adapters, rank};
-    return finish(launch_adapters(dtype, wtype, g, static_cast<hipStream_t>(stream)));
+    return finish(launch_adapters(dtype, wtype, g, workspace, static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_adapters_workspace(int n_rows, int inner, int outer, int n_adapters, int rank) {

@@ -169,13 +169,15 @@ def _adapter_shapes(a, b, gpu):
             _type("a", a)[0])
 
 
-def adapters_forward(x, adapter, a, b, scale, out, base=None, stream=None):
+def adapters_forward(x, adapter, a, b, scale, out, base=None, workspace=None, stream=None):
     """out[i] = base[i] + scale[e] B_e (A_e x[i]) with e = adapter[i] (moe_adapters_forward).
 
     x [T, inner], adapter int32 [T] (-1: none), a [n, r, inner], b [n, outer, r], scale fp32 [n], out
     and base [T, outer]; base may be out, and None stands for zeros.  a and b have x's type, or any
-    type beside fp32 activations.
+    type beside fp32 activations.  A call of many rows needs a workspace: the caller's (any contiguous
+    tensor of enough bytes, 16-byte aligned) or one of its own.
     """
+    lib = gpu_lib()
     (dtype, gpu), T = _type("x", x), _dims("x", x, 2)[0]
     n, r, inner, outer, pa, pb, wtype = _adapter_shapes(a, b, gpu)
     px, ldx = _matrix("x", x, T, inner, x.dtype, gpu)
@@ -183,8 +185,10 @@ def adapters_forward(x, adapter, a, b, scale, out, base=None, stream=None):
     p_base, ldb = (None, outer) if base is None else _matrix("base", base, T, outer, x.dtype, gpu)
     p_ad = _array("adapter", adapter, (T,), torch.int32, gpu)
     p_scale = _array("scale", scale, (n,), torch.float32, gpu)
-    _call(gpu_lib().moe_adapters_forward, gpu, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
-          wtype, p_scale, n, r, po, ldo)
+    need = lib.moe_adapters_forward_workspace(T, inner, outer, n, r)
+    ws = _workspace(need, workspace, gpu, stream) if need else None
+    _call(lib.moe_adapters_forward, gpu, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb, wtype,
+          p_scale, n, r, po, ldo, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
 
 
 def adapters_backward(d_out, x, adapter, a, b, scale, d_x, d_a, d_b, dx_base=None, workspace=None, stream=None):

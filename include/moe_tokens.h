@@ -82,10 +82,13 @@ int moe_tokens_combine_backward(const void *d_out, int64_t ld_d_out, const void 
  * Types: wtype = dtype, or dtype MOE_T_F32 with any wtype (the layer's own activations are fp32).
  * No row's values enter another row's result.  Rows of one adapter next to each other (a
  * request's prompt; rows in the order of moe_tokens_dispatch) share its matrices' reads; other orders
- * are as right, only slower.  Limits: rank <= 256; n_rows, inner and outer below 2^24. */
+ * are as right, only slower.  workspace: moe_adapters_forward_workspace bytes (NULL if that is 0, as it
+ * is for few rows), 16-byte aligned.  Limits: rank <= 256; n_rows, inner and outer below 2^24. */
+size_t moe_adapters_forward_workspace(int n_rows, int inner, int outer, int n_adapters, int rank);
 int moe_adapters_forward(const void *x, int64_t ld_x, const void *base, int64_t ld_base, int dtype, int n_rows,
                          int inner, int outer, const int32_t *adapter, const void *a, const void *b, int wtype,
-                         const float *scale, int n_adapters, int rank, void *out, int64_t ld_out, void *stream);
+                         const float *scale, int n_adapters, int rank, void *out, int64_t ld_out, void *workspace,
+                         size_t workspace_bytes, void *stream);
 
 /* Its gradients.  With v = A_e x[i], u = scale[e] * B_e^T d_out[i]:
  *   d_x[i] = dx_base[i] + A_e^T u        (dx_base, the projection's own d_x, may be NULL: zeros)

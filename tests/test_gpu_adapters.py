@@ -30,6 +30,12 @@ SHAPES = [
     (1025, 5, 33, 260, 129, "f32", "f32", "mixed"),
     (2050, 1, 128, 64, 64, "f16", "f16", "runs"),
     (640, 1000, 4, 40, 48, "bf16", "bf16", "mixed"),
+    # many rows: blocks of 16 and 32, second adapters of a block done elsewhere, several pieces an adapter
+    (4200, 9, 16, 64, 72, "bf16", "bf16", "runs"),
+    (4500, 70, 24, 72, 64, "f16", "f16", "mixed"),
+    (5000, 3, 48, 64, 64, "f32", "bf16", "runs"),
+    (4100, 5, 100, 64, 136, "bf16", "bf16", "mixed"),
+    (4111, 300, 32, 65, 64, "bf16", "bf16", "mixed"),
 ]
 
 

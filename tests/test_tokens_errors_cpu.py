@@ -59,7 +59,8 @@ def test_combine_backward_and_dispatch_backward():
 
 
 FORWARD = dict(x=M, ld_x=8, base=2 * M, ld_base=16, dtype=0, n_rows=4, inner=8, outer=16, adapter=3 * M, a=4 * M, b=5 * M,
-               wtype=2, scale=6 * M, n_adapters=3, rank=4, out=7 * M, ld_out=16, stream=None)
+               wtype=2, scale=6 * M, n_adapters=3, rank=4, out=7 * M, ld_out=16,
+               workspace=None, workspace_bytes=0, stream=None)
 
 
 @pytest.mark.parametrize("change,rc", [
@@ -68,6 +69,8 @@ FORWARD = dict(x=M, ld_x=8, base=2 * M, ld_base=16, dtype=0, n_rows=4, inner=8, 
     (dict(n_rows=1 << 24), UNS), (dict(x=None), INV), (dict(adapter=None), INV), (dict(a=None), INV), (dict(b=None), INV),
     (dict(scale=None), INV), (dict(out=None), INV), (dict(ld_x=7), INV), (dict(ld_out=15), INV), (dict(ld_base=15), INV),
     (dict(out=M), INV), (dict(out=4 * M), INV), (dict(out=2 * M, ld_out=17), INV), (dict(n_rows=0), moe.OK),
+    (dict(n_rows=2000), INV), (dict(n_rows=2000, workspace=9 * M, workspace_bytes=100), INV),   # a workspace is wanted
+    (dict(n_rows=2000, workspace=9 * M + 8, workspace_bytes=M), INV), (dict(n_rows=2000, workspace=M, workspace_bytes=M), INV),
 ])
 def test_adapters_forward(change, rc):
     assert moe.gpu_lib().moe_adapters_forward(*{**FORWARD, **change}.values()) == rc
@@ -94,3 +97,5 @@ def test_workspaces():
     assert lib.moe_tokens_workspace(-1, 8, 128) == 0
     assert lib.moe_adapters_workspace(100, 8, 8, 4, 300) == 0
     assert lib.moe_adapters_workspace(0, 8, 8, 4, 4) > 0
+    assert lib.moe_adapters_forward_workspace(32, 2048, 2048, 8, 16) == 0
+    assert lib.moe_adapters_forward_workspace(8192, 2048, 2048, 8, 16) >= 8192 * 16 * 4
