@@ -1080,7 +1080,7 @@ hipError_t forward(const AdapterArgs &g, void *workspace, hipStream_t stream) {
     const ForwardSpace s = forward_space(g.T, g.outer, g.n, g.r);
     if (s.bytes && piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.out, g.ld_out, g.outer, z) &&
         (!g.base || piecewise(g.base, g.ld_base, g.outer, z)) && reinterpret_cast<uintptr_t>(g.b) % 16 == 0 &&
-        piecewise_adapter(g.a, g.inner, g.outer, s.rp, sizeof(TW))) {
+        (int64_t)g.n * g.outer < (1 << 30) && piecewise_adapter(g.a, g.inner, g.outer, s.rp, sizeof(TW))) {
         float *v = reinterpret_cast<float *>(static_cast<char *>(workspace) + s.v);
         const void *b = g.b;
         hipError_t err = hipSuccess;

@@ -6,6 +6,8 @@ the caller holds.  A matrix needs unit stride along its rows (a column slice of 
 do); index, gate, scale, adapter and adapter-gradient tensors are contiguous.  ``MoeError`` with
 ``ERR_INVALID`` or ``ERR_UNSUPPORTED`` says what was refused; nothing is enqueued then.
 """
+import functools
+
 import torch
 
 from . import ERR_INVALID, OK, T_BF16, T_F16, T_F32, MoeError, gpu_lib
@@ -79,6 +81,12 @@ def _call(fn, gpu, stream, *args):
         raise MoeError(rc, gpu_lib().moe_last_error().decode())
 
 
+@functools.lru_cache(maxsize=1024)
+def _needed(fn, *sizes):
+    """Workspace bytes of a call of these sizes."""
+    return getattr(gpu_lib(), fn)(*sizes)
+
+
 def _workspace(nbytes, given, gpu, stream):
     """A workspace tensor: the caller's, or a new one that belongs to the call's stream."""
     if given is not None:
@@ -119,7 +127,7 @@ def tokens_dispatch(x, ids, n_experts, rows, offsets, pos, src, expert, workspac
     p_ids, p_off = _array("ids", ids, (T, k), i32, gpu), _array("offsets", offsets, (n_experts + 1,), i32, gpu)
     p_pos, p_src = _array("pos", pos, (T, k), i32, gpu), _array("src", src, (n,), i32, gpu)
     p_exp = _array("expert", expert, (n,), i32, gpu)
-    need = lib.moe_tokens_workspace(T, k, n_experts)
+    need = _needed("moe_tokens_workspace", T, k, n_experts)
     ws = _workspace(need, workspace, gpu, stream) if need else None
     _call(lib.moe_tokens_dispatch, gpu, stream, px, ldx, dtype, T, H, p_ids, k, n_experts, pr, ldr, p_off, p_pos,
           p_src, p_exp, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
@@ -185,7 +193,7 @@ def adapters_forward(x, adapter, a, b, scale, out, base=None, workspace=None, st
     p_base, ldb = (None, outer) if base is None else _matrix("base", base, T, outer, x.dtype, gpu)
     p_ad = _array("adapter", adapter, (T,), torch.int32, gpu)
     p_scale = _array("scale", scale, (n,), torch.float32, gpu)
-    need = lib.moe_adapters_forward_workspace(T, inner, outer, n, r)
+    need = _needed("moe_adapters_forward_workspace", T, inner, outer, n, r)
     ws = _workspace(need, workspace, gpu, stream) if need else None
     _call(lib.moe_adapters_forward, gpu, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb, wtype,
           p_scale, n, r, po, ldo, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
@@ -207,6 +215,6 @@ def adapters_backward(d_out, x, adapter, a, b, scale, d_x, d_a, d_b, dx_base=Non
     p_scale = _array("scale", scale, (n,), torch.float32, gpu)
     p_da = _array("d_a", d_a, (n, r, inner), torch.float32, gpu)
     p_db = _array("d_b", d_b, (n, outer, r), torch.float32, gpu)
-    ws = _workspace(lib.moe_adapters_workspace(T, inner, outer, n, r), workspace, gpu, stream)
+    ws = _workspace(_needed("moe_adapters_workspace", T, inner, outer, n, r), workspace, gpu, stream)
     _call(lib.moe_adapters_backward, gpu, stream, pd, ldd, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
           wtype, p_scale, n, r, pg, ldg, p_da, p_db, ws.data_ptr(), ws.numel() * ws.element_size())
