@@ -228,8 +228,10 @@ struct Lane {
 
 // The first product of a block of 16 MT rows: v = m w^T.  The waves take runs of 128 bytes of the
 // rows in turn, two chunks a lane, 64 bytes of a row in an instruction.  NT: tiles of 16 ranks at a time.
-// More rows a block read w from L2 less often, which is what bounds this beside m.
-template <typename TX, typename TW, int NT, int MT, int WAVES>
+// More rows a block read w from L2 less often, which is what bounds this beside m.  TILED: w lies in the
+// order in which it is loaded (tiled_at), 1 KB an instruction, which L2 gives faster than 64 bytes of 16
+// rows (both products of a backward call of 16384 rows at rank 32: 44 us against 52).
+template <typename TX, typename TW, int NT, int MT, int WAVES, bool TILED>
 struct Shrink {
     typedef Mma<TX> M;
     static constexpr int C = M::kChunk, kRun = 8 * C;
@@ -246,7 +248,10 @@ struct Shrink {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int q = q0 + 16 * i + l.l16;
-            wr[i] = q < r ? (unsigned)q * cols : kNowhere / sizeof(TW);
+            if constexpr (TILED)
+                wr[i] = ((q0 / 16 + i) * 2 * 64 + (threadIdx.x & 63)) * C;
+            else
+                wr[i] = q < r ? (unsigned)q * cols : kNowhere / sizeof(TW);
         }
         const int runs = (cols + kRun - 1) / kRun;
         for (int d = l.wave; d < runs; d += U * WAVES) {
@@ -261,7 +266,12 @@ struct Shrink {
 #pragma unroll
                     for (int j = 0; j < MT; ++j) x[u][j][s].load(m, in ? row + j * step + k * (unsigned)sizeof(TX) : kNowhere);
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) a[u][i][s].load(w, in ? (wr[i] + k) * (unsigned)sizeof(TW) : kNowhere);
+                    for (int i = 0; i < NT; ++i) {
+                        if constexpr (TILED)   // (beyond the last run: out of the buffer's range)
+                            a[u][i][s].load(w, (wr[i] + ((d + u * WAVES) * ((r + 15) / 16) * 2 + s) * 64 * C) * (unsigned)sizeof(TW));
+                        else
+                            a[u][i][s].load(w, in ? (wr[i] + k) * (unsigned)sizeof(TW) : kNowhere);
+                    }
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -280,6 +290,15 @@ struct Shrink {
                     acc[i][j];
     }
 };
+
+// Where element (q, c) of an adapter's [r x cols] matrix lies in that order, of chunks of C elements.
+__host__ __device__ inline size_t tiled_at(int q, int c, int r, int C) {
+    const int run = c / (8 * C), s = c / (4 * C) % 2, quad = c / C % 4;
+    return ((((size_t)run * ((r + 15) / 16) + q / 16) * 2 + s) * 64 + quad * 16 + q % 16) * C + c % C;
+}
+__host__ __device__ inline size_t tiled_size(int r, int cols, int C) {
+    return (size_t)((cols + 8 * C - 1) / (8 * C)) * (8 * C) * ((r + 15) / 16 * 16);
+}
 
 // The adapters of a lane's rows (e < 0: done or none): the smallest number left in the block, the same in
 // every lane of every wave; -1 if there is none.
@@ -311,7 +330,7 @@ __device__ __forceinline__ Buffer rows_of(const void *p, int64_t ld, int row0, i
 // v = scale (m w^T) for rows with their own adapters' w: the forward's x and A; the backward's x and A,
 // and d_out and B transposed.
 struct ShrinkJob {
-    const void *m, *w;    // [T x cols]; [n][at least r x cols], w_step elements from one adapter to the next
+    const void *m, *w;    // [T x cols]; [n][r x cols] (or tiled), w_step elements from one adapter to the next
     int64_t ld, w_step;
     float *v;             // [T x vr], zeros from rank r on
     int cols;
@@ -330,13 +349,13 @@ struct ShrinkArgs {
 //  - with many blocks (a full grid of such workgroups would cost more than it saves), the first `helpers`
 //    workgroups look through kHelped blocks each and do their second adapters; the others leave those out.
 constexpr int kHelped = 8;
-template <typename TX, typename TW, int NT, int MT, int WAVES>
+template <typename TX, typename TW, int NT, int MT, int WAVES, bool TILED>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4))) void k_shrink(ShrinkArgs g, int helpers) {
     constexpr int kPart = 256 * NT * MT;
     __shared__ __align__(16) float part[WAVES * kPart];
     const ShrinkJob &job = g.job[blockIdx.z];
     const Lane l;
-    Shrink<TX, TW, NT, MT, WAVES> x;
+    Shrink<TX, TW, NT, MT, WAVES, TILED> x;
     x.row = l.l16 * (unsigned)job.ld * sizeof(TX);
     x.step = 16 * (unsigned)job.ld * sizeof(TX);
     x.cols = job.cols;
@@ -354,7 +373,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4)))
         int r = g.r;
         asm volatile("" : "+s"(r));
         x.m = rows_of<TX>(job.m, job.ld, row0, 16 * MT, g.T, job.cols);
-        x.w = buffer(static_cast<const TW *>(job.w) + now * job.w_step, (size_t)r * job.cols * sizeof(TW));
+        x.w = buffer(static_cast<const TW *>(job.w) + now * job.w_step, (size_t)job.w_step * sizeof(TW));
         const float scale = g.scale[now];
         for (int q0 = 0; q0 < g.vr; q0 += 16 * NT) {
             x.run(l, q0, r, part);
@@ -682,17 +701,19 @@ __global__ __launch_bounds__(kThreads) void k_back_weights(AdapterBackArgs g, co
 // way (ranks padded to a multiple of 8); v and u go to memory on the way, and the weights' gradients
 // are products over the rows of one adapter at a time, in the order of a counting sort.
 
-// at[e][c][q] = a[e][q][c], bt[e][q][o] = b[e][o][q], zeros in the padding; and where inner is padded,
-// ap[e][q][c] = a[e][q][c].  32 ranks by 64 columns a workgroup.
+// at[e][c][q] = a[e][q][c] with zeros in the padding, and a and b transposed in the order in which the first
+// product loads them (tiled_at), zeros behind their last column.  32 ranks by 64 columns a workgroup.
 template <typename TW>
-__global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW *b, TW *at, TW *bt, TW *ap, int inner,
-                                                          int outer, int ip, int op, int r, int rp) {
+__global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW *b, TW *at, TW *aw, TW *bw, int inner, int outer,
+                                                          int ip, int r, int rp, int C) {
     __shared__ TW tile[32][65];
     const int tiles_a = (ip + 63) / 64, e = blockIdx.z, q0 = blockIdx.y * 32;
     const bool is_b = (int)blockIdx.x >= tiles_a;
     const int c0 = (is_b ? blockIdx.x - tiles_a : blockIdx.x) * 64;
-    const int cols = is_b ? outer : inner, padded = is_b ? op : ip;
+    const int cols = is_b ? outer : inner;
     const size_t ea = (size_t)e * r * inner, eb = (size_t)e * r * outer;
+    TW *to = (is_b ? bw : aw) + e * tiled_size(r, cols, C);
+    const int whole = (cols + 8 * C - 1) / (8 * C) * (8 * C);   // columns of whole runs
 #pragma unroll
     for (int k = 0; k < 32 * 64 / kThreads; ++k) {
         const int i = threadIdx.x + k * kThreads, q = is_b ? i % 32 : i / 64, c = is_b ? i / 32 : i % 64;
@@ -700,17 +721,19 @@ __global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW 
         if (q0 + q < r && c0 + c < cols)
             v = is_b ? b[eb + (size_t)(c0 + c) * r + q0 + q] : a[ea + (size_t)(q0 + q) * inner + c0 + c];
         tile[q][c] = v;
-        if (!is_b && ap && q0 + q < r && c0 + c < padded) ap[((size_t)e * r + q0 + q) * ip + c0 + c] = v;
     }
     __syncthreads();
+    // consecutive threads write consecutive elements: a chunk of a rank's, then the next rank's
 #pragma unroll
     for (int k = 0; k < 32 * 64 / kThreads; ++k) {
-        const int i = threadIdx.x + k * kThreads, q = is_b ? i / 64 : i % 32, c = is_b ? i % 64 : i / 32;
-        if (q0 + q >= rp || c0 + c >= padded) continue;
-        if (is_b)
-            bt[((size_t)e * rp + q0 + q) * op + c0 + c] = tile[q][c];
-        else
-            at[((size_t)e * ip + c0 + c) * rp + q0 + q] = tile[q][c];
+        const int i = threadIdx.x + k * kThreads, c = i % C + i / (32 * C) * C, q = i / C % 32;
+        if (q0 + q < (r + 15) / 16 * 16 && c0 + c < whole) to[tiled_at(q0 + q, c0 + c, r, C)] = tile[q][c];
+    }
+    if (is_b) return;
+#pragma unroll
+    for (int k = 0; k < 32 * 64 / kThreads; ++k) {
+        const int i = threadIdx.x + k * kThreads, q = i % 32, c = i / 32;
+        if (q0 + q < rp && c0 + c < ip) at[((size_t)e * ip + c0 + c) * rp + q0 + q] = tile[q][c];
     }
 }
 
@@ -805,8 +828,9 @@ __device__ __forceinline__ void store_grad(const BackWeights &g, int e, bool is_
 // d_a and d_b of one piece: 128 columns and 16 NT ranks a workgroup, 32 rows a wave at a time.
 // left[q][col] = sum over rows of (u or v)[row][q] (x or d_out)[row][col], the rows being the reduction:
 // a lane loads 16 bytes of 8 rows, and for bf16 turns them into the eight columns' operands, pairs of
-// rows a dword (v_perm), with u and v in two parts of 16 bits together; other types multiply in fp32,
-// whose operand is one element.
+// rows a dword (v_perm), with u and v in three parts, which hold all of an fp32 value's 24 bits (two parts
+// made the gradients' error 2.5 times that of fp32 products); other types multiply in fp32, whose operand is
+// one element.
 template <typename TX, int NT, bool SMALL>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NT == 4 && sizeof(TX) == 4 ? 1 : 2))) void k_back_pieces(BackWeights g) {
     constexpr bool kPairs = std::is_same_v<TX, bf16>;
@@ -874,15 +898,17 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NT == 
                 }
         }
         if constexpr (kPairs) {
-            bf16x8 hi[NT], lo[NT];
+            bf16x8 hi[NT], mid[NT], lo[NT];
 #pragma unroll
             for (int k = 0; k < NT; ++k)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    bf16 h, w;
-                    split(f[k][j], h, w);
+                    bf16 h, m, w;
+                    split(f[k][j], h, m);
+                    w = narrow<bf16>(f[k][j] - widen(h) - widen(m));
                     hi[k][j] = h;
-                    lo[k][j] = w;
+                    mid[k][j] = m;
+                    lo[k][j] = __builtin_isfinite(f[k][j]) ? w : narrow<bf16>(0.f);
                 }
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
@@ -896,6 +922,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NT == 
 #pragma unroll
                 for (int k = 0; k < NT; ++k) {
                     acc[k][t] = Mma<bf16>::mul(lo[k], right, acc[k][t]);
+                    acc[k][t] = Mma<bf16>::mul(mid[k], right, acc[k][t]);
                     acc[k][t] = Mma<bf16>::mul(hi[k], right, acc[k][t]);
                 }
             }
@@ -975,7 +1002,7 @@ __global__ __launch_bounds__(kThreads) void k_back_join(BackWeights g) {
 struct BackSpace {
     int ip, op, rp, piece_rows, max_pieces;
     bool padded;   // rows are copied to whole pieces of 8 elements
-    size_t offsets, order, sort, v, u, at, bt, ap, partial, x, d_out, d_x, bytes;
+    size_t offsets, order, sort, v, u, at, aw, bw, partial, x, d_out, d_x, bytes;
 };
 BackSpace back_space(int T, int inner, int outer, int n, int r) {
     BackSpace s;
@@ -1000,9 +1027,10 @@ BackSpace back_space(int T, int inner, int outer, int n, int r) {
     s.v = take(row * s.rp * 4);
     s.u = take(row * s.rp * 4);
     s.at = take(adapters * s.ip * s.rp * 4);
-    s.bt = take(adapters * s.op * s.rp * 4);
+    // whole runs of columns, 64 elements for 16-bit activations
+    s.aw = take(adapters * tiled_size(r, inner, 8) * 4);
+    s.bw = take(adapters * tiled_size(r, outer, 8) * 4);
     s.partial = take((size_t)s.max_pieces * r * (s.ip + s.op) * 4);
-    s.ap = take(s.padded ? adapters * r * s.ip * 4 : 0);
     s.x = take(s.padded ? row * s.ip * 4 : 0);
     s.d_out = take(s.padded ? row * s.op * 4 : 0);
     s.d_x = take(s.padded ? row * s.ip * 4 : 0);
@@ -1036,16 +1064,16 @@ bool piecewise_adapter(const void *a, int64_t inner, int64_t outer, int64_t rp, 
            rp * std::max(inner, outer) * (int64_t)size < kBufferBytes;
 }
 
-template <typename TX, typename TW, int MT, int WAVES>
+template <typename TX, typename TW, int MT, int WAVES, bool TILED>
 hipError_t shrink(const ShrinkArgs &g, int jobs, hipStream_t stream) {
     const int tiles = (g.T + 16 * MT - 1) / (16 * MT);
     const bool many = tiles >= 256 && g.n > 1;
     const int helpers = many ? (tiles + kHelped - 1) / kHelped : 0;
     const int turns = many ? 1 : std::min(g.n, std::max(2, std::min(16, 1024 / tiles)));
     const dim3 grid(helpers + tiles, turns, jobs), block(64 * WAVES);
-    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, WAVES>, grid, block, stream, nullptr, nullptr, g, helpers);
-    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, WAVES>, grid, block, stream, nullptr, nullptr, g, helpers);
-    return launch(k_shrink<TX, TW, 4, MT, WAVES>, grid, block, stream, nullptr, nullptr, g, helpers);
+    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, helpers);
+    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, helpers);
+    return launch(k_shrink<TX, TW, 4, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, helpers);
 }
 
 template <typename TX, typename TW, int MT>
@@ -1064,12 +1092,12 @@ hipError_t expand(ExpandArgs g, hipStream_t stream) {
 
 // Both products of a call.  A block of 32 rows instead of 16 halves the reads of the adapters' matrices
 // from L2, and the number of workgroups: worth it from rank 17 (shrink) on, with enough rows.
-template <typename TX, typename TW>
+template <typename TX, typename TW, bool TILED>
 hipError_t products(const ShrinkArgs &sa, int jobs, const ExpandArgs &ea, hipStream_t stream) {
     const bool tall = sa.r > 16 && sa.T >= kTallRows;
-    const hipError_t err = !tall          ? shrink<TX, TW, 1, 8>(sa, jobs, stream)
-                           : sa.r <= 32 ? shrink<TX, TW, 2, 8>(sa, jobs, stream)
-                                        : shrink<TX, TW, 2, 16>(sa, jobs, stream);
+    const hipError_t err = !tall          ? shrink<TX, TW, 1, 8, TILED>(sa, jobs, stream)
+                           : sa.r <= 32 ? shrink<TX, TW, 2, 8, TILED>(sa, jobs, stream)
+                                        : shrink<TX, TW, 2, 16, TILED>(sa, jobs, stream);
     if (err != hipSuccess) return err;
     return tall ? expand<TX, TW, 2>(ea, stream) : expand<TX, TW, 1>(ea, stream);
 }
@@ -1093,7 +1121,7 @@ hipError_t forward(const AdapterArgs &g, void *workspace, hipStream_t stream) {
         }
         const ShrinkArgs sa{{{g.x, g.a, g.ld_x, (int64_t)g.r * g.inner, v, g.inner}}, g.adapter, g.scale, g.T, g.n, g.r, s.rp};
         const ExpandArgs ea{g.base, b, g.out, v, g.adapter, g.ld_base, g.ld_out, g.T, g.outer, g.n, s.rp, s.rp, 0};
-        return err == hipSuccess ? products<TX, TW>(sa, 1, ea, stream) : err;
+        return err == hipSuccess ? products<TX, TW, false>(sa, 1, ea, stream) : err;
     }
     const int groups = (g.outer + kThreads - 1) / kThreads;
     const int slices = std::max(1, std::min(groups, kRowTarget / g.T)), cols = (groups + slices - 1) / slices * kThreads;
@@ -1109,7 +1137,7 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
     float *v = reinterpret_cast<float *>(ws + s.v), *u = reinterpret_cast<float *>(ws + s.u);
     constexpr size_t z = sizeof(TX);
     const bool blocks =
-        g.T > 0 && piecewise_adapter(s.padded ? workspace : g.a, s.ip, s.op, s.rp, sizeof(TW)) &&
+        g.T > 0 && piecewise_adapter(workspace, s.ip, s.op, (s.rp + 15) / 16 * 16, sizeof(TW)) &&
         (s.padded || (piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.d_out, g.ld_d_out, g.outer, z) &&
                       piecewise(g.d_x, g.ld_d_x, g.inner, z) &&
                       (!g.dx_base || piecewise(g.dx_base, g.ld_dx_base, g.inner, z))));
@@ -1136,14 +1164,15 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
                       static_cast<const float *>(v), static_cast<const float *>(u));
     }
 
-    TW *at = reinterpret_cast<TW *>(ws + s.at), *bt = reinterpret_cast<TW *>(ws + s.bt);
-    TW *ap = s.padded ? reinterpret_cast<TW *>(ws + s.ap) : nullptr;
-    err = launch(k_back_layout<TW>, dim3((s.ip + 63) / 64 + (s.op + 63) / 64, (s.rp + 31) / 32, g.n), dim3(kThreads), stream,
-                 nullptr, nullptr, static_cast<const TW *>(g.a), static_cast<const TW *>(g.b), at, bt, ap, g.inner, g.outer,
-                 s.ip, s.op, g.r, s.rp);
+    constexpr int C = Mma<TX>::kChunk;
+    TW *at = reinterpret_cast<TW *>(ws + s.at), *aw = reinterpret_cast<TW *>(ws + s.aw), *bw = reinterpret_cast<TW *>(ws + s.bw);
+    // every column that a whole run has: the runs are at most 64 columns
+    err = launch(k_back_layout<TW>, dim3((s.ip + 63) / 64 + (g.outer + 63) / 64, (g.r + 31) / 32, g.n), dim3(kThreads), stream,
+                 nullptr, nullptr, static_cast<const TW *>(g.a), static_cast<const TW *>(g.b), at, aw, bw, g.inner, g.outer, s.ip,
+                 g.r, s.rp, C);
     if (err != hipSuccess) return err;
     // what the block kernels read and write: the caller's matrices, or padded copies
-    const void *x = g.x, *d_out = g.d_out, *dx_base = g.dx_base, *am = g.a;
+    const void *x = g.x, *d_out = g.d_out, *dx_base = g.dx_base;
     void *d_x = g.d_x;
     int64_t ld_x = g.ld_x, ld_d_out = g.ld_d_out, ld_dx_base = g.ld_dx_base, ld_d_x = g.ld_d_x;
     const int copies = std::min((g.T + 3) / 4, 2048);
@@ -1157,11 +1186,11 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
         dx_base = d_x = ws + s.d_x;
         ld_x = ld_dx_base = ld_d_x = s.ip;
         ld_d_out = s.op;
-        am = ap;
     }
-    const ShrinkArgs sa{{{x, am, ld_x, (int64_t)g.r * s.ip, v, s.ip}, {d_out, bt, ld_d_out, (int64_t)s.rp * s.op, u, s.op}},
+    const ShrinkArgs sa{{{x, aw, ld_x, (int64_t)tiled_size(g.r, g.inner, C), v, s.ip},
+                         {d_out, bw, ld_d_out, (int64_t)tiled_size(g.r, g.outer, C), u, s.op}},
                         g.adapter, g.scale, g.T, g.n, g.r, s.rp};
-    err = products<TX, TW>(sa, 2, {dx_base, at, d_x, u, g.adapter, ld_dx_base, ld_d_x, g.T, s.ip, g.n, s.rp, s.rp, 0}, stream);
+    err = products<TX, TW, true>(sa, 2, {dx_base, at, d_x, u, g.adapter, ld_dx_base, ld_d_x, g.T, s.ip, g.n, s.rp, s.rp, 0}, stream);
     if (err != hipSuccess) return err;
     if (s.padded) {
         Reshape m{{d_x}, {g.d_x}, {s.ip}, {g.ld_d_x}, {g.inner}, {g.inner}};
