@@ -4,12 +4,11 @@
 #include <type_traits>
 
 #include "elements.hpp"
-#include "token_kernels.hpp"
+#include "order.hpp"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kRowCalls = 512;    // rows of a call that takes a workgroup a row
 constexpr int kTallRows = 4096;   // rows from which blocks are 32 rows high
 constexpr int kRowTarget = 512;   // workgroups of such a call: two a CU
@@ -702,14 +701,25 @@ __global__ __launch_bounds__(kThreads) void k_back_weights(AdapterBackArgs g, co
 // are products over the rows of one adapter at a time, in the order of a counting sort.
 
 // at[e][c][q] = a[e][q][c] with zeros in the padding, and a and b transposed in the order in which the first
-// product loads them (tiled_at), zeros behind their last column.  32 ranks by 64 columns a workgroup.
-template <typename TW>
+// product loads them (tiled_at), zeros behind their last column.  32 ranks by 64 columns a workgroup.  The first `order_wgs` workgroups
+// make the order of the rows by adapter meanwhile.  C: a chunk's elements.
+constexpr int kOrderedHere = 256;   // adapters that this has room for
+template <typename TW, int C>
 __global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW *b, TW *at, TW *aw, TW *bw, int inner, int outer,
-                                                          int ip, int r, int rp, int C) {
-    __shared__ TW tile[32][65];
+                                                          int ip, int r, int rp, DispatchArgs order, int order_wgs) {
+    __shared__ union {
+        TW tile[32][65];
+        OrderSpace<kOrderedHere> order;
+    } lds;
+    auto &tile = lds.tile;
+    const int tile_at = (int)blockIdx.x - order_wgs;
+    if (tile_at < 0) {
+        if (blockIdx.y == 0 && blockIdx.z == 0) order_picks<kOrderedHere>(order, blockIdx.x, kWgPicks, nullptr, 0, 1, lds.order);
+        return;
+    }
     const int tiles_a = (ip + 63) / 64, e = blockIdx.z, q0 = blockIdx.y * 32;
-    const bool is_b = (int)blockIdx.x >= tiles_a;
-    const int c0 = (is_b ? blockIdx.x - tiles_a : blockIdx.x) * 64;
+    const bool is_b = tile_at >= tiles_a;
+    const int c0 = (is_b ? tile_at - tiles_a : tile_at) * 64;
     const int cols = is_b ? outer : inner;
     const size_t ea = (size_t)e * r * inner, eb = (size_t)e * r * outer;
     TW *to = (is_b ? bw : aw) + e * tiled_size(r, cols, C);
@@ -806,6 +816,7 @@ __device__ inline Piece find_piece(const int32_t *offsets, int n, int rows, int 
 // Calls of up to this many rows: an adapter is one piece, its rows are found by the workgroups themselves,
 // and there is neither a sort nor a join.
 constexpr int kSmallBack = 512;
+constexpr int kOrderRows = 32768;   // rows whose order every ordering workgroup counts by itself
 
 struct BackWeights {
     const int32_t *adapter;
@@ -1142,19 +1153,19 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
                       piecewise(g.d_x, g.ld_d_x, g.inner, z) &&
                       (!g.dx_base || piecewise(g.dx_base, g.ld_dx_base, g.inner, z))));
     const bool small = blocks && g.T <= kSmallBack;
+    DispatchArgs d{};
+    d.ids = g.adapter;
+    d.offsets = offsets;
+    d.src = order;
+    d.T = g.T;
+    d.H = 1;
+    d.k = 1;
+    d.E = g.n;
+    // a call of few rows needs no order, and most others make it in the launch of the layout
+    const bool order_here = blocks && !small && g.T <= kOrderRows && g.n <= kOrderedHere;
     hipError_t err = hipSuccess;
-    if (!small) {
-        DispatchArgs d{};
-        d.ids = g.adapter;
-        d.offsets = offsets;
-        d.src = order;
-        d.T = g.T;
-        d.H = 1;
-        d.k = 1;
-        d.E = g.n;
-        err = launch_dispatch(dtype, d, ws + s.sort, stream);
-        if (err != hipSuccess) return err;
-    }
+    if (!small && !order_here) err = launch_dispatch(dtype, d, ws + s.sort, stream);
+    if (err != hipSuccess) return err;
     if (!blocks) {
         if (g.T > 0) err = launch(k_back_row<TX, TW>, dim3(g.T), dim3(kThreads), stream, nullptr, nullptr, g, v, u);
         if (err != hipSuccess) return err;
@@ -1166,10 +1177,10 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
 
     constexpr int C = Mma<TX>::kChunk;
     TW *at = reinterpret_cast<TW *>(ws + s.at), *aw = reinterpret_cast<TW *>(ws + s.aw), *bw = reinterpret_cast<TW *>(ws + s.bw);
-    // every column that a whole run has: the runs are at most 64 columns
-    err = launch(k_back_layout<TW>, dim3((s.ip + 63) / 64 + (g.outer + 63) / 64, (g.r + 31) / 32, g.n), dim3(kThreads), stream,
-                 nullptr, nullptr, static_cast<const TW *>(g.a), static_cast<const TW *>(g.b), at, aw, bw, g.inner, g.outer, s.ip,
-                 g.r, s.rp, C);
+    const int order_wgs = order_here ? (g.T + kWgPicks - 1) / kWgPicks : 0;
+    err = launch(k_back_layout<TW, C>, dim3(order_wgs + (s.ip + 63) / 64 + (g.outer + 63) / 64, (g.r + 31) / 32, g.n),
+                 dim3(kThreads), stream, nullptr, nullptr, static_cast<const TW *>(g.a), static_cast<const TW *>(g.b), at, aw, bw,
+                 g.inner, g.outer, s.ip, g.r, s.rp, d, order_wgs);
     if (err != hipSuccess) return err;
     // what the block kernels read and write: the caller's matrices, or padded copies
     const void *x = g.x, *d_out = g.d_out, *dx_base = g.dx_base;

@@ -6,15 +6,11 @@
 #include <algorithm>
 
 #include "elements.hpp"
-#include "token_kernels.hpp"
+#include "order.hpp"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWgPicks = 512;         // picks a dispatch workgroup ranks at most
-constexpr int kCopies = 8;            // copies of a histogram, by lane: picks of one expert in a wave
-                                      // would otherwise add to one LDS word in turn
 constexpr int kDirectPicks = 4096;    // up to here every workgroup counts all picks itself, and up to
 constexpr int kDirectOrder = 32768;   // here where it makes the order alone, in few workgroups
 constexpr int kSlicePicks = 2048;     // picks of a histogram slice above, at least
@@ -27,36 +23,6 @@ int slices_of(int N, bool rows) {
 }
 int per_slice(int N, int slices) { return (N + slices - 1) / slices; }
 
-// Adds picks p0 .. p1 to the histogram copies, eight picks a thread in flight.
-__device__ inline void count(const int32_t *ids, int p0, int p1, int E, int *hist) {
-    const int copy = threadIdx.x & (kCopies - 1);
-    auto add = [&](int e) {
-        if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e * kCopies + copy], 1);
-    };
-    int p = p0 + 4 * (int)threadIdx.x;
-    for (; p + 4 * kThreads + 4 <= p1; p += 8 * kThreads) {
-        int e[8];
-        __builtin_memcpy(e, ids + p, 16);
-        __builtin_memcpy(e + 4, ids + p + 4 * kThreads, 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) add(e[i]);
-    }
-    for (; p < p1; p += 4 * kThreads) {
-        int e[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = p + i < p1 ? ids[p + i] : -1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) add(e[i]);
-    }
-}
-
-__device__ inline int total_of(const int *hist, int e) {
-    int s = 0;
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) s += hist[e * kCopies + c];
-    return s;
-}
-
 __global__ __launch_bounds__(kThreads) void k_slice_counts(const int32_t *ids, int N, int per, int E, int32_t *counts) {
     __shared__ int hist[kMaxSegments * kCopies];
     for (int i = threadIdx.x; i < E * kCopies; i += kThreads) hist[i] = 0;
@@ -67,25 +33,13 @@ __global__ __launch_bounds__(kThreads) void k_slice_counts(const int32_t *ids, i
     for (int e = threadIdx.x; e < E; e += kThreads) counts[(size_t)blockIdx.x * E + e] = total_of(hist, e);
 }
 
-// A workgroup takes `tokens` consecutive tokens.  The row of pick p with expert e is
-//   offsets[e] + (valid picks of e before p),
-// so it counts, per expert, all picks and the picks before its own -- from the ids themselves, or for
-// many picks from the slices' counts -- and then ranks its own picks in order, 64 at a time by one
-// wave: the lanes with the same expert are found by one ballot per bit of the id.  The rows follow:
-// the first four tokens' pieces are requested before all that.  EM: experts there is room for.
+// The order of the picks (order_picks), then the rows of the workgroup's tokens: read once, written once a
+// pick.  The first four tokens' pieces are requested before the order is made.
 template <typename T, int EM>
 __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int tokens, int lanes_log2, const int32_t *counts,
                                                        int slices, int per) {
-    __shared__ int hist[EM * kCopies];
-    __shared__ int next[EM];   // picks before the workgroup's, then the next row, of each expert
-    __shared__ int all[EM];    // picks of each expert
-    __shared__ int row_of[kWgPicks];
-    __shared__ int wave_sum[kThreads / 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int E = a.E, N = a.T * a.k;
-    const int t0 = blockIdx.x * tokens, t1 = min(a.T, t0 + tokens);
-    const int p0 = t0 * a.k, p1 = t1 * a.k;
-
+    __shared__ OrderSpace<EM> o;
+    const int tid = threadIdx.x, t0 = blockIdx.x * tokens, t1 = min(a.T, t0 + tokens);
     const int L = 1 << lanes_log2, groups = kThreads >> lanes_log2, l = tid & (L - 1);
     const int first = t0 + (tid >> lanes_log2), pieces = (a.H + kVec<T> - 1) / kVec<T>;
     const T *x = static_cast<const T *>(a.x);
@@ -96,98 +50,7 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int token
     };
     uint4 ahead[4];
     if (x && l < pieces) request(ahead, first, l);
-
-    for (int i = tid; i < E * kCopies; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    const int slice = counts ? p0 / per : 0;
-    count(a.ids, counts ? slice * per : 0, p0, E, hist);
-    __syncthreads();
-    for (int e = tid; e < E; e += kThreads) {
-        int before = total_of(hist, e), sum = 0;
-        if (counts) {
-#pragma unroll 8
-            for (int s = 0; s < slices; ++s) {
-                const int n = counts[(size_t)s * E + e];
-                sum += n;
-                before += s < slice ? n : 0;
-            }
-        }
-        next[e] = before;
-        all[e] = sum;
-    }
-    if (!counts) {
-        __syncthreads();
-        count(a.ids, p0, N, E, hist);
-        __syncthreads();
-        for (int e = tid; e < E; e += kThreads) all[e] = total_of(hist, e);
-    }
-    __syncthreads();
-    // the experts' first rows: consecutive experts a thread
-    constexpr int EP = EM / kThreads;
-    int total[EP], mine = 0;
-#pragma unroll
-    for (int i = 0; i < EP; ++i) {
-        total[i] = EP * tid + i < E ? all[EP * tid + i] : 0;
-        mine += total[i];
-    }
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(upto, d);
-        if (lane >= d) upto += v;
-    }
-    if (lane == 63) wave_sum[wave] = upto;
-    __syncthreads();
-    int start = upto - mine;
-    for (int w = 0; w < wave; ++w) start += wave_sum[w];
-    const int n_rows = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
-#pragma unroll
-    for (int i = 0; i < EP; ++i) {
-        const int e = EP * tid + i;
-        if (e < E) {
-            next[e] += start;
-            if (blockIdx.x == 0) a.offsets[e] = start;
-        }
-        start += total[i];
-    }
-    if (blockIdx.x == 0 && tid == 0) a.offsets[E] = n_rows;
-    __syncthreads();
-
-    if (wave == 0) {
-        volatile int *nx = next;
-        for (int p = p0; p < p1; p += 64) {
-            const int q = p + lane;
-            const int e = q < p1 ? a.ids[q] : -1;
-            const bool valid = (unsigned)e < (unsigned)E;
-            unsigned long long same = __ballot(valid);
-            for (int bit = 0; (1 << bit) < E; ++bit) {
-                const bool set = (e >> bit) & 1;
-                const unsigned long long m = __ballot(set);
-                same &= set ? m : ~m;
-            }
-            const int rank = __popcll(same & ((1ull << lane) - 1));
-            int row = -1;
-            if (valid) {
-                const int at = nx[e];
-                row = at + rank;
-                if (rank == 0) nx[e] = at + __popcll(same);
-            }
-            if (q < p1) {
-                row_of[q - p0] = row;
-                if (a.pos) a.pos[q] = row;
-                if (valid) {
-                    a.src[row] = q;
-                    if (a.expert) a.expert[row] = e;
-                }
-            }
-        }
-    }
-    // rows behind the last
-    for (int p = p0 + tid; p < p1; p += kThreads)
-        if (p >= n_rows) {
-            a.src[p] = -1;
-            if (a.expert) a.expert[p] = -1;
-        }
+    order_picks<EM>(a, blockIdx.x, tokens, counts, slices, per, o);
     if (!x) return;
     __syncthreads();
 
@@ -205,7 +68,7 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int token
             for (int u = 0; u < 4; ++u) {
                 if (t + u * groups >= t1) break;
                 for (int j = 0; j < a.k; ++j) {
-                    const int row = row_of[(t + u * groups - t0) * a.k + j];
+                    const int row = o.row_of[(t + u * groups - t0) * a.k + j];
                     if (row >= 0) store_piece(rows + (int64_t)row * a.ld_rows, v[u], n);
                 }
             }
