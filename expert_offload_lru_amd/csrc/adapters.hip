@@ -10,7 +10,6 @@ namespace moe {
 namespace {
 
 constexpr int kRowCalls = 512;    // rows of a call that takes a workgroup a row
-constexpr int kTallRows = 4096;   // rows from which blocks are 32 rows high
 constexpr int kRowTarget = 512;   // workgroups of such a call: two a CU
 
 // Eight elements at p (n of them there, zeros behind), as loaded and as fp32.
@@ -135,9 +134,7 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kTileThreads = 512;
-constexpr int kTileWaves = kTileThreads / 64;
-constexpr int kMostRows = 64;   // rows of a block
+constexpr int kMostRows = 32;   // rows of a block
 constexpr unsigned kNowhere = 0x80000000u;                   // an offset out of every buffer's range
 constexpr int64_t kBufferBytes = (int64_t)kNowhere - 65536;   // a buffer's size at most
 
@@ -342,14 +339,10 @@ struct ShrinkArgs {
 };
 
 // 16 MT rows a workgroup, for each adapter among them: the reduction split over the waves and joined in
-// LDS.  So that a block with several adapters does not end a whole turn after the rest:
-//  - with few blocks, a block's adapters are dealt to the workgroups of blockIdx.y, the first adapter's
-//    behind all others (one without an adapter ends when it has seen the numbers);
-//  - with many blocks (a full grid of such workgroups would cost more than it saves), the first `helpers`
-//    workgroups look through kHelped blocks each and do their second adapters; the others leave those out.
-constexpr int kHelped = 8;
+// LDS.  A block's adapters are dealt to the workgroups of blockIdx.y (one without an adapter ends when it
+// has seen the numbers), so that a block with several does not end a whole turn after the rest.
 template <typename TX, typename TW, int NT, int MT, int WAVES, bool TILED>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4))) void k_shrink(ShrinkArgs g, int helpers) {
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4))) void k_shrink(ShrinkArgs g) {
     constexpr int kPart = 256 * NT * MT;
     __shared__ __align__(16) float part[WAVES * kPart];
     const ShrinkJob &job = g.job[blockIdx.z];
@@ -358,16 +351,6 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4)))
     x.row = l.l16 * (unsigned)job.ld * sizeof(TX);
     x.step = 16 * (unsigned)job.ld * sizeof(TX);
     x.cols = job.cols;
-    // the rows of e's adapter `now`, which are taken out of e
-    auto take = [&](int (&e)[MT], int now) {
-        unsigned long long rows = 0;
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            rows |= (__ballot(e[j] == now) & 0xFFFFull) << (16 * j);
-            if (e[j] == now) e[j] = -1;
-        }
-        return rows;
-    };
     auto product = [&](int row0, int now, unsigned long long rows) __attribute__((always_inline)) {
         int r = g.r;
         asm volatile("" : "+s"(r));
@@ -387,35 +370,19 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4)))
             __syncthreads();
         }
     };
-    const int turns = gridDim.y, turn = turns - 1 - blockIdx.y;
-    const bool helper = (int)blockIdx.x < helpers;
-    int row0 = (helper ? blockIdx.x * kHelped : blockIdx.x - helpers) * 16 * MT, e[MT];
-    if (helper) {
-        int ahead[kHelped][MT];
-#pragma unroll
-        for (int i = 0; i < kHelped; ++i) adapters_of(g.adapter, row0 + i * 16 * MT + l.l16, g.T, g.n, ahead[i]);
-#pragma unroll 1
-        for (int i = 0; i < kHelped; ++i, row0 += 16 * MT) {
-            if (row0 >= g.T) return;
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                e[j] = ahead[0][j];
-#pragma unroll
-                for (int k = 1; k < kHelped; ++k) e[j] = i == k ? ahead[k][j] : e[j];
-            }
-            take(e, next_adapter(e));
-            const int now = next_adapter(e);
-            if (now >= 0) product(row0, now, take(e, now));
-        }
-        return;
-    }
+    const int turns = gridDim.y, turn = blockIdx.y, row0 = blockIdx.x * 16 * MT;
+    int e[MT];
     adapters_of(g.adapter, row0 + l.l16, g.T, g.n, e);
     int seen = 0;
     for (int now = next_adapter(e); now >= 0; now = next_adapter(e)) {
-        const unsigned long long rows = take(e, now);
-        const int k = seen++;
-        if (helpers ? k == 1 : k % turns != turn) continue;
-        product(row0, now, rows);
+        // its rows, taken out of e
+        unsigned long long rows = 0;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            rows |= (__ballot(e[j] == now) & 0xFFFFull) << (16 * j);
+            if (e[j] == now) e[j] = -1;
+        }
+        if (seen++ % turns == turn) product(row0, now, rows);
     }
 }
 
@@ -1078,13 +1045,11 @@ bool piecewise_adapter(const void *a, int64_t inner, int64_t outer, int64_t rp, 
 template <typename TX, typename TW, int MT, int WAVES, bool TILED>
 hipError_t shrink(const ShrinkArgs &g, int jobs, hipStream_t stream) {
     const int tiles = (g.T + 16 * MT - 1) / (16 * MT);
-    const bool many = tiles >= 256 && g.n > 1;
-    const int helpers = many ? (tiles + kHelped - 1) / kHelped : 0;
-    const int turns = many ? 1 : std::min(g.n, std::max(2, std::min(16, 1024 / tiles)));
-    const dim3 grid(helpers + tiles, turns, jobs), block(64 * WAVES);
-    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, helpers);
-    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, helpers);
-    return launch(k_shrink<TX, TW, 4, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, helpers);
+    const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / tiles)));
+    const dim3 grid(tiles, turns, jobs), block(64 * WAVES);
+    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g);
+    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g);
+    return launch(k_shrink<TX, TW, 4, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g);
 }
 
 template <typename TX, typename TW, int MT>
@@ -1101,11 +1066,12 @@ hipError_t expand(ExpandArgs g, hipStream_t stream) {
     return launch(k_expand<TX, TW, 2, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
 }
 
+constexpr int64_t kTallWork = 1 << 17;
 // Both products of a call.  A block of 32 rows instead of 16 halves the reads of the adapters' matrices
 // from L2, and the number of workgroups: worth it from rank 17 (shrink) on, with enough rows.
 template <typename TX, typename TW, bool TILED>
 hipError_t products(const ShrinkArgs &sa, int jobs, const ExpandArgs &ea, hipStream_t stream) {
-    const bool tall = sa.r > 16 && sa.T >= kTallRows;
+    const bool tall = sa.r > 16 && (int64_t)sa.r * sa.T >= kTallWork * (TILED ? 4 : 1);
     const hipError_t err = !tall          ? shrink<TX, TW, 1, 8, TILED>(sa, jobs, stream)
                            : sa.r <= 32 ? shrink<TX, TW, 2, 8, TILED>(sa, jobs, stream)
                                         : shrink<TX, TW, 2, 16, TILED>(sa, jobs, stream);

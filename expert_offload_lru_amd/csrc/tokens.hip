@@ -11,15 +11,15 @@
 namespace moe {
 namespace {
 
-constexpr int kDirectPicks = 4096;    // up to here every workgroup counts all picks itself, and up to
-constexpr int kDirectOrder = 32768;   // here where it makes the order alone, in few workgroups
+constexpr int kDirectPicks = 8192;    // up to here every workgroup counts all picks itself
 constexpr int kSlicePicks = 2048;     // picks of a histogram slice above, at least
 constexpr int kMaxSlices = 64;
+constexpr int kLongSlice = 32768, kMostSlices = 512;
 constexpr int kWgTarget = 1024;       // workgroups of a dispatch that copies rows: four a CU
 
-int slices_of(int N, bool rows) {
-    if (N <= (rows ? kDirectPicks : kDirectOrder)) return 0;
-    return std::min(kMaxSlices, (N + kSlicePicks - 1) / kSlicePicks);
+int slices_of(int N) {
+    if (N <= kDirectPicks) return 0;
+    return std::max(std::min(kMaxSlices, (N + kSlicePicks - 1) / kSlicePicks), std::min(kMostSlices, N / kLongSlice));
 }
 int per_slice(int N, int slices) { return (N + slices - 1) / slices; }
 
@@ -192,7 +192,7 @@ int vec_of(int dtype) { return dtype == T_F32 ? 4 : 8; }
 template <typename T>
 hipError_t dispatch(const DispatchArgs &a, int32_t *counts, hipStream_t stream) {
     const int N = a.T * a.k;
-    const int slices = slices_of(N, a.x != nullptr), per = slices ? per_slice(N, slices) : 1;
+    const int slices = slices_of(N), per = slices ? per_slice(N, slices) : 1;
     if (slices) {
         const hipError_t e = launch(k_slice_counts, dim3(slices), dim3(kThreads), stream, nullptr, nullptr, a.ids, N, per,
                                     a.E, counts);
@@ -210,7 +210,7 @@ hipError_t dispatch(const DispatchArgs &a, int32_t *counts, hipStream_t stream) 
 
 }  // namespace
 
-size_t dispatch_workspace(int T, int k, int E) { return (size_t)slices_of(T * k, true) * E * sizeof(int32_t); }
+size_t dispatch_workspace(int T, int k, int E) { return (size_t)slices_of(T * k) * E * sizeof(int32_t); }
 
 hipError_t launch_dispatch(int dtype, const DispatchArgs &a, void *workspace, hipStream_t stream) {
     int32_t *counts = static_cast<int32_t *>(workspace);

@@ -10,8 +10,9 @@ import functools
 
 import torch
 
-from . import ERR_INVALID, OK, T_BF16, T_F16, T_F32, MoeError, gpu_lib
+from . import ERR_INVALID, ERR_UNSUPPORTED, OK, T_BF16, T_F16, T_F32, MoeError, gpu_lib
 
+_INT_MAX = 2 ** 31 - 1   # of the C sizes: ctypes would cut a larger number
 _TYPES = {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16}
 
 # torch.cuda.current_device() and .current_stream().cuda_stream without their Python layers (about 2 us a call)
@@ -53,6 +54,8 @@ def _dims(name, t, n):
     shape = t.shape
     if len(shape) != n:
         _refuse(f"{name} has {len(shape)} dimensions, not {n}")
+    if max(shape) > _INT_MAX:
+        raise MoeError(ERR_UNSUPPORTED, f"{name} has a size over {_INT_MAX}")
     return shape
 
 
@@ -115,6 +118,8 @@ def tokens_dispatch(x, ids, n_experts, rows, offsets, pos, src, expert, workspac
         _refuse(f"ids is on {ids.device}, not a GPU")
     T, k = _dims("ids", ids, 2)
     n = T * k
+    if n_experts > _INT_MAX:
+        raise MoeError(ERR_UNSUPPORTED, f"n_experts is over {_INT_MAX}")
     if (x is None) != (rows is None):
         _refuse("x and rows go together")
     i32 = torch.int32

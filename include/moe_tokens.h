@@ -15,11 +15,14 @@
  *  - dtype (MOE_T_*) is the type of every tensor without a type of its own; gates, scales and the
  *    adapters' gradients are fp32, indexes int32.  Sums are held in fp32 and rounded once.
  *  - Matrices are row-major; ld is the number of elements from one row to the next (>= the row's
- *    length).  No alignment beyond the element's own is needed.
+ *    length).  No alignment beyond the element's own is needed; rows that start at multiples of 16
+ *    bytes are the fast case (an adapters' backward call with others is many times slower).
  *  - An output may not overlap an input or another output, but out may be base (the same pointer and
- *    ld), and d_x may be dx_base.  Errors: MOE_ERR_INVALID (a NULL or overlapping tensor, a size or
+ *    ld), and d_x may be dx_base.  A matrix is taken as all from its first to its last element: two
+ *    column ranges of one wider matrix overlap.  Errors: MOE_ERR_INVALID (a NULL or overlapping tensor, a size or
  *    ld out of range, an unknown type, a workspace that is too small), MOE_ERR_UNSUPPORTED (a size
- *    over the limits stated), MOE_ERR_HIP (a launch failed).  Nothing is enqueued on an error.
+ *    over the limits stated), both before anything is enqueued, and MOE_ERR_HIP (a launch failed; the
+ *    kernels before it may run).
  *  - Index values are checked on the device: one out of range counts as "none".
  *  - Results do not depend on timing: the same inputs give the same bits.
  */

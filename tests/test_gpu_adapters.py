@@ -36,6 +36,9 @@ SHAPES = [
     (5000, 3, 48, 64, 64, "f32", "bf16", "runs"),
     (4100, 5, 100, 64, 136, "bf16", "bf16", "mixed"),
     (4111, 300, 32, 65, 64, "bf16", "bf16", "mixed"),
+    (16500, 3, 24, 64, 64, "bf16", "bf16", "runs"),
+    (33000, 5, 4, 24, 16, "bf16", "bf16", "mixed"),
+    (9000, 270, 64, 64, 16, "f16", "f16", "runs"),
 ]
 
 
@@ -267,6 +270,7 @@ def test_refusals():
     refused(x=s["x"][0])
     refused(out=out[:, :20])
     refused(out=torch.empty(24, 6, dtype=torch.bfloat16, device="cuda").t())
+    refused(code=moe.ERR_UNSUPPORTED, x=s["x"][:1].expand(2 ** 32 + 6, 16))   # a size that 32 bits would cut to 6
     wide = torch.empty(6, 40, dtype=torch.bfloat16, device="cuda")
     refused(out=wide[:, :24], x=wide[:, 24:])                   # rows that interleave count as overlapping
     refused(code=moe.ERR_UNSUPPORTED, a=torch.zeros(2, 257, 16, dtype=torch.bfloat16, device="cuda"),

@@ -1,5 +1,6 @@
 """Argument checks of include/moe_tokens.h that return before any HIP call (CPU): addresses are only compared."""
 import pytest
+import torch
 
 import expert_offload_lru_amd as moe
 from test_capi_symbols import _declared, _exported
@@ -99,3 +100,13 @@ def test_workspaces():
     assert lib.moe_adapters_workspace(0, 8, 8, 4, 4) > 0
     assert lib.moe_adapters_forward_workspace(32, 2048, 2048, 8, 16) == 0
     assert lib.moe_adapters_forward_workspace(8192, 2048, 2048, 8, 16) >= 8192 * 16 * 4
+
+
+def test_sizes_that_the_library_cannot_hold():
+    """Checked before ctypes cuts them to 32 bits."""
+    from expert_offload_lru_amd import tokens
+    assert tuple(tokens._dims("t", torch.zeros(1, 1).expand(2 ** 31 - 1, 5), 2)) == (2 ** 31 - 1, 5)
+    for shape in ((2 ** 31, 1), (1, 2 ** 32 + 4)):
+        with pytest.raises(moe.MoeError) as e:
+            tokens._dims("t", torch.zeros(1, 1).expand(shape), 2)
+        assert e.value.code == UNS
