@@ -170,11 +170,11 @@ def _declare_gpu(lib):
     lib.moe_tokens_dispatch_backward.argtypes = [vp, ld, ld, i, i, i, vp, i, vp, ld, vp]
     lib.moe_tokens_combine.argtypes = [vp, ld, ld, i, i, i, vp, vp, i, vp, ld, vp, ld, vp]
     lib.moe_tokens_combine_backward.argtypes = [vp, ld, vp, ld, ld, i, i, i, vp, vp, i, vp, ld, vp, vp]
-    lib.moe_adapters_forward_workspace.argtypes = [i, i, i, i, i]
-    lib.moe_adapters_forward_workspace.restype = sz
+    for name in ("moe_adapters_forward_workspace", "moe_adapters_workspace"):
+        for fn in (getattr(lib, name), getattr(lib, name + "_strided")):
+            fn.argtypes = [i, i, i, i, i]
+            fn.restype = sz
     lib.moe_adapters_forward.argtypes = [vp, ld, vp, ld, i, i, i, i, vp, vp, vp, i, vp, i, i, vp, ld, vp, sz, vp]
-    lib.moe_adapters_workspace.argtypes = [i, i, i, i, i]
-    lib.moe_adapters_workspace.restype = sz
     lib.moe_adapters_backward.argtypes = [vp, ld, vp, ld, vp, ld, i, i, i, i, vp, vp, vp, i, vp, i, i, vp, ld, vp, vp,
                                           vp, sz, vp]
 

@@ -426,12 +426,12 @@ struct Left {
 
 // out = base + v w^T, w a row's own adapter's: the forward's B, the backward's A transposed.
 struct ExpandArgs {
-    const void *base, *w;   // [T x cols] or null; [n x cols x wr]
+    const void *base, *w;   // [T x cols] or null; [n x w_rows x wr], zeros from w_rows on to cols
     void *out;
     const float *v;         // [T x vr]
     const int32_t *adapter;
     int64_t ld_base, ld_out;
-    int T, cols, n, wr, vr, groups;   // groups: of 64 columns, that a wave takes
+    int T, cols, n, w_rows, wr, vr, groups;   // groups: of 64 columns, that a wave takes
 };
 
 // 16 MT rows and a few groups of 64 columns a wave, without a barrier: bound by reading base and writing
@@ -498,7 +498,7 @@ __global__ __launch_bounds__(kThreads) void k_expand(ExpandArgs g, int col_wgs) 
         }
     }
     auto weights = [&](int now) {
-        return buffer(static_cast<const TW *>(g.w) + (size_t)now * g.cols * g.wr, (size_t)g.cols * g.wr * sizeof(TW));
+        return buffer(static_cast<const TW *>(g.w) + (size_t)now * g.w_rows * g.wr, (size_t)g.w_rows * g.wr * sizeof(TW));
     };
     auto load_weights = [&](Chunk<TX, TW> (&a)[4], Buffer w, int c0, int b) __attribute__((always_inline)) {
         const int q = b * kBlock + l.quad * C;
@@ -714,25 +714,45 @@ __global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW 
     }
 }
 
-// Up to three matrices copied row by row to another row distance and width: zeros behind the narrower
-// source (and for a missing one).
-struct Reshape {
-    const void *from[3];
-    void *to[3];
-    int64_t ld_from[3], ld_to[3];
-    int cols_from[3], cols_to[3];
+// Matrices copied row by row to another row distance and width: zeros behind the narrower source (and for
+// a missing one).
+struct Copy {
+    const void *from;
+    void *to;
+    int64_t ld_from, ld_to;
+    int cols_from, cols_to, rows;
+    bool weights;   // of the weights' type
 };
-template <typename TX>
-__global__ __launch_bounds__(kThreads) void k_reshape(Reshape g, int rows) {
-    const int m = blockIdx.y;
-    for (int row = blockIdx.x * 4 + ((int)threadIdx.x >> 6); row < rows; row += gridDim.x * 4) {
-        const TX *from = static_cast<const TX *>(g.from[m]) + row * g.ld_from[m];
-        TX *to = static_cast<TX *>(g.to[m]) + row * g.ld_to[m];
-        for (int c = (threadIdx.x & 63) * kVec<TX>; c < g.cols_to[m]; c += 64 * kVec<TX>) {
-            const uint4 v = g.from[m] && c < g.cols_from[m] ? load_piece(from + c, g.cols_from[m] - c) : uint4{0, 0, 0, 0};
-            store_piece(to + c, v, g.cols_to[m] - c);
+struct Reshape {
+    Copy copy[4];
+    int n;
+    void add(Copy c) { copy[n++] = c; }
+};
+template <typename T>
+__device__ __forceinline__ void copy_rows(const Copy &g) {
+    for (int row = blockIdx.x * 4 + ((int)threadIdx.x >> 6); row < g.rows; row += gridDim.x * 4) {
+        const T *from = static_cast<const T *>(g.from) + row * g.ld_from;
+        T *to = static_cast<T *>(g.to) + row * g.ld_to;
+        for (int c = (threadIdx.x & 63) * kVec<T>; c < g.cols_to; c += 64 * kVec<T>) {
+            const uint4 v = g.from && c < g.cols_from ? load_piece(from + c, g.cols_from - c) : uint4{0, 0, 0, 0};
+            store_piece(to + c, v, g.cols_to - c);
         }
     }
+}
+template <typename TX, typename TW>
+__global__ __launch_bounds__(kThreads) void k_reshape(Reshape g) {
+    const Copy &c = g.copy[blockIdx.y];
+    if (c.weights)
+        copy_rows<TW>(c);
+    else
+        copy_rows<TX>(c);
+}
+template <typename TX, typename TW>
+hipError_t reshape(const Reshape &g, hipStream_t stream) {
+    if (g.n == 0) return hipSuccess;
+    int rows = 0;
+    for (int i = 0; i < g.n; ++i) rows = std::max(rows, g.copy[i].rows);
+    return launch(k_reshape<TX, TW>, dim3(std::min((rows + 3) / 4, 2048), g.n), dim3(kThreads), stream, nullptr, nullptr, g);
 }
 
 // An adapter's rows, in their sorted order, are cut into pieces of `rows`; pieces are numbered through.
@@ -979,15 +999,15 @@ __global__ __launch_bounds__(kThreads) void k_back_join(BackWeights g) {
 // point does not ask for the types).
 struct BackSpace {
     int ip, op, rp, piece_rows, max_pieces;
-    bool padded;   // rows are copied to whole pieces of 8 elements
+    bool padded;   // rows are copied to whole, aligned pieces of 8 elements: odd sizes, or if asked for
     size_t offsets, order, sort, v, u, at, aw, bw, partial, x, d_out, d_x, bytes;
 };
-BackSpace back_space(int T, int inner, int outer, int n, int r) {
+BackSpace back_space(int T, int inner, int outer, int n, int r, bool copies) {
     BackSpace s;
     s.ip = (inner + 7) / 8 * 8;
     s.op = (outer + 7) / 8 * 8;
     s.rp = (r + 7) / 8 * 8;
-    s.padded = s.ip != inner || s.op != outer;
+    s.padded = copies || s.ip != inner || s.op != outer;
     // pieces such that their workgroups are about two and a half rounds of the chip's CUs
     const int64_t tiles = (s.ip + kPieceCols - 1) / kPieceCols + (s.op + kPieceCols - 1) / kPieceCols;
     s.piece_rows = (int)std::min<int64_t>(1 << 24, std::max<int64_t>(128, (T * tiles / 640 + 127) / 128 * 128));
@@ -1016,17 +1036,32 @@ BackSpace back_space(int T, int inner, int outer, int n, int r) {
     return s;
 }
 
-// A forward call of blocks holds v and, where the rank is no multiple of 8, b with its rows padded.
+// A forward call of blocks holds v; b with its rows padded where the rank is no multiple of 8, a where
+// inner is none; and copies of x, and of base and out, as above.
 struct ForwardSpace {
-    int rp;
-    size_t v, b, bytes;
+    int ip, op, rp;
+    bool copy_x, copy_out;
+    size_t v, b, a, x, out, bytes;
 };
-ForwardSpace forward_space(int T, int outer, int n, int r) {
+ForwardSpace forward_space(int T, int inner, int outer, int n, int r, bool copies) {
     ForwardSpace s{};
     if (T <= kRowCalls) return s;
+    s.ip = (inner + 7) / 8 * 8;
+    s.op = (outer + 7) / 8 * 8;
     s.rp = (r + 7) / 8 * 8;
-    s.b = ((size_t)T * s.rp * 4 + 255) & ~(size_t)255;
-    s.bytes = s.b + (s.rp == r ? 0 : (size_t)n * outer * s.rp * 4);
+    s.copy_x = copies || s.ip != inner;
+    s.copy_out = copies || s.op != outer;
+    auto take = [&](size_t bytes) {
+        const size_t here = s.bytes;
+        s.bytes += (bytes + 255) & ~(size_t)255;
+        return here;
+    };
+    const size_t rows = T, adapters = n;
+    s.v = take(rows * s.rp * 4);
+    s.b = take(s.rp == r ? 0 : adapters * outer * s.rp * 4);
+    s.a = take(s.ip == inner ? 0 : adapters * r * s.ip * 4);
+    s.x = take(s.copy_x ? rows * s.ip * 4 : 0);
+    s.out = take(s.copy_out ? rows * s.op * 4 : 0);
     return s;
 }
 
@@ -1036,11 +1071,8 @@ bool piecewise(const void *p, int64_t ld, int cols, size_t size) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && cols * size % 16 == 0 &&
            ((kMostRows - 1) * ld + cols) * (int64_t)size < kBufferBytes;
 }
-// Whether an adapter's matrices, their ranks padded to rp, fit a buffer, and its rows are whole pieces.
-bool piecewise_adapter(const void *a, int64_t inner, int64_t outer, int64_t rp, size_t size) {
-    return reinterpret_cast<uintptr_t>(a) % 16 == 0 && inner % 8 == 0 && outer % 8 == 0 &&
-           rp * std::max(inner, outer) * (int64_t)size < kBufferBytes;
-}
+// Whether an adapter's matrices, as they are laid out, fit a buffer.
+bool fits_buffer(int64_t ip, int64_t op, int64_t rp, size_t size) { return rp * std::max(ip, op) * (int64_t)size < kBufferBytes; }
 
 template <typename TX, typename TW, int MT, int WAVES, bool TILED>
 hipError_t shrink(const ShrinkArgs &g, int jobs, hipStream_t stream) {
@@ -1080,25 +1112,42 @@ hipError_t products(const ShrinkArgs &sa, int jobs, const ExpandArgs &ea, hipStr
 }
 
 template <typename TX, typename TW>
-hipError_t forward(const AdapterArgs &g, void *workspace, hipStream_t stream) {
+hipError_t forward(const AdapterArgs &g, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     constexpr size_t z = sizeof(TX);
-    const ForwardSpace s = forward_space(g.T, g.outer, g.n, g.r);
-    if (s.bytes && piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.out, g.ld_out, g.outer, z) &&
-        (!g.base || piecewise(g.base, g.ld_base, g.outer, z)) && reinterpret_cast<uintptr_t>(g.b) % 16 == 0 &&
-        (int64_t)g.n * g.outer < (1 << 30) && piecewise_adapter(g.a, g.inner, g.outer, s.rp, sizeof(TW))) {
-        float *v = reinterpret_cast<float *>(static_cast<char *>(workspace) + s.v);
-        const void *b = g.b;
-        hipError_t err = hipSuccess;
-        if (s.rp != g.r) {
-            Reshape m{{g.b}, {static_cast<char *>(workspace) + s.b}, {g.r}, {s.rp}, {g.r}, {s.rp}};
-            b = m.to[0];
-            const int rows = g.n * g.outer;
-            err = launch(k_reshape<TW>, dim3(std::min((rows + 3) / 4, 2048), 1), dim3(kThreads), stream, nullptr, nullptr,
-                         m, rows);
-        }
-        const ShrinkArgs sa{{{g.x, g.a, g.ld_x, (int64_t)g.r * g.inner, v, g.inner}}, g.adapter, g.scale, g.T, g.n, g.r, s.rp};
-        const ExpandArgs ea{g.base, b, g.out, v, g.adapter, g.ld_base, g.ld_out, g.T, g.outer, g.n, s.rp, s.rp, 0};
-        return err == hipSuccess ? products<TX, TW, false>(sa, 1, ea, stream) : err;
+    char *ws = static_cast<char *>(workspace);
+    auto fits = [&](const ForwardSpace &s) {
+        return (s.copy_x ? piecewise(ws, s.ip, s.ip, z) : piecewise(g.x, g.ld_x, g.inner, z)) &&
+               (s.copy_out ? piecewise(ws, s.op, s.op, z)
+                           : piecewise(g.out, g.ld_out, g.outer, z) && (!g.base || piecewise(g.base, g.ld_base, g.outer, z)));
+    };
+    ForwardSpace s = forward_space(g.T, g.inner, g.outer, g.n, g.r, false);
+    if (s.bytes && !fits(s)) {
+        const ForwardSpace c = forward_space(g.T, g.inner, g.outer, g.n, g.r, true);
+        if (c.bytes <= workspace_bytes) s = c;
+    }
+    const bool pad_a = s.ip != g.inner, pad_b = s.rp != g.r;
+    if (s.bytes && fits(s) && fits_buffer(s.ip, s.op, s.rp, sizeof(TW)) &&
+        (pad_a || reinterpret_cast<uintptr_t>(g.a) % 16 == 0) && (pad_b || reinterpret_cast<uintptr_t>(g.b) % 16 == 0) &&
+        (int64_t)g.n * std::max(g.outer, g.r) < (1 << 30)) {
+        float *v = reinterpret_cast<float *>(ws + s.v);
+        Reshape m{};
+        if (s.copy_x) m.add({g.x, ws + s.x, g.ld_x, s.ip, g.inner, s.ip, g.T, false});
+        if (s.copy_out) m.add({g.base, ws + s.out, g.ld_base, s.op, g.outer, s.op, g.T, false});
+        if (pad_a) m.add({g.a, ws + s.a, g.inner, s.ip, g.inner, s.ip, g.n * g.r, true});
+        if (pad_b) m.add({g.b, ws + s.b, g.r, s.rp, g.r, s.rp, g.n * g.outer, true});
+        hipError_t err = reshape<TX, TW>(m, stream);
+        if (err != hipSuccess) return err;
+        const void *x = s.copy_x ? ws + s.x : g.x, *a = pad_a ? ws + s.a : g.a, *b = pad_b ? ws + s.b : g.b;
+        void *out = s.copy_out ? ws + s.out : g.out;
+        const void *base = s.copy_out ? out : g.base;
+        const int64_t ld_x = s.copy_x ? s.ip : g.ld_x, ld_out = s.copy_out ? s.op : g.ld_out, ld_base = s.copy_out ? s.op : g.ld_base;
+        const ShrinkArgs sa{{{x, a, ld_x, (int64_t)g.r * s.ip, v, s.ip}}, g.adapter, g.scale, g.T, g.n, g.r, s.rp};
+        const ExpandArgs ea{base, b, out, v, g.adapter, ld_base, ld_out, g.T, s.op, g.n, g.outer, s.rp, s.rp, 0};
+        err = products<TX, TW, false>(sa, 1, ea, stream);
+        if (err != hipSuccess || !s.copy_out) return err;
+        Reshape back{};
+        back.add({out, g.out, s.op, g.ld_out, g.outer, g.outer, g.T, false});
+        return reshape<TX, TW>(back, stream);
     }
     const int groups = (g.outer + kThreads - 1) / kThreads;
     const int slices = std::max(1, std::min(groups, kRowTarget / g.T)), cols = (groups + slices - 1) / slices * kThreads;
@@ -1107,17 +1156,23 @@ hipError_t forward(const AdapterArgs &g, void *workspace, hipStream_t stream) {
 }
 
 template <typename TX, typename TW>
-hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStream_t stream) {
-    const BackSpace s = back_space(g.T, g.inner, g.outer, g.n, g.r);
+hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    constexpr size_t z = sizeof(TX);
     char *ws = static_cast<char *>(workspace);
+    auto fits = [&](const BackSpace &s) {
+        return s.padded ? piecewise(ws, s.ip, s.ip, z) && piecewise(ws, s.op, s.op, z)
+                        : piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.d_out, g.ld_d_out, g.outer, z) &&
+                              piecewise(g.d_x, g.ld_d_x, g.inner, z) &&
+                              (!g.dx_base || piecewise(g.dx_base, g.ld_dx_base, g.inner, z));
+    };
+    BackSpace s = back_space(g.T, g.inner, g.outer, g.n, g.r, false);
+    if (!fits(s)) {
+        const BackSpace c = back_space(g.T, g.inner, g.outer, g.n, g.r, true);
+        if (c.bytes <= workspace_bytes) s = c;
+    }
     int32_t *offsets = reinterpret_cast<int32_t *>(ws + s.offsets), *order = reinterpret_cast<int32_t *>(ws + s.order);
     float *v = reinterpret_cast<float *>(ws + s.v), *u = reinterpret_cast<float *>(ws + s.u);
-    constexpr size_t z = sizeof(TX);
-    const bool blocks =
-        g.T > 0 && piecewise_adapter(workspace, s.ip, s.op, (s.rp + 15) / 16 * 16, sizeof(TW)) &&
-        (s.padded || (piecewise(g.x, g.ld_x, g.inner, z) && piecewise(g.d_out, g.ld_d_out, g.outer, z) &&
-                      piecewise(g.d_x, g.ld_d_x, g.inner, z) &&
-                      (!g.dx_base || piecewise(g.dx_base, g.ld_dx_base, g.inner, z))));
+    const bool blocks = g.T > 0 && fits(s) && fits_buffer(s.ip, s.op, (s.rp + 15) / 16 * 16, sizeof(TW));
     const bool small = blocks && g.T <= kSmallBack;
     DispatchArgs d{};
     d.ids = g.adapter;
@@ -1152,11 +1207,12 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
     const void *x = g.x, *d_out = g.d_out, *dx_base = g.dx_base;
     void *d_x = g.d_x;
     int64_t ld_x = g.ld_x, ld_d_out = g.ld_d_out, ld_dx_base = g.ld_dx_base, ld_d_x = g.ld_d_x;
-    const int copies = std::min((g.T + 3) / 4, 2048);
     if (s.padded) {
-        Reshape m{{g.x, g.d_out, g.dx_base}, {ws + s.x, ws + s.d_out, ws + s.d_x}, {g.ld_x, g.ld_d_out, g.ld_dx_base},
-                  {s.ip, s.op, s.ip}, {g.inner, g.outer, g.inner}, {s.ip, s.op, s.ip}};
-        err = launch(k_reshape<TX>, dim3(copies, 3), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
+        Reshape m{};
+        m.add({g.x, ws + s.x, g.ld_x, s.ip, g.inner, s.ip, g.T, false});
+        m.add({g.d_out, ws + s.d_out, g.ld_d_out, s.op, g.outer, s.op, g.T, false});
+        m.add({g.dx_base, ws + s.d_x, g.ld_dx_base, s.ip, g.inner, s.ip, g.T, false});
+        err = reshape<TX, TW>(m, stream);
         if (err != hipSuccess) return err;
         x = ws + s.x;
         d_out = ws + s.d_out;
@@ -1167,11 +1223,12 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
     const ShrinkArgs sa{{{x, aw, ld_x, (int64_t)tiled_size(g.r, g.inner, C), v, s.ip},
                          {d_out, bw, ld_d_out, (int64_t)tiled_size(g.r, g.outer, C), u, s.op}},
                         g.adapter, g.scale, g.T, g.n, g.r, s.rp};
-    err = products<TX, TW, true>(sa, 2, {dx_base, at, d_x, u, g.adapter, ld_dx_base, ld_d_x, g.T, s.ip, g.n, s.rp, s.rp, 0}, stream);
+    err = products<TX, TW, true>(sa, 2, {dx_base, at, d_x, u, g.adapter, ld_dx_base, ld_d_x, g.T, s.ip, g.n, s.ip, s.rp, s.rp, 0}, stream);
     if (err != hipSuccess) return err;
     if (s.padded) {
-        Reshape m{{d_x}, {g.d_x}, {s.ip}, {g.ld_d_x}, {g.inner}, {g.inner}};
-        err = launch(k_reshape<TX>, dim3(copies, 1), dim3(kThreads), stream, nullptr, nullptr, m, g.T);
+        Reshape m{};
+        m.add({d_x, g.d_x, s.ip, g.ld_d_x, g.inner, g.inner, g.T, false});
+        err = reshape<TX, TW>(m, stream);
         if (err != hipSuccess) return err;
     }
     const BackWeights w{g.adapter, x, d_out, ld_x, ld_d_out, offsets, order, v, u, reinterpret_cast<float *>(ws + s.partial),
@@ -1194,24 +1251,29 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, hipStr
 
 }  // namespace
 
-size_t adapters_forward_workspace(int T, int outer, int n, int r) { return forward_space(T, outer, n, r).bytes; }
-size_t adapters_workspace(int T, int inner, int outer, int n, int r) { return back_space(T, inner, outer, n, r).bytes; }
-
-hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &g, void *workspace, hipStream_t stream) {
-    if (g.T == 0) return hipSuccess;
-    if (dtype == T_F16) return forward<f16, f16>(g, workspace, stream);
-    if (dtype == T_BF16) return forward<bf16, bf16>(g, workspace, stream);
-    if (wtype == T_F16) return forward<float, f16>(g, workspace, stream);
-    if (wtype == T_BF16) return forward<float, bf16>(g, workspace, stream);
-    return forward<float, float>(g, workspace, stream);
+size_t adapters_forward_workspace(int T, int inner, int outer, int n, int r, bool copies) {
+    return forward_space(T, inner, outer, n, r, copies).bytes;
+}
+size_t adapters_workspace(int T, int inner, int outer, int n, int r, bool copies) {
+    return back_space(T, inner, outer, n, r, copies).bytes;
 }
 
-hipError_t launch_adapters_back(int dtype, int wtype, const AdapterBackArgs &g, void *workspace, hipStream_t stream) {
-    if (dtype == T_F16) return backward<f16, f16>(dtype, g, workspace, stream);
-    if (dtype == T_BF16) return backward<bf16, bf16>(dtype, g, workspace, stream);
-    if (wtype == T_F16) return backward<float, f16>(dtype, g, workspace, stream);
-    if (wtype == T_BF16) return backward<float, bf16>(dtype, g, workspace, stream);
-    return backward<float, float>(dtype, g, workspace, stream);
+hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &g, void *workspace, size_t bytes, hipStream_t stream) {
+    if (g.T == 0) return hipSuccess;
+    if (dtype == T_F16) return forward<f16, f16>(g, workspace, bytes, stream);
+    if (dtype == T_BF16) return forward<bf16, bf16>(g, workspace, bytes, stream);
+    if (wtype == T_F16) return forward<float, f16>(g, workspace, bytes, stream);
+    if (wtype == T_BF16) return forward<float, bf16>(g, workspace, bytes, stream);
+    return forward<float, float>(g, workspace, bytes, stream);
+}
+
+hipError_t launch_adapters_back(int dtype, int wtype, const AdapterBackArgs &g, void *workspace, size_t bytes,
+                                hipStream_t stream) {
+    if (dtype == T_F16) return backward<f16, f16>(dtype, g, workspace, bytes, stream);
+    if (dtype == T_BF16) return backward<bf16, bf16>(dtype, g, workspace, bytes, stream);
+    if (wtype == T_F16) return backward<float, f16>(dtype, g, workspace, bytes, stream);
+    if (wtype == T_BF16) return backward<float, bf16>(dtype, g, workspace, bytes, stream);
+    return backward<float, float>(dtype, g, workspace, bytes, stream);
 }
 
 }  // namespace moe

@@ -54,8 +54,9 @@ struct AdapterArgs {
     const float *scale;
     int T, inner, outer, n, r;
 };
-size_t adapters_forward_workspace(int T, int outer, int n, int r);
-hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &a, void *workspace, hipStream_t stream);
+// Bytes of workspace; copies: with room for copies of matrices whose rows are not aligned.
+size_t adapters_forward_workspace(int T, int inner, int outer, int n, int r, bool copies);
+hipError_t launch_adapters(int dtype, int wtype, const AdapterArgs &a, void *workspace, size_t bytes, hipStream_t stream);
 
 struct AdapterBackArgs {
     const void *d_out, *x, *dx_base;
@@ -67,7 +68,7 @@ struct AdapterBackArgs {
     float *d_a, *d_b;
     int T, inner, outer, n, r;
 };
-size_t adapters_workspace(int T, int inner, int outer, int n, int r);
-hipError_t launch_adapters_back(int dtype, int wtype, const AdapterBackArgs &a, void *workspace, hipStream_t stream);
+size_t adapters_workspace(int T, int inner, int outer, int n, int r, bool copies);
+hipError_t launch_adapters_back(int dtype, int wtype, const AdapterBackArgs &a, void *workspace, size_t bytes, hipStream_t stream);
 
 }  // namespace moe

@@ -81,6 +81,16 @@ int check_adapters(int dtype, int wtype, int n_rows, int inner, int outer, int n
     return MOE_OK;
 }
 
+size_t forward_bytes(int n_rows, int inner, int outer, int n_adapters, int rank, bool copies) {
+    if (check_adapters(MOE_T_F32, MOE_T_F32, n_rows, inner, outer, n_adapters, rank) != MOE_OK) return 0;
+    return adapters_forward_workspace(n_rows, inner, outer, n_adapters, rank, copies);
+}
+
+size_t backward_bytes(int n_rows, int inner, int outer, int n_adapters, int rank, bool copies) {
+    if (check_adapters(MOE_T_F32, MOE_T_F32, n_rows, inner, outer, n_adapters, rank) != MOE_OK) return 0;
+    return n_adapters > kMaxSegments ? 0 : adapters_workspace(n_rows, inner, outer, n_adapters, rank, copies);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -194,8 +204,11 @@ int moe_tokens_combine_backward(const void *d_out, int64_t ld_d_out, const void 
 }
 
 size_t moe_adapters_forward_workspace(int n_rows, int inner, int outer, int n_adapters, int rank) {
-    if (check_adapters(MOE_T_F32, MOE_T_F32, n_rows, inner, outer, n_adapters, rank) != MOE_OK) return 0;
-    return adapters_forward_workspace(n_rows, outer, n_adapters, rank);
+    return forward_bytes(n_rows, inner, outer, n_adapters, rank, false);
+}
+
+size_t moe_adapters_forward_workspace_strided(int n_rows, int inner, int outer, int n_adapters, int rank) {
+    return forward_bytes(n_rows, inner, outer, n_adapters, rank, true);
 }
 
 int moe_adapters_forward(const void *x, int64_t ld_x, const void *base, int64_t ld_base, int dtype, int n_rows, int inner,
@@ -210,22 +223,25 @@ int moe_adapters_forward(const void *x, int64_t ld_x, const void *base, int64_t 
     MOE_TRY(check_ld("out", out, ld_out, outer));
     const size_t z = elem_size(dtype), zw = elem_size(wtype);
     const bool in_place = base == out && ld_base == ld_out;
-    const size_t need = adapters_forward_workspace(n_rows, outer, n_adapters, rank);
+    const size_t need = adapters_forward_workspace(n_rows, inner, outer, n_adapters, rank, false);
+    const size_t most = std::min(workspace_bytes, adapters_forward_workspace(n_rows, inner, outer, n_adapters, rank, true));
     if (need && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16))
         return invalid("the workspace is too small or not aligned");
-    MOE_TRY(check_overlap({matrix("out", out, n_rows, outer, ld_out, z), array("workspace", workspace, need, 1)},
+    MOE_TRY(check_overlap({matrix("out", out, n_rows, outer, ld_out, z), array("workspace", workspace, most, 1)},
                           {matrix("x", x, n_rows, inner, ld_x, z),
                            matrix("base", in_place ? nullptr : base, n_rows, outer, ld_base, z),
                            array("adapter", adapter, n_rows), array("a", a, (int64_t)n_adapters * rank * inner, zw),
                            array("b", b, (int64_t)n_adapters * rank * outer, zw), array("scale", scale, n_adapters)}));
     AdapterArgs g{x, base, out, ld_x, ld_base, ld_out, adapter, a, b, scale, n_rows, inner, outer, n_adapters, rank};
-    return finish(launch_adapters(dtype, wtype, g, workspace, static_cast<hipStream_t>(stream)));
+    return finish(launch_adapters(dtype, wtype, g, workspace, most, static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_adapters_workspace(int n_rows, int inner, int outer, int n_adapters, int rank) {
-    if (check_adapters(MOE_T_F32, MOE_T_F32, n_rows, inner, outer, n_adapters, rank) != MOE_OK) return 0;
-    if (n_adapters > kMaxSegments) return 0;
-    return adapters_workspace(n_rows, inner, outer, n_adapters, rank);
+    return backward_bytes(n_rows, inner, outer, n_adapters, rank, false);
+}
+
+size_t moe_adapters_workspace_strided(int n_rows, int inner, int outer, int n_adapters, int rank) {
+    return backward_bytes(n_rows, inner, outer, n_adapters, rank, true);
 }
 
 int moe_adapters_backward(const void *d_out, int64_t ld_d_out, const void *x, int64_t ld_x, const void *dx_base,
@@ -240,21 +256,22 @@ int moe_adapters_backward(const void *d_out, int64_t ld_d_out, const void *x, in
     MOE_TRY(check_ld("x", x, ld_x, inner));
     MOE_TRY(check_ld("dx_base", dx_base, ld_dx_base, inner));
     MOE_TRY(check_ld("d_x", d_x, ld_d_x, inner));
-    const size_t need = adapters_workspace(n_rows, inner, outer, n_adapters, rank);
+    const size_t need = adapters_workspace(n_rows, inner, outer, n_adapters, rank, false);
+    const size_t most = std::min(workspace_bytes, adapters_workspace(n_rows, inner, outer, n_adapters, rank, true));
     if (need && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16))
         return invalid("the workspace is too small or not aligned");
     const size_t z = elem_size(dtype), zw = elem_size(wtype);
     const int64_t na = (int64_t)n_adapters * rank * inner, nb = (int64_t)n_adapters * rank * outer;
     const bool in_place = dx_base == d_x && ld_dx_base == ld_d_x;
     MOE_TRY(check_overlap({matrix("d_x", d_x, n_rows, inner, ld_d_x, z), array("d_a", d_a, na), array("d_b", d_b, nb),
-                           array("workspace", workspace, need, 1)},
+                           array("workspace", workspace, most, 1)},
                           {matrix("d_out", d_out, n_rows, outer, ld_d_out, z), matrix("x", x, n_rows, inner, ld_x, z),
                            matrix("dx_base", in_place ? nullptr : dx_base, n_rows, inner, ld_dx_base, z),
                            array("adapter", adapter, n_rows), array("a", a, na, zw), array("b", b, nb, zw),
                            array("scale", scale, n_adapters)}));
     AdapterBackArgs g{d_out, x, dx_base, d_x, ld_d_out, ld_x, ld_dx_base, ld_d_x, adapter, a, b, scale, d_a, d_b, n_rows,
                       inner, outer, n_adapters, rank};
-    return finish(launch_adapters_back(dtype, wtype, g, workspace, static_cast<hipStream_t>(stream)));
+    return finish(launch_adapters_back(dtype, wtype, g, workspace, most, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

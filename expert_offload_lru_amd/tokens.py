@@ -188,7 +188,8 @@ def adapters_forward(x, adapter, a, b, scale, out, base=None, workspace=None, st
     x [T, inner], adapter int32 [T] (-1: none), a [n, r, inner], b [n, outer, r], scale fp32 [n], out
     and base [T, outer]; base may be out, and None stands for zeros.  a and b have x's type, or any
     type beside fp32 activations.  A call of many rows needs a workspace: the caller's (any contiguous
-    tensor of enough bytes, 16-byte aligned) or one of its own.
+    tensor of enough bytes, 16-byte aligned) or one of its own,
+    with room for copies where rows do not start at multiples of 16 bytes.
     """
     lib = gpu_lib()
     (dtype, gpu), T = _type("x", x), _dims("x", x, 2)[0]
@@ -198,7 +199,9 @@ def adapters_forward(x, adapter, a, b, scale, out, base=None, workspace=None, st
     p_base, ldb = (None, outer) if base is None else _matrix("base", base, T, outer, x.dtype, gpu)
     p_ad = _array("adapter", adapter, (T,), torch.int32, gpu)
     p_scale = _array("scale", scale, (n,), torch.float32, gpu)
-    need = _needed("moe_adapters_forward_workspace", T, inner, outer, n, r)
+    strided = (px | po | (p_base or 0) | (ldx | ldo | ldb) * x.element_size()) & 15
+    need = _needed("moe_adapters_forward_workspace_strided" if strided and workspace is None else
+                   "moe_adapters_forward_workspace", T, inner, outer, n, r)
     ws = _workspace(need, workspace, gpu, stream) if need else None
     _call(lib.moe_adapters_forward, gpu, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb, wtype,
           p_scale, n, r, po, ldo, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
@@ -220,6 +223,8 @@ def adapters_backward(d_out, x, adapter, a, b, scale, d_x, d_a, d_b, dx_base=Non
     p_scale = _array("scale", scale, (n,), torch.float32, gpu)
     p_da = _array("d_a", d_a, (n, r, inner), torch.float32, gpu)
     p_db = _array("d_b", d_b, (n, outer, r), torch.float32, gpu)
-    ws = _workspace(_needed("moe_adapters_workspace", T, inner, outer, n, r), workspace, gpu, stream)
+    strided = (px | pd | pg | (p_base or 0) | (ldx | ldd | ldg | ldb) * x.element_size()) & 15
+    need = _needed("moe_adapters_workspace_strided" if strided else "moe_adapters_workspace", T, inner, outer, n, r)
+    ws = _workspace(need, workspace, gpu, stream)
     _call(lib.moe_adapters_backward, gpu, stream, pd, ldd, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
           wtype, p_scale, n, r, pg, ldg, p_da, p_db, ws.data_ptr(), ws.numel() * ws.element_size())

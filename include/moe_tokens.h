@@ -16,11 +16,12 @@
  *    adapters' gradients are fp32, indexes int32.  Sums are held in fp32 and rounded once.
  *  - Matrices are row-major; ld is the number of elements from one row to the next (>= the row's
  *    length).  No alignment beyond the element's own is needed; rows that start at multiples of 16
- *    bytes are the fast case (an adapters' backward call with others is many times slower).
+ *    bytes are the fast case.
  *  - An output may not overlap an input or another output, but out may be base (the same pointer and
  *    ld), and d_x may be dx_base.  A matrix is taken as all from its first to its last element: two
- *    column ranges of one wider matrix overlap.  Errors: MOE_ERR_INVALID (a NULL or overlapping tensor, a size or
- *    ld out of range, an unknown type, a workspace that is too small), MOE_ERR_UNSUPPORTED (a size
+ *    column ranges of one wider matrix overlap.
+ *  - Errors: MOE_ERR_INVALID (a NULL or overlapping tensor, a size or ld out of range, an unknown
+ *    type, a workspace that is too small), MOE_ERR_UNSUPPORTED (a size
  *    over the limits stated), both before anything is enqueued, and MOE_ERR_HIP (a launch failed; the
  *    kernels before it may run).
  *  - Index values are checked on the device: one out of range counts as "none".
@@ -86,8 +87,11 @@ int moe_tokens_combine_backward(const void *d_out, int64_t ld_d_out, const void 
  * No row's values enter another row's result.  Rows of one adapter next to each other (a
  * request's prompt; rows in the order of moe_tokens_dispatch) share its matrices' reads; other orders
  * are as right, only slower.  workspace: moe_adapters_forward_workspace bytes (NULL if that is 0, as it
- * is for few rows), 16-byte aligned.  Limits: rank <= 256; n_rows, inner and outer below 2^24. */
+ * is for few rows), 16-byte aligned.  Where x, base or out have rows that do not start at multiples of 16
+ * bytes, moe_adapters_forward_workspace_strided bytes let the call copy them to such rows first, which is
+ * faster than the way it takes with less.  Limits: rank <= 256; n_rows, inner and outer below 2^24. */
 size_t moe_adapters_forward_workspace(int n_rows, int inner, int outer, int n_adapters, int rank);
+size_t moe_adapters_forward_workspace_strided(int n_rows, int inner, int outer, int n_adapters, int rank);
 int moe_adapters_forward(const void *x, int64_t ld_x, const void *base, int64_t ld_base, int dtype, int n_rows,
                          int inner, int outer, const int32_t *adapter, const void *a, const void *b, int wtype,
                          const float *scale, int n_adapters, int rank, void *out, int64_t ld_out, void *workspace,
@@ -98,8 +102,10 @@ int moe_adapters_forward(const void *x, int64_t ld_x, const void *base, int64_t 
  *   d_a[e] = sum over e's rows of u x[i]^T, d_b[e] = scale[e] * sum of d_out[i] v^T
  * d_a [n_adapters x rank x inner] and d_b [n_adapters x outer x rank] are fp32 and overwritten
  * (zeros for an adapter without rows).  base's gradient is d_out; scale has none.  workspace:
- * moe_adapters_workspace bytes, 16-byte aligned.  Limits: those above, n_adapters <= 1024. */
+ * moe_adapters_workspace bytes, 16-byte aligned; _strided as above (its way with less is many times
+ * slower).  Limits: those above, n_adapters <= 1024. */
 size_t moe_adapters_workspace(int n_rows, int inner, int outer, int n_adapters, int rank);
+size_t moe_adapters_workspace_strided(int n_rows, int inner, int outer, int n_adapters, int rank);
 int moe_adapters_backward(const void *d_out, int64_t ld_d_out, const void *x, int64_t ld_x, const void *dx_base,
                           int64_t ld_dx_base, int dtype, int n_rows, int inner, int outer, const int32_t *adapter,
                           const void *a, const void *b, int wtype, const float *scale, int n_adapters, int rank,

@@ -209,6 +209,33 @@ def test_large_intermediate_values_in_fp16():
     assert (forward(many) == 1000.0).all()
 
 
+@pytest.mark.parametrize("dt,wt", [("bf16", "bf16"), ("f32", "f16")])
+@pytest.mark.parametrize("inner,outer,r", [(96, 72, 12), (96, 75, 8), (90, 72, 12)])
+def test_strided_rows_with_and_without_room_for_copies(dt, wt, inner, outer, r):
+    """Rows that no 16-byte piece fits: copied first where the workspace has room for it, else read as they lie."""
+    T, n, lib = 1300, 4, moe.gpu_lib()
+    s = make(T, n, r, inner, outer, dt, wt, "runs", seed=350)
+    m, dtype = numbers(s), s["x"].dtype
+    for ld_x, ld_out, offset in ((inner + 11, outer + 8, 0), (inner + 8, outer + 8, 1)):
+        t = dict(s, **{k: place(s[k], ld, offset) for k, ld in (("x", ld_x), ("dx_base", ld_x), ("base", ld_out), ("d_out", ld_out))})
+        want = ref.adapters(m["x"], m["adapter"], m["a"], m["b"], m["scale"], m["base"])
+        for name in ("", "_strided"):
+            bytes_f = getattr(lib, "moe_adapters_forward_workspace" + name)(T, inner, outer, n, r)
+            bytes_b = getattr(lib, "moe_adapters_workspace" + name)(T, inner, outer, n, r)
+            ws = torch.full((max(bytes_f, bytes_b) + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+            out, d_x = place(torch.zeros_like(s["base"]), ld_out, offset), place(torch.zeros_like(s["x"]), ld_x, offset)
+            moe.adapters_forward(t["x"], s["adapter"], s["a"], s["b"], s["scale"], out, base=t["base"], workspace=ws[:bytes_f])
+            assert (ws[bytes_f:] == 0xFF).all()
+            assert_near(out, want, dtype, forward_slack(m, dtype, True))
+            ws.fill_(0xFF)
+            check_backward(s, m, backward(t, dx_base=t["dx_base"], d_x=d_x, workspace=ws[:bytes_b]), True)
+            assert (ws[bytes_b:] == 0xFF).all()
+            for v, ld, cols in ((out, ld_out, outer), (d_x, ld_x, inner)):
+                buf = v._base.clone()
+                buf[offset:offset + T * ld].view(T, ld)[:, :cols] = 7.0
+                assert (buf == 7.0).all()
+
+
 def test_no_rows():
     s = make(0, 3, 4, 10, 12, "f32", "f32", "mixed", seed=700)
     assert forward(s).shape == (0, 12)

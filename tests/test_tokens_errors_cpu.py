@@ -99,6 +99,13 @@ def test_workspaces():
     assert lib.moe_adapters_workspace(100, 8, 8, 4, 300) == 0
     assert lib.moe_adapters_workspace(0, 8, 8, 4, 4) > 0
     assert lib.moe_adapters_forward_workspace(32, 2048, 2048, 8, 16) == 0
+    assert lib.moe_adapters_forward_workspace_strided(32, 2048, 2048, 8, 16) == 0
+    assert lib.moe_adapters_workspace_strided(100, 8, 8, 4, 300) == 0
+    # room for copies, 4 bytes an element: of x and base and out; of x, d_out and d_x
+    for name, copied in (("moe_adapters_forward_workspace", 2), ("moe_adapters_workspace", 3)):
+        least, most = getattr(lib, name)(8192, 2048, 2048, 8, 16), getattr(lib, name + "_strided")(8192, 2048, 2048, 8, 16)
+        assert most - least == copied * 8192 * 2048 * 4
+        assert getattr(lib, name)(8192, 2047, 2047, 8, 16) == getattr(lib, name + "_strided")(8192, 2047, 2047, 8, 16)
     assert lib.moe_adapters_forward_workspace(8192, 2048, 2048, 8, 16) >= 8192 * 16 * 4
 
 
