@@ -9,7 +9,12 @@
 namespace moe {
 namespace {
 
-constexpr int kRowCalls = 512;    // rows of a call that takes a workgroup a row
+// A call takes a workgroup a row (k_adapters_row) up to this many rows and products, else blocks of rows.
+constexpr int kRowCalls = 1024;
+constexpr int64_t kRowWork = 1 << 25;    // rows x rank x (inner + outer)
+// Above, rows that have to be copied to aligned ones first are worth it from here on.
+constexpr int kCopyCalls = 8192;
+constexpr int64_t kCopyWork = 1 << 27;
 constexpr int kRowTarget = 512;   // workgroups of such a call: two a CU
 
 // Eight elements at p (n of them there, zeros behind), as loaded and as fp32.
@@ -342,7 +347,7 @@ struct ShrinkArgs {
 // LDS.  A block's adapters are dealt to the workgroups of blockIdx.y (one without an adapter ends when it
 // has seen the numbers), so that a block with several does not end a whole turn after the rest.
 template <typename TX, typename TW, int NT, int MT, int WAVES, bool TILED>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4))) void k_shrink(ShrinkArgs g) {
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4))) void k_shrink(ShrinkArgs g, int rank_groups) {
     constexpr int kPart = 256 * NT * MT;
     __shared__ __align__(16) float part[WAVES * kPart];
     const ShrinkJob &job = g.job[blockIdx.z];
@@ -357,7 +362,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4)))
         x.m = rows_of<TX>(job.m, job.ld, row0, 16 * MT, g.T, job.cols);
         x.w = buffer(static_cast<const TW *>(job.w) + now * job.w_step, (size_t)job.w_step * sizeof(TW));
         const float scale = g.scale[now];
-        for (int q0 = 0; q0 < g.vr; q0 += 16 * NT) {
+        for (int q0 = blockIdx.y % rank_groups * 16 * NT; q0 < g.vr; q0 += rank_groups * 16 * NT) {
             x.run(l, q0, r, part);
             __syncthreads();
             for (int i = threadIdx.x; i < kPart; i += 64 * WAVES) {
@@ -370,7 +375,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4)))
             __syncthreads();
         }
     };
-    const int turns = gridDim.y, turn = blockIdx.y, row0 = blockIdx.x * 16 * MT;
+    const int turns = gridDim.y / rank_groups, turn = blockIdx.y / rank_groups, row0 = blockIdx.x * 16 * MT;
     int e[MT];
     adapters_of(g.adapter, row0 + l.l16, g.T, g.n, e);
     int seen = 0;
@@ -1043,9 +1048,10 @@ struct ForwardSpace {
     bool copy_x, copy_out;
     size_t v, b, a, x, out, bytes;
 };
+int64_t work_of(int64_t T, int inner, int outer, int r) { return T * r * (inner + outer); }
 ForwardSpace forward_space(int T, int inner, int outer, int n, int r, bool copies) {
     ForwardSpace s{};
-    if (T <= kRowCalls) return s;
+    if (T <= kRowCalls && work_of(T, inner, outer, r) <= kRowWork) return s;
     s.ip = (inner + 7) / 8 * 8;
     s.op = (outer + 7) / 8 * 8;
     s.rp = (r + 7) / 8 * 8;
@@ -1074,14 +1080,20 @@ bool piecewise(const void *p, int64_t ld, int cols, size_t size) {
 // Whether an adapter's matrices, as they are laid out, fit a buffer.
 bool fits_buffer(int64_t ip, int64_t op, int64_t rp, size_t size) { return rp * std::max(ip, op) * (int64_t)size < kBufferBytes; }
 
+constexpr int kFewTiles = 64;
 template <typename TX, typename TW, int MT, int WAVES, bool TILED>
 hipError_t shrink(const ShrinkArgs &g, int jobs, hipStream_t stream) {
     const int tiles = (g.T + 16 * MT - 1) / (16 * MT);
     const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / tiles)));
     const dim3 grid(tiles, turns, jobs), block(64 * WAVES);
-    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g);
-    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g);
-    return launch(k_shrink<TX, TW, 4, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g);
+    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
+    if (MT == 1 && tiles * jobs <= kFewTiles) {
+        const int groups = (g.r + 15) / 16;
+        return launch(k_shrink<TX, TW, 1, MT, WAVES, TILED>, dim3(tiles, turns * groups, jobs), block, stream, nullptr, nullptr, g,
+                      groups);
+    }
+    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
+    return launch(k_shrink<TX, TW, 4, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
 }
 
 template <typename TX, typename TW, int MT>
@@ -1126,7 +1138,8 @@ hipError_t forward(const AdapterArgs &g, void *workspace, size_t workspace_bytes
         if (c.bytes <= workspace_bytes) s = c;
     }
     const bool pad_a = s.ip != g.inner, pad_b = s.rp != g.r;
-    if (s.bytes && fits(s) && fits_buffer(s.ip, s.op, s.rp, sizeof(TW)) &&
+    const bool worth = !(s.copy_x || s.copy_out) || g.T > kCopyCalls || work_of(g.T, g.inner, g.outer, g.r) >= kCopyWork;
+    if (s.bytes && worth && fits(s) && fits_buffer(s.ip, s.op, s.rp, sizeof(TW)) &&
         (pad_a || reinterpret_cast<uintptr_t>(g.a) % 16 == 0) && (pad_b || reinterpret_cast<uintptr_t>(g.b) % 16 == 0) &&
         (int64_t)g.n * std::max(g.outer, g.r) < (1 << 30)) {
         float *v = reinterpret_cast<float *>(ws + s.v);
