@@ -10,12 +10,20 @@ namespace moe {
 namespace {
 
 // A call takes a workgroup a row (k_adapters_row) up to this many rows and products, else blocks of rows.
+// The row's cost grows with the work, the blocks' start at 7 to 11 us and grow with the adapters mixed in a
+// block.  Rank 16 of 2048 x 2048: 256 rows 8.8 us a row against 11.1, 512 rows 13.3 against 11.3, but 16.5
+// against 26.8 with 256 adapters mixed; 1024 rows 16.3 against 12.4.  Rank 64, 256 rows: 29 against 13.
+// Rank 8 of 512 x 512: 1024 rows 5.5 against 7.8, 2048 rows 7.9 against 8.4, 4096 rows 12.2 against 9.3.
 constexpr int kRowCalls = 1024;
 constexpr int64_t kRowWork = 1 << 25;    // rows x rank x (inner + outer)
-// Above, rows that have to be copied to aligned ones first are worth it from here on.
+// Above, rows that have to be copied to aligned ones first are worth it from here on.  2048 x 2048, rank
+// 16: 2048 rows 25 us a row against 29 with copies, 4096 rows 44 against 36; rank 32: 1024 rows 26 against
+// 24, 4096 rows 87 against 41.
 constexpr int kCopyCalls = 8192;
 constexpr int64_t kCopyWork = 1 << 27;
-constexpr int kRowTarget = 512;   // workgroups of such a call: two a CU
+// Workgroups of such a call: two a CU.  Rank 16 of 2048 x 2048, 256 rows: 8.8 us, 11.0 with 256 and 9.1 with
+// 1024; 128 rows: 6.7, 7.7 and 8.0.
+constexpr int kRowTarget = 512;
 
 // Eight elements at p (n of them there, zeros behind), as loaded and as fp32.
 template <typename T>
@@ -76,7 +84,8 @@ __device__ inline void shrink_row(const TX *x, const TW *a, int inner, int r, fl
 
 // A workgroup a row and slice of the columns: v by dot products (each slice makes its own), then a
 // thread a column.  For calls of few rows, whose time is the chain of loads: the first column's share
-// of b and base is requested before v is made.
+// of b and base is requested before v is made.  32 rows with an adapter each, rank 16 of 2048 x 2048, fp32
+// with bf16 adapters: 5.4 us for 5 MB, mostly the latency of three loads that wait for each other.
 template <typename TX, typename TW>
 __global__ __launch_bounds__(kThreads) void k_adapters_row(AdapterArgs g, int slice_cols) {
     __shared__ __align__(16) float v[kMaxRank];
@@ -227,12 +236,15 @@ struct Lane {
     }
 };
 
+// Waves of a block (16: backward of 16384 rows of 2048 bf16 with rank 32 147 us against 138, rank 64 210 against 196).
+constexpr int kShrinkWaves = 8;
+
 // The first product of a block of 16 MT rows: v = m w^T.  The waves take runs of 128 bytes of the
 // rows in turn, two chunks a lane, 64 bytes of a row in an instruction.  NT: tiles of 16 ranks at a time.
 // More rows a block read w from L2 less often, which is what bounds this beside m.  TILED: w lies in the
 // order in which it is loaded (tiled_at), 1 KB an instruction, which L2 gives faster than 64 bytes of 16
 // rows (both products of a backward call of 16384 rows at rank 32: 44 us against 52).
-template <typename TX, typename TW, int NT, int MT, int WAVES, bool TILED>
+template <typename TX, typename TW, int NT, int MT, bool TILED>
 struct Shrink {
     typedef Mma<TX> M;
     static constexpr int C = M::kChunk, kRun = 8 * C;
@@ -255,21 +267,22 @@ struct Shrink {
                 wr[i] = q < r ? (unsigned)q * cols : kNowhere / sizeof(TW);
         }
         const int runs = (cols + kRun - 1) / kRun;
-        for (int d = l.wave; d < runs; d += U * WAVES) {
+        for (int d = l.wave; d < runs; d += U * kShrinkWaves) {
             Chunk<TX, TX> x[U][MT][2];
             Chunk<TX, TW> a[U][NT][2];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const int k = (d + u * WAVES) * kRun + 4 * s * C + l.quad * C;
+                    const int k = (d + u * kShrinkWaves) * kRun + 4 * s * C + l.quad * C;
                     const bool in = k < cols;
 #pragma unroll
                     for (int j = 0; j < MT; ++j) x[u][j][s].load(m, in ? row + j * step + k * (unsigned)sizeof(TX) : kNowhere);
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         if constexpr (TILED)   // (beyond the last run: out of the buffer's range)
-                            a[u][i][s].load(w, (wr[i] + ((d + u * WAVES) * ((r + 15) / 16) * 2 + s) * 64 * C) * (unsigned)sizeof(TW));
+                            a[u][i][s].load(w, (wr[i] + ((d + u * kShrinkWaves) * ((r + 15) / 16) * 2 + s) * 64 * C) *
+                                                   (unsigned)sizeof(TW));
                         else
                             a[u][i][s].load(w, in ? (wr[i] + k) * (unsigned)sizeof(TW) : kNowhere);
                     }
@@ -345,14 +358,17 @@ struct ShrinkArgs {
 
 // 16 MT rows a workgroup, for each adapter among them: the reduction split over the waves and joined in
 // LDS.  A block's adapters are dealt to the workgroups of blockIdx.y (one without an adapter ends when it
-// has seen the numbers), so that a block with several does not end a whole turn after the rest.
-template <typename TX, typename TW, int NT, int MT, int WAVES, bool TILED>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4))) void k_shrink(ShrinkArgs g, int rank_groups) {
+// has seen the numbers), so that a block with several does not end a whole turn after the rest; with few
+// blocks the ranks are dealt to them too.  8192 rows of 2048 bf16 with rank 16: 15 us for 34 MB of x and as
+// much of A from L2, which is what it waits for; both products of a backward call of 16384 rows with rank
+// 32: 37 to 45 us for 134 MB.
+template <typename TX, typename TW, int NT, int MT, bool TILED>
+__global__ __launch_bounds__(64 * kShrinkWaves) __attribute__((amdgpu_waves_per_eu(4))) void k_shrink(ShrinkArgs g, int rank_groups) {
     constexpr int kPart = 256 * NT * MT;
-    __shared__ __align__(16) float part[WAVES * kPart];
+    __shared__ __align__(16) float part[kShrinkWaves * kPart];
     const ShrinkJob &job = g.job[blockIdx.z];
     const Lane l;
-    Shrink<TX, TW, NT, MT, WAVES, TILED> x;
+    Shrink<TX, TW, NT, MT, TILED> x;
     x.row = l.l16 * (unsigned)job.ld * sizeof(TX);
     x.step = 16 * (unsigned)job.ld * sizeof(TX);
     x.cols = job.cols;
@@ -365,10 +381,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4)))
         for (int q0 = blockIdx.y % rank_groups * 16 * NT; q0 < g.vr; q0 += rank_groups * 16 * NT) {
             x.run(l, q0, r, part);
             __syncthreads();
-            for (int i = threadIdx.x; i < kPart; i += 64 * WAVES) {
+            for (int i = threadIdx.x; i < kPart; i += 64 * kShrinkWaves) {
                 float s = 0.f;
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) s += part[w * kPart + i];
+                for (int w = 0; w < kShrinkWaves; ++w) s += part[w * kPart + i];
                 const int k = i / (16 * NT), q = q0 + i % (16 * NT);
                 if (q < g.vr && (rows >> k) & 1) job.v[(size_t)(row0 + k) * g.vr + q] = q < r ? s * scale : 0.f;
             }
@@ -445,7 +461,8 @@ struct ExpandArgs {
 // piece.  kTiles: products of 16x16 that make a piece.  For a block with several adapters each one's
 // product is made in turn and the rows keep their own.  Workgroups go to the 8 XCDs in turn by index:
 // those of a block have one index modulo 8, and follow each other there.  KB: blocks of ranks whose operand
-// stays in registers.
+// stays in registers.  8192 rows of 2048 bf16 with rank 16: 67 MB in 18.2 us, 3.7 TB/s; 16384 rows with
+// rank 32: 134 MB in 32 us, 4.2 TB/s.
 template <typename TX, typename TW, int KB, int MT>
 __global__ __launch_bounds__(kThreads) void k_expand(ExpandArgs g, int col_wgs) {
     typedef Mma<TX> M;
@@ -592,6 +609,11 @@ __global__ __launch_bounds__(kThreads) void k_expand(ExpandArgs g, int col_wgs) 
     }
 }
 
+// ------------------------------------------------------------------ gradients, a workgroup a row
+//
+// For rows that the block kernels cannot read where the workspace has no room for copies of them: right,
+// and slow (16384 rows of 2048 bf16, rank 32: 3.4 ms against 0.11 aligned and 0.21 with copies).
+
 // v and u of a row to memory, and its d_x.
 template <typename TX, typename TW>
 __global__ __launch_bounds__(kThreads) void k_back_row(AdapterBackArgs g, float *gv, float *gu) {
@@ -673,8 +695,9 @@ __global__ __launch_bounds__(kThreads) void k_back_weights(AdapterBackArgs g, co
 // are products over the rows of one adapter at a time, in the order of a counting sort.
 
 // at[e][c][q] = a[e][q][c] with zeros in the padding, and a and b transposed in the order in which the first
-// product loads them (tiled_at), zeros behind their last column.  32 ranks by 64 columns a workgroup.  The first `order_wgs` workgroups
-// make the order of the rows by adapter meanwhile.  C: a chunk's elements.
+// product loads them (tiled_at), zeros behind their last column.  32 ranks by 64 columns a workgroup.  The
+// first `order_wgs` workgroups make the order of the rows by adapter meanwhile (16384 rows, 4 adapters of
+// rank 32, 2048 x 2048: 11 us, against 9 and 11 as two launches).  C: a chunk's elements.
 constexpr int kOrderedHere = 256;   // adapters that this has room for
 template <typename TW, int C>
 __global__ __launch_bounds__(kThreads) void k_back_layout(const TW *a, const TW *b, TW *at, TW *aw, TW *bw, int inner, int outer,
@@ -806,9 +829,12 @@ __device__ inline Piece find_piece(const int32_t *offsets, int n, int rows, int 
 }
 
 // Calls of up to this many rows: an adapter is one piece, its rows are found by the workgroups themselves,
-// and there is neither a sort nor a join.
+// and there is neither a sort nor a join.  512 rows, rank 16 of 2048 x 2048: 23.4 us against 24.8 (64
+// adapters mixed: 65 against 72); 1024 rows 31.8 against 30.0.
 constexpr int kSmallBack = 512;
-constexpr int kOrderRows = 32768;   // rows whose order every ordering workgroup counts by itself
+// Rows whose order is made in the layout's launch, each ordering workgroup counting them all: 32768 rows of
+// 2048 columns 210 us against 218 with a launch of its own, 131072 rows of 256 columns 188 against 168.
+constexpr int kOrderRows = 32768;
 
 struct BackWeights {
     const int32_t *adapter;
@@ -833,9 +859,11 @@ __device__ __forceinline__ void store_grad(const BackWeights &g, int e, bool is_
 // a lane loads 16 bytes of 8 rows, and for bf16 turns them into the eight columns' operands, pairs of
 // rows a dword (v_perm), with u and v in three parts, which hold all of an fp32 value's 24 bits (two parts
 // made the gradients' error 2.5 times that of fp32 products); other types multiply in fp32, whose operand is
-// one element.
+// one element.  16384 rows of 2048 bf16, rank 32, both gradients: 134 MB in 28 us, 4.8 TB/s, when they come
+// from the memory-side cache, 38 us when not; the join after it 5 us.
 template <typename TX, int NT, bool SMALL>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NT == 4 && sizeof(TX) == 4 ? 1 : 2))) void k_back_pieces(BackWeights g) {
+__global__ __launch_bounds__(kThreads)
+__attribute__((amdgpu_waves_per_eu(NT == 4 && sizeof(TX) == 4 ? 1 : 2))) void k_back_pieces(BackWeights g) {
     constexpr bool kPairs = std::is_same_v<TX, bf16>;
     constexpr int kLoads = sizeof(TX) == 4 ? 2 : 1;   // of 16 bytes for a lane's 8 columns of a row
     __shared__ __align__(16) f32x4 part[kThreads / 64][8][64];
@@ -1013,7 +1041,8 @@ BackSpace back_space(int T, int inner, int outer, int n, int r, bool copies) {
     s.op = (outer + 7) / 8 * 8;
     s.rp = (r + 7) / 8 * 8;
     s.padded = copies || s.ip != inner || s.op != outer;
-    // pieces such that their workgroups are about two and a half rounds of the chip's CUs
+    // pieces such that their workgroups are about two and a half rounds of the chip's CUs (16384 rows, rank
+    // 32, one adapter: 99 us, 106 with half as many, 102 with twice; 8 adapters: 136, 137 and 142)
     const int64_t tiles = (s.ip + kPieceCols - 1) / kPieceCols + (s.op + kPieceCols - 1) / kPieceCols;
     s.piece_rows = (int)std::min<int64_t>(1 << 24, std::max<int64_t>(128, (T * tiles / 640 + 127) / 128 * 128));
     s.max_pieces = T / s.piece_rows + std::min(n, T);
@@ -1080,26 +1109,31 @@ bool piecewise(const void *p, int64_t ld, int cols, size_t size) {
 // Whether an adapter's matrices, as they are laid out, fit a buffer.
 bool fits_buffer(int64_t ip, int64_t op, int64_t rp, size_t size) { return rp * std::max(ip, op) * (int64_t)size < kBufferBytes; }
 
+// Blocks up to which a workgroup takes 16 ranks only and the others go to more of them.  Rank 64 of 2048
+// columns: 512 rows 15.0 us against 20.3; backward of 59 rows of 5056 columns 45 against 65; with blocks up
+// to 256, backward of 2000 rows 63 against 59.
 constexpr int kFewTiles = 64;
-template <typename TX, typename TW, int MT, int WAVES, bool TILED>
+template <typename TX, typename TW, int MT, bool TILED>
 hipError_t shrink(const ShrinkArgs &g, int jobs, hipStream_t stream) {
     const int tiles = (g.T + 16 * MT - 1) / (16 * MT);
+    // turns: four workgroups a CU (8 adapters of rank 64, 2048 rows: 27 us, 35 with two turns; 64 mixed
+    // adapters of rank 16: 51 and 55)
     const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / tiles)));
-    const dim3 grid(tiles, turns, jobs), block(64 * WAVES);
-    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
+    const dim3 grid(tiles, turns, jobs), block(64 * kShrinkWaves);
+    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
     if (MT == 1 && tiles * jobs <= kFewTiles) {
         const int groups = (g.r + 15) / 16;
-        return launch(k_shrink<TX, TW, 1, MT, WAVES, TILED>, dim3(tiles, turns * groups, jobs), block, stream, nullptr, nullptr, g,
-                      groups);
+        return launch(k_shrink<TX, TW, 1, MT, TILED>, dim3(tiles, turns * groups, jobs), block, stream, nullptr, nullptr, g, groups);
     }
-    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
-    return launch(k_shrink<TX, TW, 4, MT, WAVES, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
+    if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
+    return launch(k_shrink<TX, TW, 4, MT, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
 }
 
 template <typename TX, typename TW, int MT>
 hipError_t expand(ExpandArgs g, hipStream_t stream) {
     const int tiles = (g.T + 16 * MT - 1) / (16 * MT), groups = (g.cols + 63) / 64;
-    // a wave takes more groups (v is read and split once) as long as there are 16 waves a CU
+    // a wave takes more groups (v is read and split once) as long as there are 16 waves a CU (8192 rows of
+    // 2048 bf16: rank 16 35.5 us, 40 with 8 waves; rank 64 54, 56 with 32)
     g.groups = (int)std::max<int64_t>(1, std::min<int64_t>(8, (int64_t)tiles * groups / 4096));
     const int col_wgs = (groups + 4 * g.groups - 1) / (4 * g.groups);
     const dim3 grid((tiles + 7) / 8 * 8 * col_wgs), block(kThreads);
@@ -1110,15 +1144,16 @@ hipError_t expand(ExpandArgs g, hipStream_t stream) {
     return launch(k_expand<TX, TW, 2, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
 }
 
-constexpr int64_t kTallWork = 1 << 17;
 // Both products of a call.  A block of 32 rows instead of 16 halves the reads of the adapters' matrices
-// from L2, and the number of workgroups: worth it from rank 17 (shrink) on, with enough rows.
+// from L2, and the number of workgroups: worth it from rank 17 on and this many rows x ranks, four times as
+// many where the first product's matrices are tiled.  2048 columns, rank 32: 4096 rows 22.9 us against 24.9,
+// 1024 rows 17.7 against 14.9; rank 64: 4096 rows 31.6 against 38.3.  Backward: rank 32, 16384 rows 136
+// against 141, 4096 rows 56.2 against 54.8. 
+constexpr int64_t kTallWork = 1 << 17;
 template <typename TX, typename TW, bool TILED>
 hipError_t products(const ShrinkArgs &sa, int jobs, const ExpandArgs &ea, hipStream_t stream) {
     const bool tall = sa.r > 16 && (int64_t)sa.r * sa.T >= kTallWork * (TILED ? 4 : 1);
-    const hipError_t err = !tall          ? shrink<TX, TW, 1, 8, TILED>(sa, jobs, stream)
-                           : sa.r <= 32 ? shrink<TX, TW, 2, 8, TILED>(sa, jobs, stream)
-                                        : shrink<TX, TW, 2, 16, TILED>(sa, jobs, stream);
+    const hipError_t err = tall ? shrink<TX, TW, 2, TILED>(sa, jobs, stream) : shrink<TX, TW, 1, TILED>(sa, jobs, stream);
     if (err != hipSuccess) return err;
     return tall ? expand<TX, TW, 2>(ea, stream) : expand<TX, TW, 1>(ea, stream);
 }
@@ -1153,7 +1188,8 @@ hipError_t forward(const AdapterArgs &g, void *workspace, size_t workspace_bytes
         const void *x = s.copy_x ? ws + s.x : g.x, *a = pad_a ? ws + s.a : g.a, *b = pad_b ? ws + s.b : g.b;
         void *out = s.copy_out ? ws + s.out : g.out;
         const void *base = s.copy_out ? out : g.base;
-        const int64_t ld_x = s.copy_x ? s.ip : g.ld_x, ld_out = s.copy_out ? s.op : g.ld_out, ld_base = s.copy_out ? s.op : g.ld_base;
+        const int64_t ld_x = s.copy_x ? s.ip : g.ld_x;
+        const int64_t ld_out = s.copy_out ? s.op : g.ld_out, ld_base = s.copy_out ? s.op : g.ld_base;
         const ShrinkArgs sa{{{x, a, ld_x, (int64_t)g.r * s.ip, v, s.ip}}, g.adapter, g.scale, g.T, g.n, g.r, s.rp};
         const ExpandArgs ea{base, b, out, v, g.adapter, ld_base, ld_out, g.T, s.op, g.n, g.outer, s.rp, s.rp, 0};
         err = products<TX, TW, false>(sa, 1, ea, stream);
@@ -1236,7 +1272,8 @@ hipError_t backward(int dtype, const AdapterBackArgs &g, void *workspace, size_t
     const ShrinkArgs sa{{{x, aw, ld_x, (int64_t)tiled_size(g.r, g.inner, C), v, s.ip},
                          {d_out, bw, ld_d_out, (int64_t)tiled_size(g.r, g.outer, C), u, s.op}},
                         g.adapter, g.scale, g.T, g.n, g.r, s.rp};
-    err = products<TX, TW, true>(sa, 2, {dx_base, at, d_x, u, g.adapter, ld_dx_base, ld_d_x, g.T, s.ip, g.n, s.ip, s.rp, s.rp, 0}, stream);
+    const ExpandArgs ea{dx_base, at, d_x, u, g.adapter, ld_dx_base, ld_d_x, g.T, s.ip, g.n, s.ip, s.rp, s.rp, 0};
+    err = products<TX, TW, true>(sa, 2, ea, stream);
     if (err != hipSuccess) return err;
     if (s.padded) {
         Reshape m{};

@@ -3,6 +3,7 @@
 //
 // All of it is bound by memory (at most three flops an element), so every kernel reads each input
 // row once and writes each output row once, in 16-byte pieces, and the small index work rides along.
+// Measured rates stand beside a copy's on the same card: 5.4 TB/s at 0.5 GB of traffic, 5.2 at 2 GB.
 #include <algorithm>
 
 #include "elements.hpp"
@@ -11,11 +12,18 @@
 namespace moe {
 namespace {
 
-constexpr int kDirectPicks = 8192;    // up to here every workgroup counts all picks itself
+// Up to here every workgroup counts all picks itself, above it sums the counts of slices that a launch
+// before has made.  8192 picks with rows of 2048 bf16: 13.4 us so, 14.1 with slices; 16384: 20.3 and 18.9
+// (the order alone: 10.9 and 10.4).
+constexpr int kDirectPicks = 8192;
+// 64 slices at most, and more only where a slice would be over 32768 picks: a workgroup reads every
+// slice's counts and half a slice's picks.  2^21 picks: 64 slices; 2^23: 374 us with 256, 483 with 64.
 constexpr int kSlicePicks = 2048;     // picks of a histogram slice above, at least
 constexpr int kMaxSlices = 64;
 constexpr int kLongSlice = 32768, kMostSlices = 512;
-constexpr int kWgTarget = 1024;       // workgroups of a dispatch that copies rows: four a CU
+// Workgroups of a dispatch that copies rows: four a CU.  8192 tokens of 2048 bf16: 70 us, 72 with 512
+// and 68 with 2048; 32768 tokens of 64: 19.5 us, 21.9 and 21.3.
+constexpr int kWgTarget = 1024;
 
 int slices_of(int N) {
     if (N <= kDirectPicks) return 0;
@@ -35,6 +43,8 @@ __global__ __launch_bounds__(kThreads) void k_slice_counts(const int32_t *ids, i
 
 // The order of the picks (order_picks), then the rows of the workgroup's tokens: read once, written once a
 // pick.  The first four tokens' pieces are requested before the order is made.
+// 8192 tokens of 2048 bf16, 8 picks each: 302 MB in 65 us, 4.6 TB/s (k_slice_counts before it 4 us);
+// one token 6.2 us, the steps of the order one after another.
 template <typename T, int EM>
 __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int tokens, int lanes_log2, const int32_t *counts,
                                                        int slices, int per) {
@@ -77,7 +87,8 @@ __global__ __launch_bounds__(kThreads) void k_dispatch(DispatchArgs a, int token
 }
 
 // L lanes a token (a whole workgroup for wide rows); each lane sums its pieces over the picks in
-// order, eight rows' loads in flight.
+// order, eight rows' loads in flight.  4096 tokens of 2048 columns, 8 picks each: bf16 with base 160 MB in
+// 34 us, 4.7 TB/s; fp32 302 MB in 65 us; four tokens 5.6 us, the latency of position, gate and row.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_combine_rows(CombineRowsArgs a, int lanes_log2) {
     const int L = 1 << lanes_log2;
@@ -121,7 +132,8 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(CombineRowsArgs a, in
 }
 
 // L lanes a token: d_out's piece is read once and serves every pick's gradient row and dot product.
-// KM: picks held in registers (8 or 16).
+// KM: picks held in registers (8 or 16).  8192 tokens of 2048 bf16, 8 picks each: 571 MB in 116 us,
+// 4.9 TB/s; 333 tokens 7.7 us.
 template <typename T, int KM>
 __global__ __launch_bounds__(kThreads) void k_combine_back(CombineBackArgs a, int lanes_log2) {
     __shared__ float part[kThreads / 64][KM];
