@@ -39,6 +39,15 @@ SHAPES = [
     (16500, 3, 24, 64, 64, "bf16", "bf16", "runs"),
     (33000, 5, 4, 24, 16, "bf16", "bf16", "mixed"),
     (9000, 270, 64, 64, 16, "f16", "f16", "runs"),
+    # blocks of few rows, ranks dealt to workgroups
+    (40, 3, 256, 2048, 2048, "bf16", "bf16", "mixed"),
+    (20, 2, 200, 5000, 4000, "f16", "f16", "mixed"),
+    (1, 2, 256, 70000, 65536, "bf16", "bf16", "mixed"),
+    (150, 4, 64, 2048, 3000, "f32", "bf16", "runs"),
+    # odd sizes copied to aligned rows
+    (8200, 3, 5, 33, 17, "bf16", "bf16", "runs"),
+    (8300, 4, 12, 100, 72, "f32", "f16", "mixed"),
+    (9000, 2, 8, 72, 35, "f16", "f16", "runs"),
 ]
 
 
@@ -211,9 +220,10 @@ def test_large_intermediate_values_in_fp16():
 
 @pytest.mark.parametrize("dt,wt", [("bf16", "bf16"), ("f32", "f16")])
 @pytest.mark.parametrize("inner,outer,r", [(96, 72, 12), (96, 75, 8), (90, 72, 12)])
-def test_strided_rows_with_and_without_room_for_copies(dt, wt, inner, outer, r):
+@pytest.mark.parametrize("T", [1300, 8300])
+def test_strided_rows_with_and_without_room_for_copies(T, dt, wt, inner, outer, r):
     """Rows that no 16-byte piece fits: copied first where the workspace has room for it, else read as they lie."""
-    T, n, lib = 1300, 4, moe.gpu_lib()
+    n, lib = 4, moe.gpu_lib()
     s = make(T, n, r, inner, outer, dt, wt, "runs", seed=350)
     m, dtype = numbers(s), s["x"].dtype
     for ld_x, ld_out, offset in ((inner + 11, outer + 8, 0), (inner + 8, outer + 8, 1)):
