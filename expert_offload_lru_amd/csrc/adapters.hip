@@ -12,7 +12,8 @@ namespace {
 // A call takes a workgroup a row (k_adapters_row) up to this many rows and products, else blocks of rows.
 // The row's cost grows with the work, the blocks' start at 7 to 11 us and grow with the adapters mixed in a
 // block.  Rank 16 of 2048 x 2048: 256 rows 8.8 us a row against 11.1, 512 rows 13.3 against 11.3, but 16.5
-// against 26.8 with 256 adapters mixed; 1024 rows 16.3 against 12.4.  Rank 64, 256 rows: 29 against 13.
+// against 26.8 with 256 adapters mixed; 1024 rows 16.3 against 12.4.  Rank 64, 128 rows: 19.5 against 11.7,
+// but 23 against 36 with 128 adapters mixed.
 // Rank 8 of 512 x 512: 1024 rows 5.5 against 7.8, 2048 rows 7.9 against 8.4, 4096 rows 12.2 against 9.3.
 constexpr int kRowCalls = 1024;
 constexpr int64_t kRowWork = 1 << 25;    // rows x rank x (inner + outer)
@@ -21,7 +22,7 @@ constexpr int64_t kRowWork = 1 << 25;    // rows x rank x (inner + outer)
 // 24, 4096 rows 87 against 41.
 constexpr int kCopyCalls = 8192;
 constexpr int64_t kCopyWork = 1 << 27;
-// Workgroups of such a call: two a CU.  Rank 16 of 2048 x 2048, 256 rows: 8.8 us, 11.0 with 256 and 9.1 with
+// Workgroups of such a call, of 256 threads: two a CU.  Rank 16 of 2048 x 2048, 256 rows: 8.8 us, 11.0 with 256 and 9.1 with
 // 1024; 128 rows: 6.7, 7.7 and 8.0.
 constexpr int kRowTarget = 512;
 
@@ -52,10 +53,10 @@ __device__ inline float wave_total(float v) {
 }
 
 // v[q] = <a's row q, x> for q < r: four rows of a at a time a wave, their loads in flight together.
-template <typename TX, typename TW>
+template <int THREADS, typename TX, typename TW>
 __device__ inline void shrink_row(const TX *x, const TW *a, int inner, int r, float *v) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int q0 = wave * 4; q0 < r; q0 += kThreads / 64 * 4) {
+    for (int q0 = wave * 4; q0 < r; q0 += THREADS / 64 * 4) {
         float s[4] = {};
 #pragma unroll 2
         for (int c = lane * 8; c < inner; c += 512) {
@@ -86,8 +87,8 @@ __device__ inline void shrink_row(const TX *x, const TW *a, int inner, int r, fl
 // thread a column.  For calls of few rows, whose time is the chain of loads: the first column's share
 // of b and base is requested before v is made.  32 rows with an adapter each, rank 16 of 2048 x 2048, fp32
 // with bf16 adapters: 5.4 us for 5 MB, mostly the latency of three loads that wait for each other.
-template <typename TX, typename TW>
-__global__ __launch_bounds__(kThreads) void k_adapters_row(AdapterArgs g, int slice_cols) {
+template <typename TX, typename TW, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_adapters_row(AdapterArgs g, int slice_cols) {
     __shared__ __align__(16) float v[kMaxRank];
     const int row = blockIdx.x, e = g.adapter[row];
     const int o0 = blockIdx.y * slice_cols + threadIdx.x, o1 = min(g.outer, (int)(blockIdx.y + 1) * slice_cols);
@@ -105,8 +106,8 @@ __global__ __launch_bounds__(kThreads) void k_adapters_row(AdapterArgs g, int sl
     }
     if (has) {
         scale = g.scale[e];
-        shrink_row(static_cast<const TX *>(g.x) + row * g.ld_x, static_cast<const TW *>(g.a) + (size_t)e * g.r * g.inner,
-                   g.inner, g.r, v);
+        shrink_row<THREADS>(static_cast<const TX *>(g.x) + row * g.ld_x,
+                            static_cast<const TW *>(g.a) + (size_t)e * g.r * g.inner, g.inner, g.r, v);
         if (threadIdx.x >= (unsigned)g.r && threadIdx.x < ((g.r + 7) & ~7u)) v[threadIdx.x] = 0.f;
     }
     __syncthreads();
@@ -117,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_row(AdapterArgs g, int sl
         for (int k = 0; k < 8; ++k) s = fmaf(f[k], v[q + k], s);
         return s;
     };
-    for (int o = o0; o < o1; o += kThreads) {
+    for (int o = o0; o < o1; o += THREADS) {
         float s = 0.f;
         if (has) {
             if (o != o0)
@@ -623,7 +624,7 @@ __global__ __launch_bounds__(kThreads) void k_back_row(AdapterBackArgs g, float 
     const TW *a = static_cast<const TW *>(g.a) + (has ? (size_t)e * g.r * g.inner : 0);
     const TX *dy = static_cast<const TX *>(g.d_out) + row * g.ld_d_out;
     if (has) {
-        shrink_row(static_cast<const TX *>(g.x) + row * g.ld_x, a, g.inner, g.r, v);
+        shrink_row<kThreads>(static_cast<const TX *>(g.x) + row * g.ld_x, a, g.inner, g.r, v);
         const TW *b = static_cast<const TW *>(g.b) + (size_t)e * g.outer * g.r;
         const float scale = g.scale[e];
         for (int q = wave; q < g.r; q += kThreads / 64) {
@@ -1158,6 +1159,15 @@ hipError_t products(const ShrinkArgs &sa, int jobs, const ExpandArgs &ea, hipStr
     return tall ? expand<TX, TW, 2>(ea, stream) : expand<TX, TW, 1>(ea, stream);
 }
 
+template <typename TX, typename TW, int THREADS>
+hipError_t row_calls(const AdapterArgs &g, hipStream_t stream) {
+    const int groups = (g.outer + THREADS - 1) / THREADS;
+    const int slices = std::max(1, std::min(groups, kRowTarget * kThreads / THREADS / g.T));
+    const int cols = (groups + slices - 1) / slices * THREADS;
+    return launch(k_adapters_row<TX, TW, THREADS>, dim3(g.T, (g.outer + cols - 1) / cols), dim3(THREADS), stream, nullptr, nullptr,
+                  g, cols);
+}
+
 template <typename TX, typename TW>
 hipError_t forward(const AdapterArgs &g, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     constexpr size_t z = sizeof(TX);
@@ -1198,10 +1208,11 @@ hipError_t forward(const AdapterArgs &g, void *workspace, size_t workspace_bytes
         back.add({out, g.out, s.op, g.ld_out, g.outer, g.outer, g.T, false});
         return reshape<TX, TW>(back, stream);
     }
-    const int groups = (g.outer + kThreads - 1) / kThreads;
-    const int slices = std::max(1, std::min(groups, kRowTarget / g.T)), cols = (groups + slices - 1) / slices * kThreads;
-    return launch(k_adapters_row<TX, TW>, dim3(g.T, (g.outer + cols - 1) / cols), dim3(kThreads), stream, nullptr, nullptr,
-                  g, cols);
+    // threads: four ranks a wave at once (one row of 2048 x 2048, rank 64: 9.9 us with 1024, 13.7 with 256; 64 rows
+    // with rank 32: 6.7 us with 512, 9.4 with 256); fp32 adapters' registers allow 512
+    if (g.r <= 16) return row_calls<TX, TW, 256>(g, stream);
+    if (g.r <= 32 || sizeof(TW) == 4) return row_calls<TX, TW, 512>(g, stream);
+    if constexpr (sizeof(TW) == 2) return row_calls<TX, TW, 1024>(g, stream);
 }
 
 template <typename TX, typename TW>
