@@ -1210,7 +1210,8 @@ hipError_t forward(const AdapterArgs &g, void *workspace, size_t workspace_bytes
     }
     // threads: four ranks a wave at once (one row of 2048 x 2048, rank 64: 9.9 us with 1024, 13.7 with 256; 64 rows
     // with rank 32: 6.7 us with 512, 9.4 with 256); fp32 adapters' registers allow 512
-    if (g.r <= 16) return row_calls<TX, TW, 256>(g, stream);
+    // (a launch's threads stay under 2^32)
+    if (g.r <= 16 || g.T >= 1 << 22) return row_calls<TX, TW, 256>(g, stream);
     if (g.r <= 32 || sizeof(TW) == 4) return row_calls<TX, TW, 512>(g, stream);
     if constexpr (sizeof(TW) == 2) return row_calls<TX, TW, 1024>(g, stream);
 }

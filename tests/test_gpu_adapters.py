@@ -246,6 +246,22 @@ def test_strided_rows_with_and_without_room_for_copies(T, dt, wt, inner, outer, 
                 assert (buf == 7.0).all()
 
 
+def test_millions_of_rows_a_workgroup_each():
+    """A workgroup a row for unaligned rows without room for copies: the grid stays within a launch's limits."""
+    T, n, r, inner, outer = (1 << 22) + 3, 3, 40, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(360)
+    x = torch.randn(T, inner + 1, generator=g, device="cuda").bfloat16()[:, 1:]
+    adapter = torch.randint(-1, n, (T,), generator=g, dtype=torch.int32, device="cuda")
+    a, b = randn(361, n, r, inner, dtype=torch.bfloat16), randn(362, n, outer, r, dtype=torch.bfloat16)
+    scale, out = randn(363, n), torch.empty(T, outer, dtype=torch.bfloat16, device="cuda")
+    need = moe.gpu_lib().moe_adapters_forward_workspace(T, inner, outer, n, r)
+    moe.adapters_forward(x, adapter, a, b, scale, out, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    for part in (slice(0, 7), slice(T // 2, T // 2 + 9), slice(T - 9, T)):
+        few = torch.empty_like(out[part])
+        moe.adapters_forward(x[part], adapter[part].contiguous(), a, b, scale, few)
+        assert torch.equal(out[part], few)
+
+
 def test_no_rows():
     s = make(0, 3, 4, 10, 12, "f32", "f32", "mixed", seed=700)
     assert forward(s).shape == (0, 12)
