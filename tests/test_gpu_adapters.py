@@ -283,6 +283,23 @@ def test_repeats_streams_and_a_kept_workspace_are_bitwise_equal():
                 assert torch.equal(g, w)
 
 
+def test_two_calls_at_once():
+    """Calls on two streams with tensors and workspaces of their own, in flight together."""
+    sets = [make(1400, 6, 24, 256, 320, "bf16", "bf16", "runs", seed=820 + i) for i in range(2)]
+    want = [(forward(s, base=s["base"]), *backward(s)) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for s, st, g in zip(sets, streams, got):
+            with torch.cuda.stream(st):
+                g.append((forward(s, base=s["base"]), *backward(s)))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for outputs in g:
+            assert all(torch.equal(a, b) for a, b in zip(outputs, w))
+
+
 def test_gradients_against_differences():
     """out is linear in x, in a and in b: a difference over a step of one is the derivative."""
     s = make(50, 3, 6, 40, 30, "f32", "f32", "mixed", seed=900)
