@@ -223,6 +223,35 @@ __device__ inline void split(float v, T &hi, T &lo) {
     lo = narrow<T>(__builtin_isfinite(rest) ? rest : 0.f);
 }
 
+// The 24 bits of fp32 values, 8 a part, without a rounding: f = hi + mid + lo (of an infinity the latter two are NaN).
+__device__ __forceinline__ void three_parts(float (&f)[8], bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
+    auto cut = [&](bool last) __attribute__((always_inline)) {
+        u32x4 top;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t a = __float_as_uint(f[2 * d]), b = __float_as_uint(f[2 * d + 1]);
+            top[d] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+            if (last) continue;
+            f[2 * d] -= __uint_as_float(a & 0xFFFF0000u);
+            f[2 * d + 1] -= __uint_as_float(b & 0xFFFF0000u);
+        }
+        return __builtin_bit_cast(bf16x8, top);
+    };
+    hi = cut(false);
+    mid = cut(false);
+    lo = cut(true);
+}
+
+// The low parts' products of a sum whose high parts' products are added to it.  Beside an infinite operand they are a
+// NaN (inf * 0) or an infinity of any sign, and the high parts alone give what the sum is; a finite number here, as
+// every finite sum is left, keeps it so.  (Of a NaN the median is one of the bounds.)
+__device__ __forceinline__ f32x4 bounded(f32x4 v) {
+    constexpr float kMost = 3.402823466e38f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_fmed3f(v[i], -kMost, kMost);
+    return v;
+}
+
 // A lane's place: row l16 of the block, quarter quad of the reduction (or of a piece's 64 bytes).
 struct Lane {
     int l16, quad, wave;
@@ -463,9 +492,11 @@ struct ExpandArgs {
 // product is made in turn and the rows keep their own.  Workgroups go to the 8 XCDs in turn by index:
 // those of a block have one index modulo 8, and follow each other there.  KB: blocks of ranks whose operand
 // stays in registers.  8192 rows of 2048 bf16 with rank 16: 67 MB in 18.2 us, 3.7 TB/s; 16384 rows with
-// rank 32: 134 MB in 32 us, 4.2 TB/s.
+// rank 32: 134 MB in 32 us, 4.2 TB/s.  Waves a SIMD: what 512 registers allow without a spill; left to itself the
+// compiler copied accumulators to and fro (rank 64, 2048 rows of fp16: the call 30.1 us against 26.0).
 template <typename TX, typename TW, int KB, int MT>
-__global__ __launch_bounds__(kThreads) void k_expand(ExpandArgs g, int col_wgs) {
+__global__ __launch_bounds__(kThreads)
+__attribute__((amdgpu_waves_per_eu(MT == 2 ? 2 : sizeof(TX) == 2 && KB == 1 ? 4 : 3))) void k_expand(ExpandArgs g, int col_wgs) {
     typedef Mma<TX> M;
     constexpr int C = M::kChunk, kBlock = 4 * C, V = kVec<TX>, kPieces = 16 / V, kTiles = V / 4;
     const Lane l;
@@ -531,13 +562,6 @@ __global__ __launch_bounds__(kThreads) void k_expand(ExpandArgs g, int col_wgs) 
             a[t].load(w, c < g.cols && q < g.wr ? ((unsigned)c * g.wr + q) * (unsigned)sizeof(TW) : kNowhere);
         }
     };
-    auto multiply = [&](f32x4 (&acc)[4], const Chunk<TX, TW> (&a)[4], const Left<TX> &f) __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if constexpr (sizeof(TX) == 2) acc[t] = M::mul(a[t].frag(), f.lo, acc[t]);
-            acc[t] = M::mul(a[t].frag(), f.hi, acc[t]);
-        }
-    };
     const int g0 = ((of % col_wgs) * (kThreads / 64) + l.wave) * g.groups, g1 = min(g0 + g.groups, (g.cols + 63) / 64);
     auto or_nowhere = [](unsigned row, unsigned c) { return (row | c) >= kNowhere ? kNowhere : row + c; };
     auto column = [&](int k, int p) {
@@ -550,9 +574,17 @@ __global__ __launch_bounds__(kThreads) void k_expand(ExpandArgs g, int col_wgs) 
 #pragma unroll
         for (int b = 0; b < KB; ++b) load_weights(a[b], w, k * 64, b);
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < MT; ++j) multiply(acc[j], a[b], left[b][j]);
+            for (int j = 0; j < MT; ++j) {
+                f32x4 low = {};
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    if constexpr (sizeof(TX) == 2) low = M::mul(a[b][t].frag(), left[b][j].lo, low);
+                    acc[j][t] = M::mul(a[b][t].frag(), left[b][j].hi, acc[j][t]);
+                }
+                if constexpr (sizeof(TX) == 2) acc[j][t] += bounded(low);
+            }
         for (int b = KB; b < blocks; ++b) {
             Chunk<TX, TW> o[4];
             load_weights(o, w, k * 64, b);
@@ -561,7 +593,11 @@ __global__ __launch_bounds__(kThreads) void k_expand(ExpandArgs g, int col_wgs) 
                 Left<TX> f;
                 f.load(v, left_at(b, j));
                 f.part(exponent[j]);
-                multiply(acc[j], o, f);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if constexpr (sizeof(TX) == 2) acc[j][t] += bounded(M::mul(o[t].frag(), f.lo, f32x4{}));
+                    acc[j][t] = M::mul(o[t].frag(), f.hi, acc[j][t]);
+                }
             }
         }
     };
@@ -848,11 +884,8 @@ struct BackWeights {
     int T, inner, outer, ip, op, n, r, vr, piece_rows;
 };
 
-__device__ __forceinline__ void store_grad(const BackWeights &g, int e, bool is_b, int q, int c, float s) {
-    if (is_b)
-        g.d_b[((size_t)e * g.outer + c) * g.r + q] = s;
-    else
-        g.d_a[((size_t)e * g.r + q) * g.inner + c] = s;
+__device__ __forceinline__ float *grad_at(const BackWeights &g, int e, bool is_b, int q, int c) {
+    return is_b ? g.d_b + ((size_t)e * g.outer + c) * g.r + q : g.d_a + ((size_t)e * g.r + q) * g.inner + c;
 }
 
 // d_a and d_b of one piece: 128 columns and 16 NT ranks a workgroup, 32 rows a wave at a time.
@@ -891,7 +924,6 @@ __attribute__((amdgpu_waves_per_eu(NT == 4 && sizeof(TX) == 4 ? 1 : 2))) void k_
         if (p.e < 0) return;
         order = g.order;
     }
-    const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4, wave = threadIdx.x >> 6;
     const int tiles_a = (g.ip + kPieceCols - 1) / kPieceCols;
     const bool is_b = (int)blockIdx.x >= tiles_a;
     const int c0 = (is_b ? blockIdx.x - tiles_a : blockIdx.x) * kPieceCols, cols = is_b ? g.op : g.ip;
@@ -899,110 +931,119 @@ __attribute__((amdgpu_waves_per_eu(NT == 4 && sizeof(TX) == 4 ? 1 : 2))) void k_
     const TX *m = static_cast<const TX *>(is_b ? g.d_out : g.x);
     const int64_t ld = is_b ? g.ld_d_out : g.ld_x;
     const float *left = is_b ? g.v : g.u;
-    // the lane's first column of a load; beyond the matrix its last piece (the results are dropped)
-    int at[kLoads], rank[NT];
+    // Beside an infinite x or d_out the parts' products are infinities of any sign and NaN (0 * inf): if a result is not
+    // finite, a second pass takes the first part three times, whose sums are NaN or an infinity where the result is.
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        bool bad = false;
+        int id = threadIdx.x;
+        asm volatile("" : "+v"(id));   // or addresses of all of a pass are computed ahead of the first, and spill
+        const int lane = id & 63, l16 = lane & 15, quad = lane >> 4, wave = id >> 6;
+        // the lane's first column of a load; beyond the matrix its last piece (the results are dropped)
+        int at[kLoads], rank[NT];
 #pragma unroll
-    for (int h = 0; h < kLoads; ++h) at[h] = min(c0 + h * 64 + l16 * kVec<TX>, cols - kVec<TX>);
+        for (int h = 0; h < kLoads; ++h) at[h] = min(c0 + h * 64 + l16 * kVec<TX>, cols - kVec<TX>);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) rank[i] = min(q0 + 16 * i + l16, g.r - 1);
-    f32x4 acc[NT][8] = {};
-    for (int b = p.begin + wave * 32; b < p.end; b += 32 * (kThreads / 64)) {
-        uint4 x[8][kLoads];
-        float f[NT][8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // rows 8 quad + j of the 32 (bf16: a lane's chunk of the reduction), or 4 j + quad
-            const int i = b + (kPairs ? 8 * quad + j : 4 * j + quad);
-            const int row = order[min(i, p.end - 1)];
-#pragma unroll
-            for (int h = 0; h < kLoads; ++h) x[j][h] = load_piece(m + row * ld + at[h], kVec<TX>);
-#pragma unroll
-            for (int k = 0; k < NT; ++k) f[k][j] = left[(size_t)row * g.vr + rank[k]];
-        }
-        if (b + 32 > p.end) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (b + (kPairs ? 8 * quad + j : 4 * j + quad) >= p.end) {
-#pragma unroll
-                    for (int h = 0; h < kLoads; ++h) x[j][h] = uint4{0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < NT; ++k) f[k][j] = 0.f;
-                }
-        }
-        if constexpr (kPairs) {
-            bf16x8 hi[NT], mid[NT], lo[NT];
-#pragma unroll
-            for (int k = 0; k < NT; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    bf16 h, m, w;
-                    split(f[k][j], h, m);
-                    w = narrow<bf16>(f[k][j] - widen(h) - widen(m));
-                    hi[k][j] = h;
-                    mid[k][j] = m;
-                    lo[k][j] = __builtin_isfinite(f[k][j]) ? w : narrow<bf16>(0.f);
-                }
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                u32x4 pairs;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const u32x4 r0 = __builtin_bit_cast(u32x4, x[2 * d][0]), r1 = __builtin_bit_cast(u32x4, x[2 * d + 1][0]);
-                    pairs[d] = __builtin_amdgcn_perm(r1[t / 2], r0[t / 2], t % 2 ? 0x07060302u : 0x05040100u);
-                }
-                const bf16x8 right = __builtin_bit_cast(bf16x8, pairs);
-#pragma unroll
-                for (int k = 0; k < NT; ++k) {
-                    acc[k][t] = Mma<bf16>::mul(lo[k], right, acc[k][t]);
-                    acc[k][t] = Mma<bf16>::mul(mid[k], right, acc[k][t]);
-                    acc[k][t] = Mma<bf16>::mul(hi[k], right, acc[k][t]);
-                }
-            }
-        } else {
+        for (int i = 0; i < NT; ++i) rank[i] = min(q0 + 16 * i + l16, g.r - 1);
+        f32x4 acc[NT][8] = {};
+        for (int b = p.begin + wave * 32; b < p.end; b += 32 * (kThreads / 64)) {
+            uint4 x[8][kLoads];
+            float f[NT][8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float w[8];
+                // rows 8 quad + j of the 32 (bf16: a lane's chunk of the reduction), or 4 j + quad
+                const int i = b + (kPairs ? 8 * quad + j : 4 * j + quad);
+                const int row = order[min(i, p.end - 1)];
 #pragma unroll
-                for (int h = 0; h < kLoads; ++h) {
-                    float e[kVec<TX>];
-                    unpack<TX>(x[j][h], e);
+                for (int h = 0; h < kLoads; ++h) x[j][h] = load_piece(m + row * ld + at[h], kVec<TX>);
 #pragma unroll
-                    for (int i = 0; i < kVec<TX>; ++i) w[h * kVec<TX> + i] = e[i];
+                for (int k = 0; k < NT; ++k) f[k][j] = left[(size_t)row * g.vr + rank[k]];
+            }
+            if (b + 32 > p.end) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (b + (kPairs ? 8 * quad + j : 4 * j + quad) >= p.end) {
+#pragma unroll
+                        for (int h = 0; h < kLoads; ++h) x[j][h] = uint4{0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < NT; ++k) f[k][j] = 0.f;
+                    }
+            }
+            if constexpr (kPairs) {
+                bf16x8 hi[NT], mid[NT], lo[NT];
+#pragma unroll
+                for (int k = 0; k < NT; ++k) three_parts(f[k], hi[k], mid[k], lo[k]);
+                if (pass == 1)
+#pragma unroll
+                    for (int k = 0; k < NT; ++k) mid[k] = lo[k] = hi[k];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    u32x4 pairs;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const u32x4 r0 = __builtin_bit_cast(u32x4, x[2 * d][0]), r1 = __builtin_bit_cast(u32x4, x[2 * d + 1][0]);
+                        pairs[d] = __builtin_amdgcn_perm(r1[t / 2], r0[t / 2], t % 2 ? 0x07060302u : 0x05040100u);
+                    }
+                    const bf16x8 right = __builtin_bit_cast(bf16x8, pairs);
+#pragma unroll
+                    for (int k = 0; k < NT; ++k) {
+                        acc[k][t] = Mma<bf16>::mul(lo[k], right, acc[k][t]);
+                        acc[k][t] = Mma<bf16>::mul(mid[k], right, acc[k][t]);
+                        acc[k][t] = Mma<bf16>::mul(hi[k], right, acc[k][t]);
+                    }
                 }
+            } else {
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+                for (int j = 0; j < 8; ++j) {
+                    float w[8];
 #pragma unroll
-                    for (int k = 0; k < NT; ++k)
-                        acc[k][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[k][j], w[t], acc[k][t], 0, 0, 0);
+                    for (int h = 0; h < kLoads; ++h) {
+                        float e[kVec<TX>];
+                        unpack<TX>(x[j][h], e);
+#pragma unroll
+                        for (int i = 0; i < kVec<TX>; ++i) w[h * kVec<TX> + i] = e[i];
+                    }
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+#pragma unroll
+                        for (int k = 0; k < NT; ++k)
+                            acc[k][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[k][j], w[t], acc[k][t], 0, 0, 0);
+                }
             }
         }
-    }
-    // the waves' sums, joined in order; each wave writes two of the eight column tiles
-    const int real = is_b ? g.outer : g.inner;
-    const size_t width = g.ip + g.op;
+        // the waves' sums, joined in order; each wave writes two of the eight column tiles
+        const int real = is_b ? g.outer : g.inner;
+        const size_t width = g.ip + g.op;
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
-        if (k) __syncthreads();
+        for (int k = 0; k < NT; ++k) {
+            if (k) __syncthreads();
 #pragma unroll
-        for (int t = 0; t < 8; ++t) part[wave][t][lane] = acc[k][t];
-        __syncthreads();
+            for (int t = 0; t < 8; ++t) part[wave][t][lane] = acc[k][t];
+            __syncthreads();
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int t = 2 * wave + s;
-            const int c = c0 + (kLoads == 2 ? 64 * (t / 4) + 4 * l16 + t % 4 : 8 * l16 + t);
-            f32x4 sum = part[0][t][lane];
+            for (int s = 0; s < 2; ++s) {
+                const int t = 2 * wave + s;
+                const int c = c0 + (kLoads == 2 ? 64 * (t / 4) + 4 * l16 + t % 4 : 8 * l16 + t);
+                f32x4 sum = part[0][t][lane];
 #pragma unroll
-            for (int w = 1; w < kThreads / 64; ++w) sum += part[w][t][lane];
+                for (int w = 1; w < kThreads / 64; ++w) sum += part[w][t][lane];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int q = q0 + 16 * k + 4 * quad + i;
-                if (q >= g.r || c >= real) continue;
-                if (p.count == 1)
-                    store_grad(g, p.e, is_b, q, c, sum[i]);
-                else
-                    g.partial[((size_t)blockIdx.y * g.r + q) * width + (is_b ? g.ip : 0) + c] = sum[i];
+                for (int i = 0; i < 4; ++i) {
+                    const int q = q0 + 16 * k + 4 * quad + i;
+                    if (q >= g.r || c >= real) continue;
+                    float *to = p.count == 1 ? grad_at(g, p.e, is_b, q, c)
+                                             : g.partial + ((size_t)blockIdx.y * g.r + q) * width + (is_b ? g.ip : 0) + c;
+                    if (pass == 0) {
+                        *to = sum[i];
+                        bad |= !__builtin_isfinite(sum[i]);
+                    } else if (!__builtin_isfinite(sum[i]) && !__builtin_isfinite(*to)) {
+                        *to = sum[i];
+                    }
+                }
             }
         }
+        if constexpr (!kPairs) break;
+        if (!__syncthreads_or(bad)) break;
     }
 }
 
@@ -1026,7 +1067,7 @@ __global__ __launch_bounds__(kThreads) void k_back_join(BackWeights g) {
     float s = 0.f;
 #pragma unroll 4
     for (int p = 0; p < count; ++p) s += g.partial[((size_t)(first + p) * g.r + q) * width + at];
-    store_grad(g, e, is_b, q, c, s);
+    *grad_at(g, e, is_b, q, c) = s;
 }
 
 // Sizes of a backward call and where its workspace holds what (element sizes as for fp32: the entry
