@@ -223,23 +223,31 @@ __device__ inline void split(float v, T &hi, T &lo) {
     lo = narrow<T>(__builtin_isfinite(rest) ? rest : 0.f);
 }
 
-// The 24 bits of fp32 values, 8 a part, without a rounding: f = hi + mid + lo (of an infinity the latter two are NaN).
-__device__ __forceinline__ void three_parts(float (&f)[8], bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
-    auto cut = [&](bool last) __attribute__((always_inline)) {
-        u32x4 top;
+// The first 8 bits of fp32 values as bf16, and what is left of them.
+__device__ __forceinline__ bf16x8 cut(float (&f)[8]) {
+    u32x4 top;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const uint32_t a = __float_as_uint(f[2 * d]), b = __float_as_uint(f[2 * d + 1]);
-            top[d] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-            if (last) continue;
-            f[2 * d] -= __uint_as_float(a & 0xFFFF0000u);
-            f[2 * d + 1] -= __uint_as_float(b & 0xFFFF0000u);
-        }
-        return __builtin_bit_cast(bf16x8, top);
-    };
-    hi = cut(false);
-    mid = cut(false);
-    lo = cut(true);
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t a = __float_as_uint(f[2 * d]), b = __float_as_uint(f[2 * d + 1]);
+        top[d] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+        f[2 * d] -= __uint_as_float(a & 0xFFFF0000u);
+        f[2 * d + 1] -= __uint_as_float(b & 0xFFFF0000u);
+    }
+    return __builtin_bit_cast(bf16x8, top);
+}
+// All 24 bits: f = hi + mid + lo (of an infinity the latter two are NaN).
+__device__ __forceinline__ void three_parts(float (&f)[8], bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
+    hi = cut(f);
+    mid = cut(f);
+    lo = cut(f);
+}
+// The 11 bits of fp16 values: w = hi + lo.
+__device__ __forceinline__ void two_parts(f16x8 w, bf16x8 &hi, bf16x8 &lo) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = widen(w[i]);
+    hi = cut(f);
+    lo = cut(f);
 }
 
 // The low parts' products of a sum whose high parts' products are added to it.  Beside an infinite operand they are a
@@ -437,13 +445,14 @@ __global__ __launch_bounds__(64 * kShrinkWaves) __attribute__((amdgpu_waves_per_
     }
 }
 
-// v's operand for the second product: fp32 as it is, 16-bit types in two parts; fp16, whose range
-// v may exceed, after a power of two per row.
+// v's operand for the second product: fp32 as it is; beside bf16 weights in two parts; beside fp16 ones in three of
+// bf16, which has the range that v may take (fp16 parts lost components 2^14 below a row's largest).
 template <typename TX>
 struct Left {
     static constexpr int C = Mma<TX>::kChunk;
+    typedef typename std::conditional<sizeof(TX) == 4, f32x4, bf16x8>::type Part;
     float raw[C];
-    typename Mma<TX>::Frag hi, lo;
+    Part hi, mid, lo;
     __device__ __forceinline__ void load(Buffer v, unsigned at) {
 #pragma unroll
         for (int i = 0; i < C; i += 4) {
@@ -452,28 +461,42 @@ struct Left {
             for (int k = 0; k < 4; ++k) raw[i + k] = f[k];
         }
     }
-    __device__ __forceinline__ float most(float m) const {
+    __device__ __forceinline__ void part() {
+        if constexpr (sizeof(TX) == 4) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const float a = fabsf(raw[i]);
-            m = a < __builtin_inff() ? fmaxf(m, a) : m;
-        }
-        return m;
-    }
-    __device__ __forceinline__ void part(int exponent) {
+            for (int i = 0; i < C; ++i) hi[i] = raw[i];
+        } else if constexpr (std::is_same_v<TX, f16>) {
+            three_parts(raw, hi, mid, lo);
+        } else {
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            if constexpr (sizeof(TX) == 4) {
-                hi[i] = raw[i];
-            } else {
-                TX a, b;
-                split(std::is_same_v<TX, f16> ? ldexpf(raw[i], -exponent) : raw[i], a, b);
+            for (int i = 0; i < C; ++i) {
+                bf16 a, b;
+                split(raw[i], a, b);
                 hi[i] = a;
                 lo[i] = b;
             }
         }
     }
 };
+
+// Adds w v to the sums of the high parts' products and of the others.  fp16 weights are cut into two bf16 parts (the
+// kernel with 8192 rows of 2048 columns, rank 64: 29.0 us, with fp32 products 37.4; rank 16: 23.1 and 25.0).
+template <typename TX, typename TW>
+__device__ __forceinline__ void multiply(const Chunk<TX, TW> &w, const Left<TX> &f, f32x4 &high, f32x4 &low) {
+    if constexpr (std::is_same_v<TX, f16>) {
+        bf16x8 wh, wl;
+        two_parts(w.frag(), wh, wl);
+        low = Mma<bf16>::mul(wl, f.lo, low);
+        low = Mma<bf16>::mul(wl, f.mid, low);
+        low = Mma<bf16>::mul(wh, f.lo, low);
+        low = Mma<bf16>::mul(wl, f.hi, low);
+        low = Mma<bf16>::mul(wh, f.mid, low);
+        high = Mma<bf16>::mul(wh, f.hi, high);
+    } else {
+        if constexpr (sizeof(TX) == 2) low = Mma<TX>::mul(w.frag(), f.lo, low);
+        high = Mma<TX>::mul(w.frag(), f.hi, high);
+    }
+}
 
 // out = base + v w^T, w a row's own adapter's: the forward's B, the backward's A transposed.
 struct ExpandArgs {
@@ -526,30 +549,15 @@ __attribute__((amdgpu_waves_per_eu(MT == 2 ? 2 : sizeof(TX) == 2 && KB == 1 ? 4 
         return e[j] >= 0 && q < g.vr ? ((16 * j + l.l16) * g.vr + q) * 4u : kNowhere;   // 0 for a row without an adapter
     };
     Left<TX> left[KB][MT];
-    int exponent[MT] = {};
     if (first >= 0) {
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int j = 0; j < MT; ++j) left[b][j].load(v, left_at(b, j));
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            if constexpr (std::is_same_v<TX, f16>) {
-                float most = 0.f;
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
-                for (int b = 0; b < KB; ++b) most = left[b][j].most(most);
-                for (int b = KB; b < blocks; ++b) {
-                    Left<TX> f;
-                    f.load(v, left_at(b, j));
-                    most = f.most(most);
-                }
-                most = fmaxf(most, __shfl_xor(most, 16));
-                most = fmaxf(most, __shfl_xor(most, 32));
-                if (most > 0.f) frexpf(most, &exponent[j]);
-            }
-#pragma unroll
-            for (int b = 0; b < KB; ++b) left[b][j].part(exponent[j]);
-        }
+            for (int j = 0; j < MT; ++j) left[b][j].part();
     }
     auto weights = [&](int now) {
         return buffer(static_cast<const TW *>(g.w) + (size_t)now * g.w_rows * g.wr, (size_t)g.w_rows * g.wr * sizeof(TW));
@@ -579,10 +587,7 @@ __attribute__((amdgpu_waves_per_eu(MT == 2 ? 2 : sizeof(TX) == 2 && KB == 1 ? 4 
             for (int j = 0; j < MT; ++j) {
                 f32x4 low = {};
 #pragma unroll
-                for (int b = 0; b < KB; ++b) {
-                    if constexpr (sizeof(TX) == 2) low = M::mul(a[b][t].frag(), left[b][j].lo, low);
-                    acc[j][t] = M::mul(a[b][t].frag(), left[b][j].hi, acc[j][t]);
-                }
+                for (int b = 0; b < KB; ++b) multiply(a[b][t], left[b][j], acc[j][t], low);
                 if constexpr (sizeof(TX) == 2) acc[j][t] += bounded(low);
             }
         for (int b = KB; b < blocks; ++b) {
@@ -592,11 +597,12 @@ __attribute__((amdgpu_waves_per_eu(MT == 2 ? 2 : sizeof(TX) == 2 && KB == 1 ? 4 
             for (int j = 0; j < MT; ++j) {
                 Left<TX> f;
                 f.load(v, left_at(b, j));
-                f.part(exponent[j]);
+                f.part();
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    if constexpr (sizeof(TX) == 2) acc[j][t] += bounded(M::mul(o[t].frag(), f.lo, f32x4{}));
-                    acc[j][t] = M::mul(o[t].frag(), f.hi, acc[j][t]);
+                    f32x4 low = {};
+                    multiply(o[t], f, acc[j][t], low);
+                    if constexpr (sizeof(TX) == 2) acc[j][t] += bounded(low);
                 }
             }
         }
@@ -637,8 +643,7 @@ __attribute__((amdgpu_waves_per_eu(MT == 2 ? 2 : sizeof(TX) == 2 && KB == 1 ? 4 
                 unpack<TX>(__builtin_bit_cast(uint4, held[j][p]), sum);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    float s = res[j][(p * V + i) / 4][i % 4];
-                    if constexpr (std::is_same_v<TX, f16>) s = ldexpf(s, exponent[j]);
+                    const float s = res[j][(p * V + i) / 4][i % 4];
                     sum[i] += e[j] >= 0 ? s : 0.f;
                 }
                 store16(out, or_nowhere(out_row[j], column(k, p)), __builtin_bit_cast(u32x4, pack<TX>(sum)));

@@ -1,11 +1,12 @@
-"""Adapters on values that are hard to hold: infinities among the operands, and all 24 bits of v and u."""
+"""Adapters on values that are hard to hold: infinities among the operands, all 24 bits of v and u, and
+a wide range of them."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import tokens as ref
-from test_gpu_adapters import backward, forward, make, numbers
-from token_harness import DTYPES
+from test_gpu_adapters import backward, forward, make, numbers, sizes
+from token_harness import DTYPES, assert_near
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +100,31 @@ def test_gradients_of_single_rows_hold_all_of_v_and_u(T, r, dt, wt):
     got = backward(s)
     for g, w in zip(got[1:], want[1:]):
         assert np.array_equal(g.double().cpu().numpy(), w)
+
+
+# rows of one kernel each (forward), blocks of 16 rows, ranks beyond the ones a wave keeps, blocks of 32 rows
+WIDE = [(40, 16), (1500, 16), (1500, 100), (4200, 32), (8200, 64)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,r", WIDE)
+@pytest.mark.parametrize("m", [12, 20, 28])
+def test_components_far_below_the_largest(T, r, m, dt):
+    """v and u with one component 2^m above the others, which weights of zero keep out of the result."""
+    s = make(T, 3, r, 64, 72, dt, dt, "runs", seed=950 + m)
+    up, down = 2.0 ** (m // 2), 2.0 ** -(m // 2)
+    t = dict(s, a=s["a"] * down, b=s["b"] * up)
+    t["a"][:, 0], t["b"][:, :, 0] = s["a"][:, 0] * up, 0
+    mm, dtype = numbers(t), s["x"].dtype
+    z = sizes(mm)
+    want = ref.adapters(mm["x"], mm["adapter"], mm["a"], mm["b"], mm["scale"])
+    size = ref.adapters(z["x"], mm["adapter"], z["a"], z["b"], z["scale"])
+    assert_near(forward(t), want, dtype, (64 + r + 16) * 2.0 ** -23 * size)
+    t = dict(s, b=s["b"] * down, a=s["a"] * up)
+    t["b"][:, :, 0], t["a"][:, 0] = s["b"][:, :, 0] * up, 0
+    mm = numbers(t)
+    z = sizes(mm)
+    args = [(q["d_out"], q["x"], mm["adapter"], q["a"], q["b"], q["scale"]) for q in (mm, z)]
+    want, size = ref.adapters_backward(*args[0]), ref.adapters_backward(*args[1])
+    for g, w, e, terms, of in zip(backward(t), want, size, (72 + r, 72 + T, 64 + T), (dtype, torch.float32, torch.float32)):
+        assert_near(g, w, of, (terms + 16) * 2.0 ** -23 * e)
