@@ -215,14 +215,6 @@ struct Chunk {
     }
 };
 
-// Two parts of v whose sum is v to 16 bits or more; an infinity is all in the first.
-template <typename T>
-__device__ inline void split(float v, T &hi, T &lo) {
-    hi = narrow<T>(v);
-    const float rest = v - widen(hi);
-    lo = narrow<T>(__builtin_isfinite(rest) ? rest : 0.f);
-}
-
 // The first 8 bits of fp32 values as bf16, and what is left of them.
 __device__ __forceinline__ bf16x8 cut(float (&f)[8]) {
     u32x4 top;
@@ -445,8 +437,9 @@ __global__ __launch_bounds__(64 * kShrinkWaves) __attribute__((amdgpu_waves_per_
     }
 }
 
-// v's operand for the second product: fp32 as it is; beside bf16 weights in two parts; beside fp16 ones in three of
-// bf16, which has the range that v may take (fp16 parts lost components 2^14 below a row's largest).
+// v's operand for the second product: fp32 as it is, beside 16-bit weights in three parts of bf16, which has the range
+// that v may take (fp16 parts lost components 2^14 below a row's largest).  Two parts beside bf16 weights were no
+// faster (8192 rows of 2048 columns, rank 16: the call 36.0 us against 36.3; rank 64: 57.2 against 56.6).
 template <typename TX>
 struct Left {
     static constexpr int C = Mma<TX>::kChunk;
@@ -465,16 +458,8 @@ struct Left {
         if constexpr (sizeof(TX) == 4) {
 #pragma unroll
             for (int i = 0; i < C; ++i) hi[i] = raw[i];
-        } else if constexpr (std::is_same_v<TX, f16>) {
-            three_parts(raw, hi, mid, lo);
         } else {
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                bf16 a, b;
-                split(raw[i], a, b);
-                hi[i] = a;
-                lo[i] = b;
-            }
+            three_parts(raw, hi, mid, lo);
         }
     }
 };
@@ -493,7 +478,7 @@ __device__ __forceinline__ void multiply(const Chunk<TX, TW> &w, const Left<TX> 
         low = Mma<bf16>::mul(wh, f.mid, low);
         high = Mma<bf16>::mul(wh, f.hi, high);
     } else {
-        if constexpr (sizeof(TX) == 2) low = Mma<TX>::mul(w.frag(), f.lo, low);
+        if constexpr (sizeof(TX) == 2) low = Mma<TX>::mul(w.frag(), f.mid, Mma<TX>::mul(w.frag(), f.lo, low));
         high = Mma<TX>::mul(w.frag(), f.hi, high);
     }
 }

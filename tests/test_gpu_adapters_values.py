@@ -128,3 +128,35 @@ def test_components_far_below_the_largest(T, r, m, dt):
     want, size = ref.adapters_backward(*args[0]), ref.adapters_backward(*args[1])
     for g, w, e, terms, of in zip(backward(t), want, size, (72 + r, 72 + T, 64 + T), (dtype, torch.float32, torch.float32)):
         assert_near(g, w, of, (terms + 16) * 2.0 ** -23 * e)
+
+
+@pytest.mark.parametrize("dt,wt", [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("T,r", [(24, 2), (1100, 2), (1500, 40), (1500, 90), (8200, 64)])
+def test_products_that_cancel(T, r, dt, wt):
+    """Two ranks with v = s p and v = s p q, of weights q and -1: what is left of s p q - s p q are the roundings of v and
+    of the sum of the two products, in three parts each at most: 8 times 2^-23 of the products' sizes."""
+    n, inner, outer, q = 5, 64, 72, 1 + 2.0 ** -7
+    s = make(T, n, r, inner, outer, dt, wt, "mixed", seed=980)
+    rng = np.random.default_rng(T + r)
+    one, other = rng.permutation(r)[:2]
+
+    def single(t):
+        t.zero_()
+        at = torch.from_numpy(rng.integers(0, t.shape[1], T)).cuda()
+        t[torch.arange(T, device="cuda"), at] = torch.from_numpy(2.0 ** rng.integers(-3, 4, T)).to(t.dtype).cuda()
+
+    for name in ("x", "d_out"):
+        single(s[name])
+    for a, b in (((1, q), (q, -1)), ((q, -1), (1, q))):     # of the forward; of the backward
+        s["a"].zero_()
+        s["b"].zero_()
+        s["a"][:, one], s["a"][:, other] = a
+        s["b"][:, :, one], s["b"][:, :, other] = b
+        m = numbers(s)
+        z, dtype = sizes(m), s["x"].dtype
+        if a[0] == 1:
+            assert_near(forward(s), np.zeros((T, outer)), dtype,
+                        2.0 ** -20 * ref.adapters(z["x"], m["adapter"], z["a"], z["b"], z["scale"]))
+        else:
+            size = ref.adapters_backward(z["d_out"], z["x"], m["adapter"], z["a"], z["b"], z["scale"])[0]
+            assert_near(backward(s)[0], np.zeros((T, inner)), dtype, 2.0 ** -20 * size)
