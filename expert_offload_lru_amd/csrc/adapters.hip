@@ -1152,10 +1152,12 @@ hipError_t shrink(const ShrinkArgs &g, int jobs, hipStream_t stream) {
     // adapters of rank 16: 51 and 55)
     const int turns = std::min(g.n, std::max(2, std::min(16, 1024 / tiles)));
     const dim3 grid(tiles, turns, jobs), block(64 * kShrinkWaves);
-    if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
-    if (MT == 1 && tiles * jobs <= kFewTiles) {
-        const int groups = (g.r + 15) / 16;
-        return launch(k_shrink<TX, TW, 1, MT, TILED>, dim3(tiles, turns * groups, jobs), block, stream, nullptr, nullptr, g, groups);
+    if constexpr (MT == 1) {   // (taller blocks are for ranks from 17 on and many rows)
+        if (g.r <= 16) return launch(k_shrink<TX, TW, 1, MT, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
+        if (tiles * jobs <= kFewTiles) {
+            const int groups = (g.r + 15) / 16;
+            return launch(k_shrink<TX, TW, 1, MT, TILED>, dim3(tiles, turns * groups, jobs), block, stream, nullptr, nullptr, g, groups);
+        }
     }
     if (g.r <= 32) return launch(k_shrink<TX, TW, 2, MT, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
     return launch(k_shrink<TX, TW, 4, MT, TILED>, grid, block, stream, nullptr, nullptr, g, 1);
@@ -1170,7 +1172,8 @@ hipError_t expand(ExpandArgs g, hipStream_t stream) {
     const int col_wgs = (groups + 4 * g.groups - 1) / (4 * g.groups);
     const dim3 grid((tiles + 7) / 8 * 8 * col_wgs), block(kThreads);
     constexpr int kBlock = 4 * Mma<TX>::kChunk;
-    if (g.wr <= kBlock) return launch(k_expand<TX, TW, 1, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
+    if constexpr (MT == 1 || kBlock > 16)
+        if (g.wr <= kBlock) return launch(k_expand<TX, TW, 1, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
     if constexpr (kBlock < 32)
         if (g.wr > 2 * kBlock) return launch(k_expand<TX, TW, 4, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
     return launch(k_expand<TX, TW, 2, MT>, grid, block, stream, nullptr, nullptr, g, col_wgs);
