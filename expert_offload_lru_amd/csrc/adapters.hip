@@ -1094,7 +1094,7 @@ BackSpace back_space(int T, int inner, int outer, int n, int r, bool copies) {
     // whole runs of columns, 64 elements for 16-bit activations
     s.aw = take(adapters * tiled_size(r, inner, 8) * 4);
     s.bw = take(adapters * tiled_size(r, outer, 8) * 4);
-    s.partial = take((size_t)s.max_pieces * r * (s.ip + s.op) * 4);
+    s.partial = take(T <= kSmallBack ? 0 : (size_t)s.max_pieces * r * (s.ip + s.op) * 4);   // (few rows: no pieces to join)
     s.x = take(s.padded ? row * s.ip * 4 : 0);
     s.d_out = take(s.padded ? row * s.op * 4 : 0);
     s.d_x = take(s.padded ? row * s.ip * 4 : 0);

@@ -96,3 +96,14 @@ def test_rows_in_the_order_of_a_dispatch():
     want = ref.adapters(m["x"], m["adapter"], m["a"], m["b"], m["scale"])
     assert_near(forward(s), want, torch.bfloat16, forward_slack(m, torch.bfloat16, False))
     check_backward(s, m, backward(s), False)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,n,r", [(1, 6, 64), (300, 20, 24), (512, 40, 16)])
+def test_workspace_of_few_rows_is_enough(T, n, r, dt):
+    """Nothing is written behind the bytes that a call of few rows asks for."""
+    s = make(T, n, r, 64, 72, dt, dt, "mixed", seed=1500)
+    need = moe.gpu_lib().moe_adapters_workspace(T, 64, 72, n, r)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    check_backward(s, numbers(s), backward(s, workspace=ws[:need]), False)
+    assert (ws[need:] == 0xFF).all()
