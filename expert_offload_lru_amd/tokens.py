@@ -5,6 +5,10 @@ library's kernels on ``stream`` (default: the current stream of that GPU).  Outp
 the caller holds.  A matrix needs unit stride along its rows (a column slice of a wider matrix will
 do); index, gate, scale, adapter and adapter-gradient tensors are contiguous.  ``MoeError`` with
 ``ERR_INVALID`` or ``ERR_UNSUPPORTED`` says what was refused; nothing is enqueued then.
+
+Nothing here is recorded by torch's autograd: an output has no gradient, whether or not an input requires
+one, and the ``_backward`` functions are the gradients, called by the training step (or from the ``backward``
+of a ``torch.autograd.Function``).  Outputs count as modified in place.
 """
 import functools
 
@@ -19,6 +23,9 @@ _TYPES = {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16}
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
                    or (lambda gpu: torch.cuda.current_stream(gpu).cuda_stream))
+# tells torch's autograd of outputs written through their addresses, so that a graph that has kept one refuses to run
+# backward on the new values (a third of torch.autograd.graph.increment_version's time)
+_written = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
 
 
 def _refuse(msg):
@@ -70,11 +77,11 @@ def _type(name, t):
     return code, gpu
 
 
-def _call(fn, gpu, stream, *args):
-    """The library call with `gpu` current and the stream's handle as last argument."""
+def _call(fn, outputs, gpu, stream, *args):
+    """The library call with `gpu` current and the stream's handle as last argument, writing the tensors of `outputs`."""
     if _current_device() != gpu:
         with torch.cuda.device(gpu):
-            return _call(fn, gpu, stream, *args)
+            return _call(fn, outputs, gpu, stream, *args)
     if stream is None:
         handle = _current_stream(gpu)
     else:
@@ -82,6 +89,7 @@ def _call(fn, gpu, stream, *args):
     rc = fn(*args, handle)
     if rc != OK:
         raise MoeError(rc, gpu_lib().moe_last_error().decode())
+    _written(outputs)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -134,7 +142,8 @@ def tokens_dispatch(x, ids, n_experts, rows, offsets, pos, src, expert, workspac
     p_exp = _array("expert", expert, (n,), i32, gpu)
     need = _needed("moe_tokens_workspace", T, k, n_experts)
     ws = _workspace(need, workspace, gpu, stream) if need else None
-    _call(lib.moe_tokens_dispatch, gpu, stream, px, ldx, dtype, T, H, p_ids, k, n_experts, pr, ldr, p_off, p_pos,
+    outputs = (offsets, pos, src, expert) if x is None else (rows, offsets, pos, src, expert)
+    _call(lib.moe_tokens_dispatch, outputs, gpu, stream, px, ldx, dtype, T, H, p_ids, k, n_experts, pr, ldr, p_off, p_pos,
           p_src, p_exp, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
 
 
@@ -145,7 +154,7 @@ def tokens_dispatch_backward(d_rows, pos, d_x, stream=None):
     pr, ldr = _matrix("d_rows", d_rows, R, H, d_rows.dtype, gpu)
     px, ldx = _matrix("d_x", d_x, T, H, d_rows.dtype, gpu)
     p_pos = _array("pos", pos, (T, k), torch.int32, gpu)
-    _call(gpu_lib().moe_tokens_dispatch_backward, gpu, stream, pr, ldr, R, dtype, T, H, p_pos, k, px, ldx)
+    _call(gpu_lib().moe_tokens_dispatch_backward, (d_x,), gpu, stream, pr, ldr, R, dtype, T, H, p_pos, k, px, ldx)
 
 
 def tokens_combine(rows, pos, gate, out, base=None, stream=None):
@@ -157,7 +166,7 @@ def tokens_combine(rows, pos, gate, out, base=None, stream=None):
     pb, ldb = (None, H) if base is None else _matrix("base", base, T, H, rows.dtype, gpu)
     p_pos = _array("pos", pos, (T, k), torch.int32, gpu)
     p_gate = _array("gate", gate, (T, k), torch.float32, gpu)
-    _call(gpu_lib().moe_tokens_combine, gpu, stream, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pb, ldb, po, ldo)
+    _call(gpu_lib().moe_tokens_combine, (out,), gpu, stream, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pb, ldb, po, ldo)
 
 
 def tokens_combine_backward(d_out, rows, pos, gate, d_rows, d_gate, stream=None):
@@ -171,8 +180,8 @@ def tokens_combine_backward(d_out, rows, pos, gate, d_rows, d_gate, stream=None)
     p_pos = _array("pos", pos, (T, k), torch.int32, gpu)
     p_gate = _array("gate", gate, (T, k), torch.float32, gpu)
     p_dgate = _array("d_gate", d_gate, (T, k), torch.float32, gpu)
-    _call(gpu_lib().moe_tokens_combine_backward, gpu, stream, pd, ldd, pr, ldr, R, dtype, T, H, p_pos, p_gate, k, pg,
-          ldg, p_dgate)
+    _call(gpu_lib().moe_tokens_combine_backward, (d_rows, d_gate), gpu, stream, pd, ldd, pr, ldr, R, dtype, T, H, p_pos,
+          p_gate, k, pg, ldg, p_dgate)
 
 
 def _adapter_shapes(a, b, gpu):
@@ -203,8 +212,8 @@ def adapters_forward(x, adapter, a, b, scale, out, base=None, workspace=None, st
     need = _needed("moe_adapters_forward_workspace_strided" if strided and workspace is None else
                    "moe_adapters_forward_workspace", T, inner, outer, n, r)
     ws = _workspace(need, workspace, gpu, stream) if need else None
-    _call(lib.moe_adapters_forward, gpu, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb, wtype,
-          p_scale, n, r, po, ldo, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
+    _call(lib.moe_adapters_forward, (out,), gpu, stream, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
+          wtype, p_scale, n, r, po, ldo, ws.data_ptr() if need else None, ws.numel() * ws.element_size() if need else 0)
 
 
 def adapters_backward(d_out, x, adapter, a, b, scale, d_x, d_a, d_b, dx_base=None, workspace=None, stream=None):
@@ -226,5 +235,5 @@ def adapters_backward(d_out, x, adapter, a, b, scale, d_x, d_a, d_b, dx_base=Non
     strided = (px | pd | pg | (p_base or 0) | (ldx | ldd | ldg | ldb) * x.element_size()) & 15
     need = _needed("moe_adapters_workspace_strided" if strided else "moe_adapters_workspace", T, inner, outer, n, r)
     ws = _workspace(need, workspace, gpu, stream)
-    _call(lib.moe_adapters_backward, gpu, stream, pd, ldd, px, ldx, p_base, ldb, dtype, T, inner, outer, p_ad, pa, pb,
-          wtype, p_scale, n, r, pg, ldg, p_da, p_db, ws.data_ptr(), ws.numel() * ws.element_size())
+    _call(lib.moe_adapters_backward, (d_x, d_a, d_b), gpu, stream, pd, ldd, px, ldx, p_base, ldb, dtype, T, inner, outer,
+          p_ad, pa, pb, wtype, p_scale, n, r, pg, ldg, p_da, p_db, ws.data_ptr(), ws.numel() * ws.element_size())
