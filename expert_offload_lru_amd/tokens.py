@@ -79,6 +79,8 @@ def _type(name, t):
 
 def _call(fn, outputs, gpu, stream, *args):
     """The library call with `gpu` current and the stream's handle as last argument, writing the tensors of `outputs`."""
+    if stream is not None and not isinstance(stream, int) and stream.device_index != gpu:
+        _refuse(f"stream is one of GPU {stream.device_index}, the tensors are on GPU {gpu}")
     if _current_device() != gpu:
         with torch.cuda.device(gpu):
             return _call(fn, outputs, gpu, stream, *args)
