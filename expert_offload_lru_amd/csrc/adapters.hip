@@ -13,7 +13,8 @@ namespace {
 // The row's cost grows with the work, the blocks' start at 7 to 11 us and grow with the adapters mixed in a
 // block.  Rank 16 of 2048 x 2048: 256 rows 8.8 us a row against 11.1, 512 rows 13.3 against 11.3, but 16.5
 // against 26.8 with 256 adapters mixed; 1024 rows 16.3 against 12.4.  Rank 64, 128 rows: 19.5 against 11.7,
-// but 23 against 36 with 128 adapters mixed.
+// but 23 against 36 with 128 adapters mixed (how many are mixed is known on the device alone; n, which the rule
+// does not ask, only bounds it).
 // Rank 8 of 512 x 512: 1024 rows 5.5 against 7.8, 2048 rows 7.9 against 8.4, 4096 rows 12.2 against 9.3.
 constexpr int kRowCalls = 1024;
 constexpr int64_t kRowWork = 1 << 25;    // rows x rank x (inner + outer)

@@ -200,7 +200,8 @@ def adapters_forward(x, adapter, a, b, scale, out, base=None, workspace=None, st
     and base [T, outer]; base may be out, and None stands for zeros.  a and b have x's type, or any
     type beside fp32 activations.  A call of many rows needs a workspace: the caller's (any contiguous
     tensor of enough bytes, 16-byte aligned) or one of its own,
-    with room for copies where rows do not start at multiples of 16 bytes.
+    with room for copies where rows do not start at multiples of 16 bytes.  Many rows are faster with an a and
+    b that start at such multiples too.
     """
     lib = gpu_lib()
     (dtype, gpu), T = _type("x", x), _dims("x", x, 2)[0]

@@ -5,7 +5,9 @@
  *
  * moe_layer_forward (moe_offload.h) does its own grouping; these entry points are for products that
  * a caller runs on the routed rows itself: adapters trained or served beside the frozen 4-bit
- * experts, or experts of its own.
+ * experts, or experts of its own.  The gradients are of these operators alone: the layer's experts
+ * and router have none.  The layer gives its routing as host arrays (moe_cache_last_routing), so a
+ * step that takes ids and gates from there copies them to the device, and no one graph holds both.
  *
  * Conventions (those of moe_offload.h, and)
  *  - Every function enqueues its kernels on `stream` (a hipStream_t as void*) of the current device
@@ -13,7 +15,9 @@
  *    call may be captured into a graph.  Pointers are memory of that device.
  *  - Two calls may run at once if neither writes what the other reads or writes (workspaces included).
  *  - dtype (MOE_T_*) is the type of every tensor without a type of its own; gates, scales and the
- *    adapters' gradients are fp32, indexes int32.  Sums are held in fp32 and rounded once.
+ *    adapters' gradients are fp32, indexes int32.  Sums (and the adapters' v and u below) are held
+ *    in fp32, and a result is rounded once.  An infinite operand gives the infinities and NaN that
+ *    the formula gives.
  *  - Matrices are row-major; ld is the number of elements from one row to the next (>= the row's
  *    length).  No alignment beyond the element's own is needed; rows that start at multiples of 16
  *    bytes are the fast case.
@@ -89,7 +93,9 @@ int moe_tokens_combine_backward(const void *d_out, int64_t ld_d_out, const void 
  * are as right, only slower.  workspace: moe_adapters_forward_workspace bytes (NULL if that is 0, as it
  * is for few rows), 16-byte aligned.  Where x, base or out have rows that do not start at multiples of 16
  * bytes, moe_adapters_forward_workspace_strided bytes let the call copy them to such rows first, which is
- * faster than the way it takes with less.  Limits: rank <= 256; n_rows, inner and outer below 2^24. */
+ * faster than the way it takes with less.  Many rows want a and b to start at multiples of 16 bytes too
+ * (a where inner is a multiple of 8, b where rank is); otherwise either workspace gives the slower way.
+ * Limits: rank <= 256; n_rows, inner and outer below 2^24. */
 size_t moe_adapters_forward_workspace(int n_rows, int inner, int outer, int n_adapters, int rank);
 size_t moe_adapters_forward_workspace_strided(int n_rows, int inner, int outer, int n_adapters, int rank);
 int moe_adapters_forward(const void *x, int64_t ld_x, const void *base, int64_t ld_base, int dtype, int n_rows,
