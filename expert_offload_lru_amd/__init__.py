@@ -11,6 +11,7 @@ If the GPU library has not been built, importing :class:`Cache` raises: there
 is no fallback path.
 """
 import ctypes
+import importlib
 import os
 
 import numpy as np
@@ -177,6 +178,22 @@ def _declare_gpu(lib):
     lib.moe_adapters_forward.argtypes = [vp, ld, vp, ld, i, i, i, i, vp, vp, vp, i, vp, i, i, vp, ld, vp, sz, vp]
     lib.moe_adapters_backward.argtypes = [vp, ld, vp, ld, vp, ld, i, i, i, i, vp, vp, vp, i, vp, i, i, vp, ld, vp, vp,
                                           vp, sz, vp]
+    f = ctypes.c_float
+    lib.moe_rows_encode.argtypes = [vp, ld, i, i, i, vp, ld, vp, ld, vp]
+    lib.moe_rows_decode.argtypes = [vp, ld, vp, ld, i, i, i, vp, ld, vp]
+    lib.moe_experts_hidden.argtypes = [vp, ld, i, i, i, i, vp, i, vp, i, vp, ld, vp, ld, vp, ld, vp, ld, vp]
+    lib.moe_experts_hidden_backward.argtypes = [vp, ld, i, i, i, i, vp, i, vp, i, vp, ld, vp, ld, vp, ld, vp, ld, vp, ld,
+                                                vp]
+    lib.moe_experts_product.argtypes = [vp, ld, i, i, i, i, vp, i, vp, vp, ld, vp]
+    lib.moe_experts_product_workspace.argtypes = [i, i, i, i]
+    lib.moe_experts_product_workspace.restype = sz
+    lib.moe_experts_product_backward.argtypes = [vp, ld, i, i, i, i, vp, i, vp, vp, ld, vp, ld, vp, ld, vp, ld, vp, vp,
+                                                 sz, vp]
+    lib.moe_block_norm.argtypes = [vp, ld, vp, ld, i, i, i, vp, vp, i, vp, vp, f, vp, ld, vp, ld, vp, vp]
+    lib.moe_block_norm_workspace.argtypes = [i, i, i]
+    lib.moe_block_norm_workspace.restype = sz
+    lib.moe_block_norm_backward.argtypes = [vp, ld, vp, ld, vp, ld, vp, ld, i, i, i, vp, vp, i, vp, vp, vp, vp, ld, vp, ld,
+                                            vp, vp, vp, vp, vp, sz, vp]
 
 
 _gpu_lib = None
@@ -488,14 +505,18 @@ class Planner:
             pass
 
 
-_TOKEN_OPS = ("tokens_dispatch", "tokens_dispatch_backward", "tokens_combine", "tokens_combine_backward",
-              "adapters_forward", "adapters_backward")
+_TORCH_OPS = {
+    "tokens": ("tokens_dispatch", "tokens_dispatch_backward", "tokens_combine", "tokens_combine_backward",
+               "adapters_forward", "adapters_backward"),
+    "experts": ("rows_encode", "rows_decode", "experts_hidden", "experts_hidden_backward", "experts_product",
+                "experts_product_backward", "block_norm", "block_norm_backward"),
+}
 
 
 def __getattr__(name):
-    # the token and adapter operators take torch tensors: torch is imported on their first use
-    if name in _TOKEN_OPS:
-        from . import tokens
-        globals()[name] = getattr(tokens, name)
-        return globals()[name]
+    # these operators take torch tensors: torch is imported on their first use
+    for module, names in _TORCH_OPS.items():
+        if name in names:
+            globals()[name] = getattr(importlib.import_module("." + module, __name__), name)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,443 @@
+// Norms around a block with its gate and residual scale, and rows kept in 8 bits (include/moe_experts.h).
+//
+// Both are bound by memory: a row is read once, held in registers while its sums are made, and its results
+// are written from there.
+#include <algorithm>
+
+#include "expert_kernels.hpp"
+#include "pieces8.hpp"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------------------------- rows in 8 bits
+
+constexpr int kRowsPer = 4;   // rows a thread has in flight
+
+// A thread holds 8 columns of kRowsPer rows; `lanes` threads (a power of two, whole blocks) go along a row.
+template <typename T>
+__global__ __launch_bounds__(256) void k_encode(Rows x, CodesOut c, int R, int C, int lanes) {
+    const int per = 256 / lanes, groups = (C + kBlock - 1) / kBlock * 4;
+    const int64_t row0 = (int64_t)blockIdx.x * per * kRowsPer + threadIdx.x / lanes;
+    for (int at = threadIdx.x & (lanes - 1); at < groups; at += lanes) {
+        float f[kRowsPer][8];
+#pragma unroll
+        for (int i = 0; i < kRowsPer; ++i) {
+            const int64_t row = row0 + i * per;
+            load8(static_cast<const T *>(x.p) + row * x.ld + at * 8, f[i], row < R ? C - at * 8 : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsPer; ++i) {
+            const int64_t row = row0 + i * per;
+            int scale;
+            const uint2 q = encode8(f[i], C - at * 8, scale);
+            if (row < R) {
+                store_codes(c.q + row * c.ld + at * 8, q, C - at * 8);
+                if ((at & 3) == 0) c.s[row * c.ld_s + at / 4] = (uint8_t)scale;
+            }
+        }
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_decode(Codes c, RowsOut x, int R, int C, int lanes) {
+    const int per = 256 / lanes, groups = (C + 7) / 8;
+    const int64_t row0 = (int64_t)blockIdx.x * per * kRowsPer + threadIdx.x / lanes;
+    for (int at = threadIdx.x & (lanes - 1); at < groups; at += lanes) {
+        uint2 q[kRowsPer];
+        int s[kRowsPer];
+#pragma unroll
+        for (int i = 0; i < kRowsPer; ++i) {
+            const int64_t row = row0 + i * per;
+            q[i] = load_codes(c.q + row * c.ld + at * 8, row < R ? C - at * 8 : 0);
+            s[i] = row < R ? c.s[row * c.ld_s + at / 4] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsPer; ++i) {
+            const int64_t row = row0 + i * per;
+            float f[8];
+            decode8<T>(q[i], s[i], f);
+            if (row < R) store8(static_cast<T *>(x.p) + row * x.ld + at * 8, f, C - at * 8);
+        }
+    }
+}
+
+int lanes_of(int groups) {
+    int l = 4;
+    while (l < groups && l < 256) l *= 2;
+    return l;
+}
+unsigned row_blocks(int R, int lanes) {
+    const int64_t per = (int64_t)256 / lanes * kRowsPer;
+    return (unsigned)((R + per - 1) / per);
+}
+
+// --------------------------------------------------------------------------------------------- norms
+
+__device__ inline float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+// Sums over the waves of a row; the buffer `s` has a place for each wave and is not written again before
+// the next barrier but one.
+template <int WAVES, int N>
+__device__ inline void row_sum(float (&v)[N], float *s, int wave_in_row, int first_wave) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    if constexpr (WAVES > 1) {
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[(first_wave + wave_in_row) * N + i] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) v[i] += s[(first_wave + w) * N + i];
+        }
+    }
+}
+
+__device__ inline void load_vector(const float *p, int col, int n, float (&f)[8], float other) {
+    if (p) {
+        load8(p + col, f, n);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = other;
+    }
+}
+
+// WAVES waves a row, 8 columns x V a lane.  Waves of one row are WAVES next to each other; WAVES = 1: four rows
+// a workgroup.
+template <typename T, int WAVES, int V>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_norm(NormArgs g) {
+    __shared__ float s_y[WAVES], s_o[WAVES];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, w = WAVES == 1 ? 0 : wave;
+    const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+    if (row >= g.T) return;
+    float x[V][8], y[V][8];
+    int col[V], n[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        col[v] = ((v * WAVES + w) * 64 + lane) * 8;
+        n[v] = g.H - col[v];
+        load8(static_cast<const T *>(g.x.p) + row * g.x.ld + col[v], x[v], n[v]);
+        if (g.y.p) load8(static_cast<const T *>(g.y.p) + row * g.y.ld + col[v], y[v], n[v]);
+    }
+    float r_y = 0.f, r_o = 0.f;
+    const float inv = 1.f / (float)g.H;
+    if (g.y.p) {
+        float r = 1.f;
+        if (g.w_post) {
+            float s[1] = {0.f};
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[0] += y[v][i] * y[v][i];
+            row_sum<WAVES, 1>(s, s_y, w, 0);
+            r = r_y = 1.f / sqrtf(s[0] * inv + g.eps);
+        }
+        const int64_t gate_row = row / g.per_gate;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float p[8], q[8], a[8];
+            load_vector(g.w_post, col[v], n[v], p, 1.f);
+            load_vector(g.gate ? g.gate + gate_row * g.H : nullptr, col[v], n[v], q, 1.f);
+            load_vector(g.alpha, col[v], n[v], a, 1.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[v][i] = a[i] * x[v][i] + q[i] * (p[i] * (y[v][i] * r));
+            if (g.out.p && n[v] > 0) store8(static_cast<T *>(g.out.p) + row * g.out.ld + col[v], x[v], n[v]);
+        }
+    }
+    if (g.w_pre) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[0] += n[v] > i ? x[v][i] * x[v][i] : 0.f;
+        row_sum<WAVES, 1>(s, s_o, w, 0);
+        r_o = 1.f / sqrtf(s[0] * inv + g.eps);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float p[8];
+            load_vector(g.w_pre, col[v], n[v], p, 1.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = p[i] * (x[v][i] * r_o);
+            if (n[v] > 0) store8(static_cast<T *>(g.normed.p) + row * g.normed.ld + col[v], p, n[v]);
+        }
+    }
+    if (g.stats && lane == 0 && w == 0) {
+        g.stats[2 * row] = r_y;
+        g.stats[2 * row + 1] = r_o;
+    }
+}
+
+// How the rows of a backward call are dealt: `chunks` workgroups; rows of a chunk share a row of gate
+// (rows_each of them, or what is left), or, where a gate's rows are fewer than a chunk's, a chunk has `units`
+// whole gates of `unit` rows.
+struct Deal {
+    int chunks, rows_each, per_gate_chunks, unit;   // unit 0: rows of one gate
+};
+
+constexpr int kBackWaves = 8, kMaxChunks = 512;
+
+// Waves along a row and columns (x8) of a lane for a width.
+inline int back_waves(int H) { return H <= 512 ? 1 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 8192 ? 8 : 16; }
+inline int back_groups(int H) { return std::max(1, kBackWaves / back_waves(H)); }
+
+Deal deal(int T, int H, int per_gate, bool gate) {
+    const int groups = back_groups(H), n = std::max(1, gate ? std::min(per_gate, T) : T);
+    int each = std::max(groups, (T + kMaxChunks - 1) / kMaxChunks);
+    if (!gate || n >= each) {
+        const int parts = (n + each - 1) / each, gates = (T + n - 1) / n;
+        return {parts * gates, each, parts, 0};
+    }
+    each = (each + n - 1) / n * n;   // whole gates
+    each = std::max(each, n * groups);
+    return {(T + each - 1) / each, each, 0, n};
+}
+
+template <typename T, int WAVES, int V>
+__global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) void k_norm_back(NormBackArgs g, Deal d,
+                                                                                              float *parts) {
+    constexpr int GROUPS = WAVES > kBackWaves ? 1 : kBackWaves / WAVES, ALL = GROUPS * WAVES;
+    __shared__ float sums[2][ALL * 3];
+    __shared__ float join[GROUPS > 1 ? GROUPS * WAVES * 64 * 8 * V : 1];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = wave / WAVES, w = wave % WAVES;
+    int64_t begin, end;
+    if (d.unit == 0) {
+        const int n = g.gate ? min(g.per_gate, g.T) : g.T;
+        const int64_t gate = blockIdx.x / d.per_gate_chunks;
+        begin = gate * n + (int64_t)(blockIdx.x % d.per_gate_chunks) * d.rows_each;
+        end = min(min(begin + d.rows_each, (gate + 1) * n), (int64_t)g.T);
+    } else {
+        begin = (int64_t)blockIdx.x * d.rows_each;
+        end = min(begin + d.rows_each, (int64_t)g.T);
+    }
+    const int steps = d.unit == 0 ? (d.rows_each + GROUPS - 1) / GROUPS
+                                  : (d.rows_each / d.unit + GROUPS - 1) / GROUPS * d.unit;
+    float post[V][8], pre[V][8], alpha[V][8], gate[V][8];
+    float a_post[V][8] = {}, a_pre[V][8] = {}, a_alpha[V][8] = {}, a_gate[V][8] = {};
+    int col[V], n[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        col[v] = ((v * WAVES + w) * 64 + lane) * 8;
+        n[v] = g.H - col[v];
+        load_vector(g.w_post, col[v], n[v], post[v], 1.f);
+        load_vector(g.w_pre, col[v], n[v], pre[v], 0.f);
+        load_vector(g.alpha, col[v], n[v], alpha[v], 1.f);
+        load_vector(g.gate && begin < end && d.unit == 0 ? g.gate + begin / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
+    }
+    const float inv = 1.f / (float)g.H;
+    for (int it = 0; it < steps; ++it) {
+        int64_t row;
+        bool last = false;
+        if (d.unit == 0) {
+            row = begin + (int64_t)it * GROUPS + group;
+        } else {
+            const int u = it / d.unit, i = it - u * d.unit;
+            row = begin + (int64_t)(u * GROUPS + group) * d.unit + i;
+            last = i == d.unit - 1;
+            if (i == 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    load_vector(row < end ? g.gate + row / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
+        }
+        const bool there = row < end;
+        float x[V][8], y[V][8], dd[V][8], t[V][8], o[V][8];
+        float r_y = 0.f, r_o = 0.f;
+        if (there) {
+            r_y = g.w_post ? g.stats[2 * row] : 1.f;
+            r_o = g.stats[2 * row + 1];
+        }
+        float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int m = there ? n[v] : 0;
+            load8(static_cast<const T *>(g.x.p) + row * g.x.ld + col[v], x[v], m);
+            load8(static_cast<const T *>(g.y.p) + row * g.y.ld + col[v], y[v], g.y.p ? m : 0);
+            load8(static_cast<const T *>(g.d_out.p) + row * g.d_out.ld + col[v], dd[v], g.d_out.p ? m : 0);
+            load8(static_cast<const T *>(g.d_normed.p) + row * g.d_normed.ld + col[v], t[v], g.d_normed.p ? m : 0);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (n[v] > i && there) {
+                    const float k = gate[v][i] * post[v][i];
+                    o[v][i] = alpha[v][i] * x[v][i] + (g.y.p ? gate[v][i] * (post[v][i] * (y[v][i] * r_y)) : 0.f);
+                    if (g.d_normed.p) {
+                        a_pre[v][i] += t[v][i] * (o[v][i] * r_o);
+                        t[v][i] *= pre[v][i];
+                        s[0] += t[v][i] * o[v][i];
+                        dd[v][i] += r_o * t[v][i];
+                    }
+                    const float ky = k * y[v][i];
+                    s[1] += ky * dd[v][i];
+                    s[2] += ky * o[v][i];
+                }
+            }
+        row_sum<WAVES, 3>(s, sums[it & 1], w, group * WAVES);
+        const float c1 = g.d_normed.p ? r_o * r_o * r_o * (s[0] * inv) : 0.f;
+        // mean of c y, c = k D: its parts' sums are made with S1's
+        const float c2 = g.w_post ? r_y * r_y * r_y * ((s[1] - c1 * s[2]) * inv) : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (!there || n[v] <= 0) continue;
+            float dx[8], dy[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float D = g.d_normed.p ? dd[v][i] - c1 * o[v][i] : dd[v][i];
+                const float z = y[v][i] * r_y, c = gate[v][i] * post[v][i] * D;
+                dx[i] = alpha[v][i] * D;
+                dy[i] = r_y * c - c2 * y[v][i];
+                a_alpha[v][i] += D * x[v][i];
+                a_post[v][i] += gate[v][i] * D * z;
+                a_gate[v][i] += post[v][i] * D * z;
+            }
+            if (g.d_x.p) store8(static_cast<T *>(g.d_x.p) + row * g.d_x.ld + col[v], dx, n[v]);
+            if (g.d_y.p) store8(static_cast<T *>(g.d_y.p) + row * g.d_y.ld + col[v], dy, n[v]);
+        }
+        if (last && g.d_gate) {   // this gate's rows are all this group's
+            const int64_t q = (begin + (int64_t)((it / d.unit) * GROUPS + group) * d.unit) / g.per_gate;
+            if (q * g.per_gate < end)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (n[v] > 0) store8(g.d_gate + q * g.H + col[v], a_gate[v], n[v]);
+        }
+        if (last)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a_gate[v][i] = 0.f;
+    }
+    if (!parts) return;
+    // the groups' sums, in order, then the chunk's row of each parameter's partial sums
+    auto put = [&](float(&a)[V][8], int which) {
+        if constexpr (GROUPS > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) join[(v * 8 + i) * (ALL * 64) + threadIdx.x] = a[v][i];
+            __syncthreads();
+            if (group == 0) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int k = 1; k < GROUPS; ++k) a[v][i] += join[(v * 8 + i) * (ALL * 64) + k * WAVES * 64 + threadIdx.x];
+            }
+        }
+        if (group == 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (n[v] > 0) store8(parts + ((int64_t)which * d.chunks + blockIdx.x) * g.H + col[v], a[v], n[v]);
+    };
+    if (g.d_w_post) put(a_post, 0);
+    if (g.d_alpha) put(a_alpha, 1);
+    if (g.d_w_pre) put(a_pre, 2);
+    if (g.d_gate && d.unit == 0) put(a_gate, 3);
+}
+
+// Sums of the chunks' rows, in order, 64 columns a workgroup.  y: parameter (0 .. 2), from 3 on a row of gate.
+__global__ __launch_bounds__(1024) void k_norm_join(NormBackArgs g, Deal d, const float *parts) {
+    __shared__ float s[16][64];
+    const int c = threadIdx.x & 63, k = threadIdx.x >> 6, col = blockIdx.x * 64 + c, which = blockIdx.y;
+    float *out = which == 0 ? g.d_w_post : which == 1 ? g.d_alpha : which == 2 ? g.d_w_pre : g.d_gate;
+    if (!out) return;
+    int64_t first = 0, rows = d.chunks;
+    if (which >= 3) {
+        first = (int64_t)(which - 3) * d.per_gate_chunks;
+        rows = d.per_gate_chunks;
+        out += (int64_t)(which - 3) * g.H;
+    }
+    const float *p = parts + ((int64_t)min(which, 3) * d.chunks + first) * g.H + col;
+    const int64_t per = (rows + 15) / 16, b = k * per, e = min(b + per, rows);
+    float v = 0.f;
+    if (col < g.H)
+#pragma unroll 8
+        for (int64_t i = b; i < e; ++i) v += p[i * g.H];
+    s[k][c] = v;
+    __syncthreads();
+    if (k == 0 && col < g.H) {
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += s[i][c];
+        out[col] = v;
+    }
+}
+
+template <typename T>
+hipError_t norm_launch(const NormArgs &a, hipStream_t stream) {
+    const dim3 four((unsigned)((a.T + 3) / 4)), one((unsigned)a.T);
+    if (a.H <= 512) return launch(k_norm<T, 1, 1>, four, dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 1024) return launch(k_norm<T, 1, 2>, four, dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 2048) return launch(k_norm<T, 1, 4>, four, dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 4096) return launch(k_norm<T, 4, 2>, one, dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 8192) return launch(k_norm<T, 4, 4>, one, dim3(256), stream, nullptr, nullptr, a);
+    return launch(k_norm<T, 8, 4>, one, dim3(512), stream, nullptr, nullptr, a);
+}
+
+template <typename T>
+hipError_t norm_back_launch(const NormBackArgs &a, float *parts, hipStream_t stream) {
+    const Deal d = deal(a.T, a.H, a.per_gate, a.gate != nullptr);
+    const dim3 grid((unsigned)d.chunks);
+    hipError_t e = hipSuccess;
+    if (a.T > 0) {
+        const int w = back_waves(a.H);
+        if (w == 1) e = launch(k_norm_back<T, 1, 1>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
+        else if (w == 2) e = launch(k_norm_back<T, 2, 1>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
+        else if (w == 4) e = launch(k_norm_back<T, 4, 1>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
+        else if (a.H <= 4096) e = launch(k_norm_back<T, 8, 1>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
+        else if (w == 8) e = launch(k_norm_back<T, 8, 2>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
+        else e = launch(k_norm_back<T, 16, 2>, grid, dim3(1024), stream, nullptr, nullptr, a, d, parts);
+    }
+    if (e != hipSuccess || !(a.d_w_post || a.d_alpha || a.d_w_pre || a.d_gate)) return e;
+    const bool gates = a.d_gate && d.unit == 0;
+    const int y = gates ? 3 + (a.T + std::max(1, std::min(a.per_gate, a.T)) - 1) / std::max(1, std::min(a.per_gate, a.T)) : 3;
+    return launch(k_norm_join, dim3((unsigned)((a.H + 63) / 64), (unsigned)y), dim3(1024), stream, nullptr, nullptr, a, d,
+                  static_cast<const float *>(parts));
+}
+
+}  // namespace
+
+hipError_t launch_encode(int dtype, Rows x, CodesOut c, int R, int C, hipStream_t stream) {
+    const int lanes = lanes_of((C + kBlock - 1) / kBlock * 4);
+    const dim3 grid(row_blocks(R, lanes)), block(256);
+    if (dtype == T_F32) return launch(k_encode<float>, grid, block, stream, nullptr, nullptr, x, c, R, C, lanes);
+    if (dtype == T_F16) return launch(k_encode<f16>, grid, block, stream, nullptr, nullptr, x, c, R, C, lanes);
+    return launch(k_encode<bf16>, grid, block, stream, nullptr, nullptr, x, c, R, C, lanes);
+}
+
+hipError_t launch_decode(int dtype, Codes c, RowsOut x, int R, int C, hipStream_t stream) {
+    const int lanes = lanes_of((C + 7) / 8);
+    const dim3 grid(row_blocks(R, lanes)), block(256);
+    if (dtype == T_F32) return launch(k_decode<float>, grid, block, stream, nullptr, nullptr, c, x, R, C, lanes);
+    if (dtype == T_F16) return launch(k_decode<f16>, grid, block, stream, nullptr, nullptr, c, x, R, C, lanes);
+    return launch(k_decode<bf16>, grid, block, stream, nullptr, nullptr, c, x, R, C, lanes);
+}
+
+hipError_t launch_norm(int dtype, const NormArgs &a, hipStream_t stream) {
+    if (dtype == T_F32) return norm_launch<float>(a, stream);
+    if (dtype == T_F16) return norm_launch<f16>(a, stream);
+    return norm_launch<bf16>(a, stream);
+}
+
+size_t norm_workspace(int T, int H, int per_gate) {
+    const int with = deal(T, H, per_gate, true).chunks, without = deal(T, H, per_gate, false).chunks;
+    return (size_t)std::max(with, without) * 4 * H * sizeof(float);
+}
+
+hipError_t launch_norm_back(int dtype, const NormBackArgs &a, void *workspace, hipStream_t stream) {
+    float *parts = a.d_w_post || a.d_alpha || a.d_w_pre || a.d_gate ? static_cast<float *>(workspace) : nullptr;
+    if (dtype == T_F32) return norm_back_launch<float>(a, parts, stream);
+    if (dtype == T_F16) return norm_back_launch<f16>(a, parts, stream);
+    return norm_back_launch<bf16>(a, parts, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,48 @@
+// Rows kept in 8 bits: blocks of 32 columns, int8 codes and a shared power of two.
+//
+// value = code * 2^e, e = scale - 133.  e is the least exponent for which the block's largest size, over
+// 2^e and rounded, is 127 or less, so the largest code is 64 .. 127 and a value is off by at most 2^(e-1).
+// A power of two makes the codes exact values of the 16-bit types: code * 2^e has 7 bits, so reading a row
+// back rounds nothing (a product with a scale of 24 bits would round again), and x / 2^e is exact.
+#pragma once
+
+#include <type_traits>
+
+#include "elements.hpp"
+
+namespace moe {
+
+constexpr int kScaleBias = 133, kScaleNaN = 255;
+constexpr int kMinExp = -133, kMaxExp = 121;
+
+// The scale of a block whose largest size is amax (inf or NaN: kScaleNaN).
+__device__ inline int block_scale(float amax) {
+    if (!(amax <= 3.402823466e38f)) return kScaleNaN;
+    if (amax == 0.f) return 0;
+    int e = __builtin_amdgcn_frexp_expf(amax) - 7;   // amax / 2^e in [64, 128)
+    if (__builtin_rintf(__builtin_ldexpf(amax, -e)) > 127.f) ++e;
+    return min(max(e, kMinExp), kMaxExp) + kScaleBias;
+}
+
+__device__ inline int encode1(float v, int scale) {
+    const float q = __builtin_rintf(__builtin_ldexpf(v, kScaleBias - scale));
+    return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+// values of 8 columns from their codes and their block's scale, within T's finite range
+template <typename T>
+__device__ inline void decode8(uint2 q, int scale, float (&f)[8]) {
+    if (scale == kScaleNaN) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __builtin_nanf("");
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = i < 4 ? q.x : q.y;
+        const float v = __builtin_ldexpf((float)(int8_t)(w >> (8 * (i & 3))), scale - kScaleBias);
+        f[i] = std::is_same_v<T, f16> ? fminf(fmaxf(v, -65504.f), 65504.f) : v;   // 127 * 2^121 is within the others' range
+    }
+}
+
+}  // namespace moe

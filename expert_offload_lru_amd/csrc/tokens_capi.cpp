@@ -1,60 +1,12 @@
 // C entry points of include/moe_tokens.h: argument checks, then the launches.
 #include <algorithm>
-#include <initializer_list>
 
-#include "errors.hpp"
-#include "moe_offload.h"
 #include "moe_tokens.h"
+#include "token_checks.hpp"
 #include "token_kernels.hpp"
 
 namespace moe {
 namespace {
-
-constexpr int kMaxTokenCount = 1 << 24;   // grids of one workgroup of 256 a token stay under 2^32 threads
-
-// A caller's matrix of `rows` rows of `cols` elements.
-struct Span {
-    const char *name;
-    const void *p;
-    size_t bytes;
-};
-
-size_t elem_size(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
-bool known(int dtype) { return dtype == MOE_T_F32 || dtype == MOE_T_F16 || dtype == MOE_T_BF16; }
-
-Span matrix(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, size_t size) {
-    return {name, p, p && rows > 0 ? (size_t)((rows - 1) * ld + cols) * size : 0};
-}
-Span array(const char *name, const void *p, int64_t n, size_t size = 4) { return {name, p, p ? (size_t)n * size : 0}; }
-
-bool overlap(const Span &a, const Span &b) {
-    if (a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x < y + b.bytes && y < x + a.bytes;
-}
-
-int invalid(const std::string &msg) { return set_error(MOE_ERR_INVALID, msg); }
-int unsupported(const std::string &msg) { return set_error(MOE_ERR_UNSUPPORTED, msg); }
-
-// No output overlaps an input or another output.
-int check_overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
-    for (auto o = outputs.begin(); o != outputs.end(); ++o) {
-        for (const Span &i : inputs)
-            if (overlap(*o, i)) return invalid(std::string(o->name) + " overlaps " + i.name);
-        for (auto p = o + 1; p != outputs.end(); ++p)
-            if (overlap(*o, *p)) return invalid(std::string(o->name) + " overlaps " + p->name);
-    }
-    return MOE_OK;
-}
-
-int check_ld(const char *name, const void *p, int64_t ld, int64_t cols) {
-    if (p && (ld < cols || ld > ((int64_t)1 << 40))) return invalid(std::string("ld of ") + name + " is out of range");
-    return MOE_OK;
-}
-
-int finish(hipError_t e) {
-    return e == hipSuccess ? MOE_OK : set_error(MOE_ERR_HIP, std::string("launch: ") + hipGetErrorString(e));
-}
 
 int check_tokens(int n_tokens, int top_k, int n_experts) {
     if (n_tokens < 0 || top_k < 1 || n_experts < 1) return invalid("sizes must be positive");
@@ -95,12 +47,6 @@ size_t backward_bytes(int n_rows, int inner, int outer, int n_adapters, int rank
 }  // namespace moe
 
 using namespace moe;
-
-#define MOE_TRY(call)                  \
-    do {                               \
-        const int rc_ = (call);        \
-        if (rc_ != MOE_OK) return rc_; \
-    } while (0)
 
 extern "C" {
 
