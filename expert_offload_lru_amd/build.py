@@ -23,7 +23,8 @@ ARCH = "gfx950"
 LIB = os.path.join(PKG, "libmoe_offload.so")
 PLANNER_LIB = os.path.join(PKG, "libmoe_planner.so")
 
-HIP_SOURCES = ["expert_gemv.hip", "router.hip", "prefill.hip", "tokens.hip", "adapters.hip", "experts.hip", "norms.hip"]
+HIP_SOURCES = ["expert_gemv.hip", "router.hip", "prefill.hip", "tokens.hip", "adapters.hip", "experts.hip", "experts_f32.hip",
+               "experts_f16.hip", "experts_bf16.hip", "norms.hip"]
 HOST_SOURCES = ["runtime.cpp", "decode.cpp", "uploads.cpp", "file_tier.cpp", "graph.cpp", "prefill_host.cpp",
                 "planner.cpp", "planner_capi.cpp", "errors.cpp", "tokens_capi.cpp", "experts_capi.cpp"]
 PLANNER_SOURCES = ["planner.cpp", "planner_capi.cpp", "errors.cpp"]

@@ -56,17 +56,31 @@ __device__ inline void store_codes(int8_t *p, uint2 c, int n) {
 // Codes of 8 columns of a row; the 4 lanes of a block of 32 (lanes 4j .. 4j+3) share its scale.  Columns
 // from n on count as zeros.
 __device__ inline uint2 encode8(const float (&f)[8], int n, int &scale) {
+    float v[8];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, i < n ? __float_as_uint(f[i]) & 0x7FFFFFFFu : 0u);
+    for (int i = 0; i < 8; ++i) {
+        v[i] = i < n ? f[i] : 0.f;
+        top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);   // NaN is the largest
+    }
     top = max(top, (uint32_t)__shfl_xor((int)top, 1));
     top = max(top, (uint32_t)__shfl_xor((int)top, 2));
     scale = block_scale(__uint_as_float(top));
-    uint32_t w[2] = {0, 0};
+    uint32_t b[8];
+    if ((unsigned)(scale - 6) < 248u) {   // 2^(133 - scale) is a normal number, and no code leaves the range
+        // added to 1.5 * 2^23, a value becomes a whole number, rounded to nearest, ties to even: the low byte is the code
+        const float to = __uint_as_float((uint32_t)(127 + kScaleBias - scale) << 23);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n && scale != kScaleNaN) w[i >> 2] |= (uint32_t)(uint8_t)(int8_t)encode1(f[i], scale) << (8 * (i & 3));
-    return {w[0], w[1]};
+        for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(v[i], to, 12582912.f));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = scale == kScaleNaN ? 0u : (uint32_t)encode1(v[i], scale);
+    }
+    auto four = [&](int i) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[i + 1], b[i], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[i + 3], b[i + 2], 0x0c0c0400u);
+        return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+    };
+    return {four(0), four(4)};
 }
 
 }  // namespace moe

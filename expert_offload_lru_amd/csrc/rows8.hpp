@@ -32,16 +32,21 @@ __device__ inline int encode1(float v, int scale) {
 // values of 8 columns from their codes and their block's scale, within T's finite range
 template <typename T>
 __device__ inline void decode8(uint2 q, int scale, float (&f)[8]) {
-    if (scale == kScaleNaN) {
+    // fast: 2^(scale - 133) and 128 of it are normal numbers, and 127 of it is within f16's range
+    constexpr unsigned kFast = std::is_same_v<T, f16> ? 142 - 7 : 254 - 7;
+    if ((unsigned)(scale - 7) < kFast) {
+        const float s = __uint_as_float((uint32_t)(scale - 6) << 23), less = -128.f * s;
+        const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};   // codes + 128
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __builtin_nanf("");
+        for (int i = 0; i < 8; ++i) f[i] = fmaf((float)((w[i >> 2] >> (8 * (i & 3))) & 0xFFu), s, less);
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t w = i < 4 ? q.x : q.y;
         const float v = __builtin_ldexpf((float)(int8_t)(w >> (8 * (i & 3))), scale - kScaleBias);
-        f[i] = std::is_same_v<T, f16> ? fminf(fmaxf(v, -65504.f), 65504.f) : v;   // 127 * 2^121 is within the others' range
+        // 127 * 2^121 is within the other types' range
+        f[i] = scale == kScaleNaN ? __builtin_nanf("") : std::is_same_v<T, f16> ? fminf(fmaxf(v, -65504.f), 65504.f) : v;
     }
 }
 

@@ -8,67 +8,56 @@
 
 namespace moe {
 
-constexpr int kSegPerLane = 16;   // 1024 experts over 64 lanes
-
-__device__ inline int wave_max_scan(int v) {   // inclusive
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v = max(v, o);
-    }
-    return v;
-}
-__device__ inline int wave_sum_scan(int v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
+// Inclusive scans over a wave of values from 0 on.
+template <typename Op>
+__device__ inline int wave_scan(int v, Op op) {
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));   // row_shr:1 .. 8: within 16 lanes
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));   // row_bcast:15, to rows 1 and 3
+    return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));   // row_bcast:31, to rows 2 and 3
 }
 
 struct Tile {
     int e, row, end;   // expert; the tile's first row and the expert's end
 };
 
-// Tile `index` of the experts' rows in tiles of `per` rows, experts in order; total: how many there are.
-// False if there is no such tile.  index(total) may choose the tile by the total.  Every wave does it by itself.
-// An offset counts as at least the ones before it and as 0 .. R.
-template <typename Index>
-__device__ inline bool find_tile(const int32_t *offsets, int E, int R, int per, Index index, Tile &t) {
-    const int lane = threadIdx.x & 63;
-    const int n = (E + 63) >> 6, first = lane * n;
-    int most = 0;   // of the offsets up to the end of the lane's last expert
-    int o[kSegPerLane + 1];
+// find_tile for up to 64 N experts, n a lane.
+template <int N, typename Index>
+__device__ inline bool find_tile_n(const int32_t *offsets, int E, int R, int per, int n, Index index, Tile &t) {
+    const int lane = threadIdx.x & 63, first = lane * n;
+    int o[N + 1], most = 0;   // most: of the offsets up to the end of the lane's last expert
 #pragma unroll
-    for (int i = 0; i <= kSegPerLane; ++i) {
+    for (int i = 0; i <= N; ++i) {
         o[i] = 0;
-        if (i <= n && first + i <= E) o[i] = min(max(offsets[first + i], 0), R);
+        if (i <= n && first + i <= E) o[i] = offsets[first + i];
+    }
+#pragma unroll
+    for (int i = 0; i <= N; ++i) {
+        o[i] = min(max(o[i], 0), R);
         most = max(most, o[i]);
     }
-    int before = __shfl_up(wave_max_scan(most), 1);
-    if (lane == 0) before = 0;
+    const int before = __builtin_amdgcn_update_dpp(0, wave_scan(most, [](int a, int b) { return max(a, b); }), 0x138, 0xf,
+                                                   0xf, false);   // wave_shr:1
     int run = max(before, o[0]), tiles = 0;
 #pragma unroll
-    for (int i = 0; i < kSegPerLane; ++i)
+    for (int i = 0; i < N; ++i)
         if (i < n && first + i < E) {
             const int next = max(run, o[i + 1]);
             tiles += (next - run + per - 1) / per;
             run = next;
         }
-    const int upto = wave_sum_scan(tiles), total = __builtin_amdgcn_readlane(upto, 63);
+    const int upto = wave_scan(tiles, [](int a, int b) { return a + b; }), total = __builtin_amdgcn_readlane(upto, 63);
     const int at = index(total);
     if (at < 0 || at >= total) return false;
-    const uint64_t has = __ballot(upto > at);
-    const int who = __ffsll((unsigned long long)has) - 1;
+    const int who = __ffsll((unsigned long long)__ballot(upto > at)) - 1;
     // the lane that holds it walks its experts again
     int e = 0, row = 0, end = 0, left = at - (upto - tiles);
     run = max(before, o[0]);
     bool found = false;
 #pragma unroll
-    for (int i = 0; i < kSegPerLane; ++i)
+    for (int i = 0; i < N; ++i)
         if (i < n && first + i < E && !found) {
             const int next = max(run, o[i + 1]);
             const int c = (next - run + per - 1) / per;
@@ -81,10 +70,20 @@ __device__ inline bool find_tile(const int32_t *offsets, int E, int R, int per, 
             left -= c;
             run = next;
         }
-    t.e = __builtin_amdgcn_readfirstlane(__shfl(e, who));
-    t.row = __builtin_amdgcn_readfirstlane(__shfl(row, who));
-    t.end = __builtin_amdgcn_readfirstlane(__shfl(end, who));
+    t.e = __builtin_amdgcn_readlane(e, who);
+    t.row = __builtin_amdgcn_readlane(row, who);
+    t.end = __builtin_amdgcn_readlane(end, who);
     return true;
+}
+
+// Tile `index` of the experts' rows in tiles of `per` rows (a power of two), experts in order; total: how many there
+// are.  False if there is no such tile.  index(total) may choose the tile by the total.  Every wave does it by
+// itself.  An offset counts as at least the ones before it and as 0 .. R.
+template <typename Index>
+__device__ inline bool find_tile(const int32_t *offsets, int E, int R, int per, Index index, Tile &t) {
+    const int n = (E + 63) >> 6;
+    if (n <= 2) return find_tile_n<2>(offsets, E, R, per, n, index, t);
+    return find_tile_n<16>(offsets, E, R, per, n, index, t);   // 1024 experts at most
 }
 
 // Rows of expert e: begin and end.
