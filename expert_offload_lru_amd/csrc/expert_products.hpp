@@ -376,8 +376,8 @@ __device__ inline void put_hidden(const ExpertArgs &g, int row, int col, bool th
     if (n <= 0) return;
     if (g.pre.p) {
         T *p = static_cast<T *>(g.pre.p) + row * g.pre.ld + col;
-        store8(p, gv, n);
-        store8(p + g.M, uv, n);
+        stream8(p, gv, n);
+        stream8(p + g.M, uv, n);
     }
     float h[8];
 #pragma unroll
@@ -386,7 +386,7 @@ __device__ inline void put_hidden(const ExpertArgs &g, int row, int col, bool th
         activation<T>(gv[i], g.act, h[i], slope);
         h[i] *= uv[i];
     }
-    store8(static_cast<T *>(g.out.p) + row * g.out.ld + col, h, n);
+    stream8(static_cast<T *>(g.out.p) + row * g.out.ld + col, h, n);
 }
 
 // What the activation's gradient needs of 8 columns of a row, as it lies in memory.
@@ -448,9 +448,9 @@ __device__ inline void put_hidden_back(const ExpertArgs &g, int row, int col, co
         h[i] = a * uv[i];
     }
     T *p = static_cast<T *>(g.pre.p) + row * g.pre.ld + col;
-    store8(p, dg, n);
-    store8(p + g.M, du, n);
-    if (g.out.p) store8(static_cast<T *>(g.out.p) + row * g.out.ld + col, h, n);
+    stream8(p, dg, n);
+    stream8(p + g.M, du, n);
+    if (g.out.p) stream8(static_cast<T *>(g.out.p) + row * g.out.ld + col, h, n);
 }
 
 // LDS operations of one wave are done in order; this keeps the compiler from reordering them.
@@ -572,7 +572,7 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
     } else {
         spill<C, false, 2>(stage, acc, nothing, [&](int r, int p, const float(&f)[8], const float(&)[8], Nothing) {
             const int row = row0 + r, col = col0 + 8 * p;
-            if (row < t.end && col < g.M) store8(static_cast<T *>(g.out.p) + row * g.out.ld + col, f, g.M - col);
+            if (row < t.end && col < g.M) stream8(static_cast<T *>(g.out.p) + row * g.out.ld + col, f, g.M - col);
         });
     }
 }
@@ -616,7 +616,7 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
     float *out = (splits > 1 ? parts + (int64_t)sp * g.E * g.N * g.M : g.d_w) + (int64_t)e * g.N * g.M;
     spill<C, false, 2>(stage, acc, [](int, int) { return Nothing{}; }, [&](int r, int p, const float(&f)[8], const float(&)[8], Nothing) {
         const int row = n0 + wn * C::WN + r, col = m0 + wm * C::WM + 8 * p;
-        if (row < g.N && col < g.M) store8(out + (int64_t)row * g.M + col, f, g.M - col);
+        if (row < g.N && col < g.M) stream8(out + (int64_t)row * g.M + col, f, g.M - col);
     });
 }
 

@@ -101,6 +101,14 @@ __device__ inline void row_sum(float (&v)[N], float *s, int wave_in_row, int fir
     }
 }
 
+// A row's results: past the caches (8192 rows of 2048: 32 -> 28 us); in fp32, where a lane's 32 bytes take two
+// instructions that each leave half lines, through them (40 against 42 us).
+template <typename T>
+__device__ inline void put8(T *p, const float (&f)[8], int n) {
+    if constexpr (sizeof(T) == 4) store8(p, f, n);
+    else stream8(p, f, n);
+}
+
 __device__ inline void load_vector(const float *p, int col, int n, float (&f)[8], float other) {
     if (p) {
         load8(p + col, f, n);
@@ -110,68 +118,111 @@ __device__ inline void load_vector(const float *p, int col, int n, float (&f)[8]
     }
 }
 
-// WAVES waves a row, 8 columns x V a lane.  Waves of one row are WAVES next to each other; WAVES = 1: four rows
-// a workgroup.
+// 8 columns x V of a row, as they lie in memory.
+template <typename T, int V>
+struct Raw {
+    uint4 v[V][sizeof(T) / 2];
+    __device__ void load(const Rows &m, int64_t row, const int (&col)[V], const int (&n)[V], bool there) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+                v[i][j] = load_piece(static_cast<const T *>(m.p) + row * m.ld + col[i] + j * kVec<T>,
+                                     there && m.p ? n[i] - j * kVec<T> : 0);
+    }
+    __device__ void get(int i, float (&f)[8]) const {
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T) / 2; ++j) {
+            float e[kVec<T>];
+            unpack<T>(v[i][j], e);
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) f[j * kVec<T> + k] = e[k];
+        }
+    }
+};
+
+// WAVES waves next to each other a row, 8 columns x V a lane; GROUPS rows a workgroup at a time.  A workgroup takes rows
+// gridDim.x * GROUPS apart, so that the parameters stay in registers (read for every row they were twice its bytes), and
+// requests the next row while it works on one.
 template <typename T, int WAVES, int V>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_norm(NormArgs g) {
-    __shared__ float s_y[WAVES], s_o[WAVES];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, w = WAVES == 1 ? 0 : wave;
-    const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
-    if (row >= g.T) return;
-    float x[V][8], y[V][8];
+__global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void k_norm(NormArgs g) {
+    constexpr int GROUPS = WAVES < 4 ? 4 / WAVES : 1, ALL = GROUPS * WAVES;
+    __shared__ float s_y[2][ALL], s_o[2][ALL];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = wave / WAVES, w = wave % WAVES;
     int col[V], n[V];
+    float post[V][8], pre[V][8], alpha[V][8], gate[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         col[v] = ((v * WAVES + w) * 64 + lane) * 8;
         n[v] = g.H - col[v];
-        load8(static_cast<const T *>(g.x.p) + row * g.x.ld + col[v], x[v], n[v]);
-        if (g.y.p) load8(static_cast<const T *>(g.y.p) + row * g.y.ld + col[v], y[v], n[v]);
+        load_vector(g.w_post, col[v], n[v], post[v], 1.f);
+        load_vector(g.w_pre, col[v], n[v], pre[v], 1.f);
+        load_vector(g.alpha, col[v], n[v], alpha[v], 1.f);
+        load_vector(nullptr, col[v], n[v], gate[v], 1.f);
     }
-    float r_y = 0.f, r_o = 0.f;
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+    const int steps = (int)((g.T + step - 1) / step);
+    int64_t row = (int64_t)blockIdx.x * GROUPS + group, gate_row = -1;
+    Raw<T, V> rx[2], ry[2];
+    rx[0].load(g.x, row, col, n, row < g.T);
+    ry[0].load(g.y, row, col, n, row < g.T);
     const float inv = 1.f / (float)g.H;
-    if (g.y.p) {
-        float r = 1.f;
-        if (g.w_post) {
+    auto one = [&](const Raw<T, V> &nx, const Raw<T, V> &ny, Raw<T, V> &fx, Raw<T, V> &fy, int it) {
+        const bool there = row < g.T;
+        fx.load(g.x, row + step, col, n, row + step < g.T);
+        fy.load(g.y, row + step, col, n, row + step < g.T);
+        if (g.gate && there && row / g.per_gate != gate_row) {
+            gate_row = row / g.per_gate;
+#pragma unroll
+            for (int v = 0; v < V; ++v) load_vector(g.gate + gate_row * g.H, col[v], n[v], gate[v], 1.f);
+        }
+        float x[V][8], y[V][8], r_y = 0.f, r_o = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) nx.get(v, x[v]);
+        if (g.y.p) {
+            float s[1] = {0.f}, r = 1.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                ny.get(v, y[v]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[0] += y[v][i] * y[v][i];
+            }
+            if (g.w_post) {
+                row_sum<WAVES, 1>(s, s_y[it & 1], w, group * WAVES);
+                r = r_y = 1.f / sqrtf(s[0] * inv + g.eps);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[v][i] = alpha[v][i] * x[v][i] + gate[v][i] * (post[v][i] * (y[v][i] * r));
+                if (g.out.p && there && n[v] > 0) put8(static_cast<T *>(g.out.p) + row * g.out.ld + col[v], x[v], n[v]);
+            }
+        }
+        if (g.w_pre) {
             float s[1] = {0.f};
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[0] += y[v][i] * y[v][i];
-            row_sum<WAVES, 1>(s, s_y, w, 0);
-            r = r_y = 1.f / sqrtf(s[0] * inv + g.eps);
+                for (int i = 0; i < 8; ++i) s[0] += n[v] > i ? x[v][i] * x[v][i] : 0.f;
+            row_sum<WAVES, 1>(s, s_o[it & 1], w, group * WAVES);
+            r_o = 1.f / sqrtf(s[0] * inv + g.eps);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = pre[v][i] * (x[v][i] * r_o);
+                if (there && n[v] > 0) put8(static_cast<T *>(g.normed.p) + row * g.normed.ld + col[v], p, n[v]);
+            }
         }
-        const int64_t gate_row = row / g.per_gate;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float p[8], q[8], a[8];
-            load_vector(g.w_post, col[v], n[v], p, 1.f);
-            load_vector(g.gate ? g.gate + gate_row * g.H : nullptr, col[v], n[v], q, 1.f);
-            load_vector(g.alpha, col[v], n[v], a, 1.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[v][i] = a[i] * x[v][i] + q[i] * (p[i] * (y[v][i] * r));
-            if (g.out.p && n[v] > 0) store8(static_cast<T *>(g.out.p) + row * g.out.ld + col[v], x[v], n[v]);
+        if (g.stats && lane == 0 && w == 0 && there) {
+            g.stats[2 * row] = r_y;
+            g.stats[2 * row + 1] = r_o;
         }
-    }
-    if (g.w_pre) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[0] += n[v] > i ? x[v][i] * x[v][i] : 0.f;
-        row_sum<WAVES, 1>(s, s_o, w, 0);
-        r_o = 1.f / sqrtf(s[0] * inv + g.eps);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float p[8];
-            load_vector(g.w_pre, col[v], n[v], p, 1.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = p[i] * (x[v][i] * r_o);
-            if (n[v] > 0) store8(static_cast<T *>(g.normed.p) + row * g.normed.ld + col[v], p, n[v]);
-        }
-    }
-    if (g.stats && lane == 0 && w == 0) {
-        g.stats[2 * row] = r_y;
-        g.stats[2 * row + 1] = r_o;
+        row += step;
+    };
+    for (int it = 0; it < steps; it += 2) {
+        one(rx[0], ry[0], rx[1], ry[1], it);
+        if (it + 1 < steps) one(rx[1], ry[1], rx[0], ry[0], it + 1);
     }
 }
 
@@ -182,15 +233,17 @@ struct Deal {
     int chunks, rows_each, per_gate_chunks, unit;   // unit 0: rows of one gate
 };
 
-constexpr int kBackWaves = 8, kMaxChunks = 512;
+constexpr int kBackWaves = 4;   // waves of a workgroup, at least
 
 // Waves along a row and columns (x8) of a lane for a width.
 inline int back_waves(int H) { return H <= 512 ? 1 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 8192 ? 8 : 16; }
 inline int back_groups(int H) { return std::max(1, kBackWaves / back_waves(H)); }
+// One round of workgroups: two waves a SIMD, as the registers allow (a row more ahead or three waves were slower).
+inline int back_chunks(int H) { return std::max(256, 2048 / std::max(kBackWaves, back_waves(H))); }
 
 Deal deal(int T, int H, int per_gate, bool gate) {
     const int groups = back_groups(H), n = std::max(1, gate ? std::min(per_gate, T) : T);
-    int each = std::max(groups, (T + kMaxChunks - 1) / kMaxChunks);
+    int each = std::max(groups, (T + back_chunks(H) - 1) / back_chunks(H));
     if (!gate || n >= each) {
         const int parts = (n + each - 1) / each, gates = (T + n - 1) / n;
         return {parts * gates, each, parts, 0};
@@ -204,6 +257,7 @@ template <typename T, int WAVES, int V>
 __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) void k_norm_back(NormBackArgs g, Deal d,
                                                                                               float *parts) {
     constexpr int GROUPS = WAVES > kBackWaves ? 1 : kBackWaves / WAVES, ALL = GROUPS * WAVES;
+    constexpr bool ROOM = V == 1;   // registers for a row ahead
     __shared__ float sums[2][ALL * 3];
     __shared__ float join[GROUPS > 1 ? GROUPS * WAVES * 64 * 8 * V : 1];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = wave / WAVES, w = wave % WAVES;
@@ -232,36 +286,53 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
         load_vector(g.gate && begin < end && d.unit == 0 ? g.gate + begin / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
     }
     const float inv = 1.f / (float)g.H;
-    for (int it = 0; it < steps; ++it) {
-        int64_t row;
-        bool last = false;
+    // a row of step `it`; last: of its gate
+    auto row_of = [&](int it, bool &first, bool &last) {
         if (d.unit == 0) {
-            row = begin + (int64_t)it * GROUPS + group;
-        } else {
-            const int u = it / d.unit, i = it - u * d.unit;
-            row = begin + (int64_t)(u * GROUPS + group) * d.unit + i;
-            last = i == d.unit - 1;
-            if (i == 0)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    load_vector(row < end ? g.gate + row / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
+            first = last = false;
+            return begin + (int64_t)it * GROUPS + group;
         }
+        const int u = it / d.unit, i = it - u * d.unit;
+        first = i == 0;
+        last = i == d.unit - 1;
+        return begin + (int64_t)(u * GROUPS + group) * d.unit + i;
+    };
+    struct Four {
+        Raw<T, V> x, y, d, n;
+        float r_y, r_o;
+    };
+    auto fetch = [&](Four &f, int it) {
+        bool a, b;
+        const int64_t row = row_of(it, a, b);
+        const bool there = it < steps && row < end;
+        f.x.load(g.x, row, col, n, there);
+        f.y.load(g.y, row, col, n, there);
+        f.d.load(g.d_out, row, col, n, there);
+        f.n.load(g.d_normed, row, col, n, there);
+        f.r_y = there && g.w_post ? g.stats[2 * row] : 1.f;
+        f.r_o = there && g.w_pre ? g.stats[2 * row + 1] : 0.f;
+    };
+    Four ahead;
+    fetch(ahead, 0);
+    for (int it = 0; it < steps; ++it) {
+        bool first, last;
+        const int64_t row = row_of(it, first, last);
+        if (first)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                load_vector(row < end ? g.gate + row / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
         const bool there = row < end;
         float x[V][8], y[V][8], dd[V][8], t[V][8], o[V][8];
-        float r_y = 0.f, r_o = 0.f;
-        if (there) {
-            r_y = g.w_post ? g.stats[2 * row] : 1.f;
-            r_o = g.stats[2 * row + 1];
-        }
-        float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int m = there ? n[v] : 0;
-            load8(static_cast<const T *>(g.x.p) + row * g.x.ld + col[v], x[v], m);
-            load8(static_cast<const T *>(g.y.p) + row * g.y.ld + col[v], y[v], g.y.p ? m : 0);
-            load8(static_cast<const T *>(g.d_out.p) + row * g.d_out.ld + col[v], dd[v], g.d_out.p ? m : 0);
-            load8(static_cast<const T *>(g.d_normed.p) + row * g.d_normed.ld + col[v], t[v], g.d_normed.p ? m : 0);
+            ahead.x.get(v, x[v]);
+            ahead.y.get(v, y[v]);
+            ahead.d.get(v, dd[v]);
+            ahead.n.get(v, t[v]);
         }
+        const float r_y = ahead.r_y, r_o = ahead.r_o;
+        if (ROOM) fetch(ahead, it + 1);
+        float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -298,8 +369,8 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
                 a_post[v][i] += gate[v][i] * D * z;
                 a_gate[v][i] += post[v][i] * D * z;
             }
-            if (g.d_x.p) store8(static_cast<T *>(g.d_x.p) + row * g.d_x.ld + col[v], dx, n[v]);
-            if (g.d_y.p) store8(static_cast<T *>(g.d_y.p) + row * g.d_y.ld + col[v], dy, n[v]);
+            if (g.d_x.p) put8(static_cast<T *>(g.d_x.p) + row * g.d_x.ld + col[v], dx, n[v]);
+            if (g.d_y.p) put8(static_cast<T *>(g.d_y.p) + row * g.d_y.ld + col[v], dy, n[v]);
         }
         if (last && g.d_gate) {   // this gate's rows are all this group's
             const int64_t q = (begin + (int64_t)((it / d.unit) * GROUPS + group) * d.unit) / g.per_gate;
@@ -313,6 +384,7 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) a_gate[v][i] = 0.f;
+        if (!ROOM) fetch(ahead, it + 1);
     }
     if (!parts) return;
     // the groups' sums, in order, then the chunk's row of each parameter's partial sums
@@ -374,13 +446,14 @@ __global__ __launch_bounds__(1024) void k_norm_join(NormBackArgs g, Deal d, cons
 
 template <typename T>
 hipError_t norm_launch(const NormArgs &a, hipStream_t stream) {
-    const dim3 four((unsigned)((a.T + 3) / 4)), one((unsigned)a.T);
-    if (a.H <= 512) return launch(k_norm<T, 1, 1>, four, dim3(256), stream, nullptr, nullptr, a);
-    if (a.H <= 1024) return launch(k_norm<T, 1, 2>, four, dim3(256), stream, nullptr, nullptr, a);
-    if (a.H <= 2048) return launch(k_norm<T, 1, 4>, four, dim3(256), stream, nullptr, nullptr, a);
-    if (a.H <= 4096) return launch(k_norm<T, 4, 2>, one, dim3(256), stream, nullptr, nullptr, a);
-    if (a.H <= 8192) return launch(k_norm<T, 4, 4>, one, dim3(256), stream, nullptr, nullptr, a);
-    return launch(k_norm<T, 8, 4>, one, dim3(512), stream, nullptr, nullptr, a);
+    // about as many workgroups as run at a time: more rows each keep the parameters longer
+    const auto grid = [&](int rows, int most) { return dim3((unsigned)std::min((a.T + rows - 1) / rows, most)); };
+    if (a.H <= 512) return launch(k_norm<T, 1, 1>, grid(4, 2048), dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 1024) return launch(k_norm<T, 2, 1>, grid(2, 2048), dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 2048) return launch(k_norm<T, 4, 1>, grid(1, 1024), dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 4096) return launch(k_norm<T, 8, 1>, grid(1, 1024), dim3(512), stream, nullptr, nullptr, a);
+    if (a.H <= 8192) return launch(k_norm<T, 16, 1>, grid(1, 512), dim3(1024), stream, nullptr, nullptr, a);
+    return launch(k_norm<T, 16, 2>, grid(1, 256), dim3(1024), stream, nullptr, nullptr, a);
 }
 
 template <typename T>
@@ -390,12 +463,13 @@ hipError_t norm_back_launch(const NormBackArgs &a, float *parts, hipStream_t str
     hipError_t e = hipSuccess;
     if (a.T > 0) {
         const int w = back_waves(a.H);
-        if (w == 1) e = launch(k_norm_back<T, 1, 1>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
-        else if (w == 2) e = launch(k_norm_back<T, 2, 1>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
-        else if (w == 4) e = launch(k_norm_back<T, 4, 1>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
-        else if (a.H <= 4096) e = launch(k_norm_back<T, 8, 1>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
-        else if (w == 8) e = launch(k_norm_back<T, 8, 2>, grid, dim3(512), stream, nullptr, nullptr, a, d, parts);
-        else e = launch(k_norm_back<T, 16, 2>, grid, dim3(1024), stream, nullptr, nullptr, a, d, parts);
+        const dim3 block((unsigned)(std::max(w, kBackWaves) * 64));
+        if (w == 1) e = launch(k_norm_back<T, 1, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
+        else if (w == 2) e = launch(k_norm_back<T, 2, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
+        else if (w == 4) e = launch(k_norm_back<T, 4, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
+        else if (a.H <= 4096) e = launch(k_norm_back<T, 8, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
+        else if (w == 8) e = launch(k_norm_back<T, 8, 2>, grid, block, stream, nullptr, nullptr, a, d, parts);
+        else e = launch(k_norm_back<T, 16, 2>, grid, block, stream, nullptr, nullptr, a, d, parts);
     }
     if (e != hipSuccess || !(a.d_w_post || a.d_alpha || a.d_w_pre || a.d_gate)) return e;
     const bool gates = a.d_gate && d.unit == 0;
