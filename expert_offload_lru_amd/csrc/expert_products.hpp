@@ -9,6 +9,7 @@
 #pragma once
 
 #include <algorithm>
+#include <utility>
 
 #include "expert_kernels.hpp"
 #include "expert_shapes.hpp"
@@ -26,6 +27,10 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) short4v lds_short4;
 
 enum Kind { KC, KR, KR_CODES };
+// How an operand comes from memory.  DIRECT: rows start at multiples of 16 bytes and are whole pieces, offsets fit 31
+// bits; the loads write LDS (codes: registers, by as many instructions whatever is asked for).  Otherwise through
+// registers, STAGES steps of them: PIECES, 16 bytes at any element; ELEMENTS, where a row is shorter than a piece.
+enum Way { DIRECT, PIECES, ELEMENTS };
 enum Epi { E_HIDDEN, E_PLAIN, E_HIDDEN_BACK, E_GRAD };
 
 constexpr int kRsrcWord3 = 0x00020000;    // buffer resource flags of the gfx9 family (raw, untyped)
@@ -87,14 +92,12 @@ struct Source {
 };
 
 // One operand's steps from memory to LDS: DIM lines x KE; the piece at `slot` by thread slot % THREADS.
-// DIRECT: rows start at multiples of 16 bytes and are whole pieces, offsets fit 31 bits; the loads write LDS (codes:
-// registers, by as many instructions whatever is asked for).  Otherwise through registers, STAGES steps of them.
-template <typename T, int KIND, int DIM, typename C, bool DIRECT>
+template <typename T, int KIND, int DIM, typename C, int WAY>
 struct Loader {
     static constexpr int LOADS = DIM * 4 / C::THREADS, GROUPS = DIM / 16;   // GROUPS: of 16 columns (KR)
-    static constexpr bool TO_LDS = DIRECT && KIND != KR_CODES;
+    static constexpr bool TO_LDS = WAY == DIRECT && KIND != KR_CODES;
     Source s;
-    int voff[DIRECT ? LOADS : 1], soff[KIND == KR_CODES && DIRECT ? LOADS : 1];
+    int voff[WAY == DIRECT ? LOADS : 1], soff[KIND == KR_CODES && WAY == DIRECT ? LOADS : 1];
     uint4 r[TO_LDS ? 1 : C::STAGES][TO_LDS ? 1 : LOADS];
 
     // The line (KC) or row (KR) and the piece along it that LDS holds at `slot`.  KC: a line's 4 pieces, swizzled.  KR,
@@ -112,7 +115,7 @@ struct Loader {
 
     __device__ void begin(const Source &src) {
         s = src;
-        if constexpr (DIRECT) {
+        if constexpr (WAY == DIRECT) {
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
                 const int slot = i * C::THREADS + threadIdx.x, l = line(slot), pc = piece(slot);
@@ -142,7 +145,7 @@ struct Loader {
     __device__ void load(int step, int stage) {
         if constexpr (TO_LDS) return;
         const int k0 = step * KE<T>;
-        if constexpr (DIRECT && KIND == KR_CODES) {
+        if constexpr (WAY == DIRECT && KIND == KR_CODES) {
             const __amdgpu_buffer_rsrc_t q = codes_rsrc(static_cast<const int8_t *>(s.p) + k0 * s.ld), c = codes_rsrc(s.s + k0 * s.ld_s);
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
@@ -155,28 +158,58 @@ struct Loader {
         } else {
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
-                const int slot = i * C::THREADS + threadIdx.x, l = line(slot), pc = piece(slot) * kVec<T>;
-                if constexpr (KIND == KC) {
-                    r[stage][i] = load_piece(static_cast<const T *>(s.p) + at(l) + k0 + pc, there(l) ? s.K - k0 - pc : 0);
-                } else if constexpr (KIND == KR) {
-                    r[stage][i] = load_piece(static_cast<const T *>(s.p) + (k0 + l) * s.ld + pc, k0 + l < s.K ? s.lines - pc : 0);
-                } else {
-                    const int n = k0 + l < s.K ? min(s.lines - pc, kVec<T>) : 0;
-                    const uint2 c = load_codes(static_cast<const int8_t *>(s.p) + (k0 + l) * s.ld + pc, n);
+                const int slot = i * C::THREADS + threadIdx.x, l = line(slot), pc = piece(slot) * kVec<T>, n = left(k0, l, pc);
+                const int64_t to = KIND == KC ? at(l) + k0 + pc : (k0 + l) * s.ld + pc;
+                if constexpr (WAY == PIECES) {
+                    // no branches, so that loads of several steps are on their way: a piece past the end of its row is read
+                    // as the row's last one, and shifted in store; where there is nothing, the first one of all
+                    const int64_t from = n > 0 ? to - max(kVec<T> - n, 0) : KIND == KC ? 0 : min(s.lines - kVec<T>, 0);
+                    if constexpr (KIND == KR_CODES) {
+                        uint2 q = {0, 0};
+                        __builtin_memcpy(&q, static_cast<const int8_t *>(s.p) + from, kVec<T>);
+                        r[stage][i] = {q.x, q.y, s.s[n > 0 ? (k0 + l) * s.ld_s + pc / kBlock : 0], 0u};
+                    } else {
+                        __builtin_memcpy(&r[stage][i], static_cast<const T *>(s.p) + from, 16);
+                    }
+                } else if constexpr (KIND == KR_CODES) {
+                    const uint2 c = load_codes(static_cast<const int8_t *>(s.p) + to, min(n, kVec<T>));
                     r[stage][i] = {c.x, c.y, n > 0 ? s.s[(k0 + l) * s.ld_s + pc / kBlock] : 0u, 0u};
+                } else {
+                    r[stage][i] = load_piece(static_cast<const T *>(s.p) + to, n);
                 }
             }
         }
+    }
+    // elements from a piece on that there are
+    __device__ int left(int k0, int l, int pc) const {
+        if constexpr (KIND == KC) return there(l) ? s.K - k0 - pc : 0;
+        return k0 + l < s.K ? s.lines - pc : 0;
+    }
+    // v without its lowest bits
+    __device__ static uint4 shifted(uint4 v, int bits) {
+        uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+        if (bits >= 64) lo = hi, hi = 0, bits -= 64;
+        if (bits) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
+        return {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
     }
     __device__ static __amdgpu_buffer_rsrc_t codes_rsrc(const void *p) {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)kReach, kRsrcWord3);
     }
     // and from there to LDS
-    __device__ void store(int stage, uint4 *buf) {
+    __device__ void store(int step, int stage, uint4 *buf) {
         if constexpr (TO_LDS) return;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             uint4 v = r[stage][i];
+            if constexpr (WAY == PIECES) {
+                const int slot = i * C::THREADS + threadIdx.x, n = left(step * KE<T>, line(slot), piece(slot) * kVec<T>);
+                if (n < kVec<T>) {
+                    const uint32_t scale = v.z;
+                    if (KIND == KR_CODES) v.z = 0;
+                    v = n > 0 ? shifted(v, (kVec<T> - n) * (KIND == KR_CODES ? 8 : 8 * (int)sizeof(T))) : uint4{0, 0, 0, 0};
+                    if (KIND == KR_CODES) v.z = n > 0 ? scale : 0;
+                }
+            }
             if constexpr (KIND == KR_CODES) {
                 float f[8], g[kVec<T>];
                 decode8<T>({v.x, v.y}, v.z, f);
@@ -226,15 +259,22 @@ struct Reader {
 // LDS of a workgroup: the steps' two operands.
 template <typename C>
 struct Stages {
-    uint4 (*a)[C::BM * 4], (*b)[C::BN * 4];
+    uint4 *all;
+    __device__ uint4 *a(int stage) const { return all + stage * (C::BM * 4); }
+    __device__ uint4 *b(int stage) const { return all + C::STAGES * (C::BM * 4) + stage * (C::BN * 4); }
 };
 
+template <typename F, int... I>
+__device__ inline void each(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
 // The whole reduction of a tile.  fa, fb: lines of the wave's first 32 x 32 piece; da: lines between its pieces.
-// One barrier a step: every wave has read the step's buffers, and the next step's loads, requested three steps
+// One barrier a step: every wave has read the step's buffers, and the next step's loads, requested S - 1 steps
 // before, have landed.  A piece of the reduction is read from LDS while the one before is multiplied,
 // across steps too.  Loads are spread between the products: a wave that issues them at once waits for the
 // address unit that all waves share, and its products with it.  A wave without work (`active` false) only loads.
-template <typename T, int AK, int BK, typename C, bool DIRECT, typename Da>
+template <typename T, int AK, int BK, typename C, int WAY, typename Da>
 __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da, int fb, bool active, int steps,
                               const Stages<C> &l, float16v (&acc)[C::FM][C::FN]) {
     constexpr int FM = C::FM, FN = C::FN, S = C::STAGES;
@@ -245,8 +285,8 @@ __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da,
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
     if (steps <= 0) return;
-    using LA = Loader<T, AK, C::BM, C, DIRECT>;
-    using LB = Loader<T, BK, C::BN, C, DIRECT>;
+    using LA = Loader<T, AK, C::BM, C, WAY>;
+    using LB = Loader<T, BK, C::BN, C, WAY>;
     LA la;
     LB lb;
     la.begin(sa);
@@ -258,23 +298,23 @@ __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da,
 #pragma unroll
         for (int q = 0; q < ALL; ++q)
             if (q * GROUPS / ALL == order) {
-                if (q < NA) la.direct(step, l.a[stage], q);
-                else lb.direct(step, l.b[stage], q - NA);
+                if (q < NA) la.direct(step, l.a(stage), q);
+                else lb.direct(step, l.b(stage), q - NA);
             }
     };
     constexpr int FIRST = (BEHIND * ALL + GROUPS - 1) / GROUPS;   // loads of order < BEHIND
     // loads that may still be on their way when the next step's have to be there: those of the S - 2 steps behind
     // it.  Codes are two loads each.  Loads to registers alone: the compiler waits for them.
-    constexpr int CODES = DIRECT && AK == KR_CODES ? 2 * LA::LOADS : 0;
+    constexpr int CODES = WAY == DIRECT && AK == KR_CODES ? 2 * LA::LOADS : 0;
     constexpr int LEFT = ALL ? (S - 2) * (ALL + CODES) : 63;
     const Reader<T, AK == KR_CODES ? KR : AK, C::BM> ra(fa);
     const Reader<T, BK, C::BN> rb(fb);
     uint4 x[2][FM], y[2][FN];
     auto read = [&](int stage, int kk) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) y[kk][j] = rb.get(l.b[stage], kk, j * 32);
+        for (int j = 0; j < FN; ++j) y[kk][j] = rb.get(l.b(stage), kk, j * 32);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) x[kk][i] = ra.get(l.a[stage], kk, da(i));
+        for (int i = 0; i < FM; ++i) x[kk][i] = ra.get(l.a(stage), kk, da(i));
     };
 #pragma unroll
     for (int k = 0; k < S; ++k) {
@@ -283,8 +323,8 @@ __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da,
 #pragma unroll
         for (int order = 0; order < (k + 1 < S ? GROUPS : BEHIND); ++order) issue(k, k, order);
     }
-    la.store(0, l.a[0]);
-    lb.store(0, l.b[0]);
+    la.store(0, 0, l.a(0));
+    lb.store(0, 0, l.b(0));
     wait_and_meet<ALL ? (S - 2) * ALL + FIRST : 63>();
     auto run = [&](auto works) {   // a loop for each kind of wave: branches inside would join the waits for LDS
         constexpr bool W = decltype(works)::value;
@@ -304,8 +344,8 @@ __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da,
                 products(i);
                 issue(s + S - 1, last, i + BEHIND);
             }
-            la.store(n, l.a[n]);
-            lb.store(n, l.b[n]);
+            la.store(s + 1, n, l.a(n));
+            lb.store(s + 1, n, l.b(n));
             wait_and_meet<LEFT>();
             // past the last step the loads give zeros, and what is read is not used
             if (W) read(n, 0);
@@ -317,17 +357,12 @@ __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da,
                 products(i);
             }
         };
-        static_assert(S == 4, "steps by stage");
         int s = 0;
-        for (; s + 4 <= steps; s += 4) {
-            step(std::integral_constant<int, 0>{}, s);
-            step(std::integral_constant<int, 1>{}, s + 1);
-            step(std::integral_constant<int, 2>{}, s + 2);
-            step(std::integral_constant<int, 3>{}, s + 3);
-        }
-        if (s < steps) step(std::integral_constant<int, 0>{}, s);
-        if (s + 1 < steps) step(std::integral_constant<int, 1>{}, s + 1);
-        if (s + 2 < steps) step(std::integral_constant<int, 2>{}, s + 2);
+        constexpr auto stages = std::make_integer_sequence<int, S>{};
+        for (; s + S <= steps; s += S) each([&](auto i) { step(i, s + decltype(i)::value); }, stages);
+        each([&](auto i) {
+            if (s + decltype(i)::value < steps) step(i, s + decltype(i)::value);
+        }, stages);
     };
     if (active) run(std::true_type{});
     else run(std::false_type{});
@@ -507,12 +542,11 @@ __device__ inline void spill(uint4 *stage, const float16v (&acc)[C::FM][C::FN], 
 struct Nothing {};
 
 #define MOE_TILES                                                                                                  \
-    __shared__ __align__(16) uint4 steps_a[C::STAGES][C::BM * 4], steps_b[C::STAGES][C::BN * 4];                     \
-    static_assert(C::WAVES == 2 * C::STAGES ? C::FM * 256 <= C::BM * 4 && C::BM == C::BN                              \
-                                            : C::WAVES <= C::STAGES && C::FM * 256 <= C::BM * 4, "room of a wave");  \
-    const Stages<C> l = {steps_a, steps_b};                                                                          \
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;                \
-    uint4 *const stage = wave < C::STAGES ? steps_a[wave] : steps_b[wave - C::STAGES];
+    __shared__ __align__(16) uint4 steps[C::STAGES * (C::BM + C::BN) * 4];                                           \
+    static_assert(C::WAVES * C::FM * 256 <= C::STAGES * (C::BM + C::BN) * 4, "room for the results of every wave");  \
+    const Stages<C> l = {steps};                                                                                     \
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave % C::MW, wn = wave / C::MW;         \
+    uint4 *const stage = steps + wave * (C::FM * 256);
 
 // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles next to each other, so that the rows
 // and the weights that they share are in one L2.  Tile `b` of `total`, or -1.
@@ -521,7 +555,7 @@ __device__ inline int xcd_tile(int b, int total) {
     return i < per && t < total ? t : -1;
 }
 
-template <typename T, int AK, int EPI, typename C, bool DIRECT>
+template <typename T, int AK, int EPI, typename C, int WAY>
 __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_rows(ExpertArgs g, int tiles_m) {
     MOE_TILES
     Tile t;
@@ -532,7 +566,7 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
             return x < 0 ? -1 : x / tiles_m;
         }, t))
         return;
-    constexpr int COLS = EPI == E_HIDDEN ? C::BM / 2 : C::BM, MINE = COLS / 2;   // columns of a tile, and of a wave
+    constexpr int COLS = EPI == E_HIDDEN ? C::BM / 2 : C::BM, MINE = COLS / C::MW;   // columns of a tile, and of a wave
     const int m0 = mt * COLS;
     Source sa{}, sb{};
     const T *w = static_cast<const T *>(g.w);
@@ -553,7 +587,7 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
     float16v acc[C::FM][C::FN];
     const bool active = wm * MINE < sa.lines && wn * C::WN < sb.lines;
     // hidden: the second half of a wave's pieces are up's, of the same columns
-    reduce<T, AK, KC, C, DIRECT>(
+    reduce<T, AK, KC, C, WAY>(
         sa, sb, wm * MINE, [](int i) { return EPI == E_HIDDEN ? i / (C::FM / 2) * (C::BM / 2) + i % (C::FM / 2) * 32 : i * 32; },
         wn * C::WN, active, (g.K + KE<T> - 1) / KE<T>, l, acc);
     if (!active) return;
@@ -578,7 +612,7 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
 }
 
 // d_w of one expert's tile and one of `splits` runs of its rows.
-template <typename T, int AK, typename C, bool DIRECT>
+template <typename T, int AK, typename C, int WAY>
 __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_grad(ExpertGradArgs g, int tiles_m,
                                                                                           int tiles_n, int splits, float *parts) {
     MOE_TILES
@@ -610,7 +644,7 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
     sa.K = sb.K = end - begin;
     float16v acc[C::FM][C::FN];
     const bool active = wm * C::WM < sa.lines && wn * C::WN < sb.lines;
-    reduce<T, AK, KR, C, DIRECT>(sa, sb, wm * C::WM, [](int i) { return i * 32; }, wn * C::WN, active,
+    reduce<T, AK, KR, C, WAY>(sa, sb, wm * C::WM, [](int i) { return i * 32; }, wn * C::WN, active,
                                  (end - begin + KE<T> - 1) / KE<T>, l, acc);
     if (!active) return;
     float *out = (splits > 1 ? parts + (int64_t)sp * g.E * g.N * g.M : g.d_w) + (int64_t)e * g.N * g.M;
@@ -629,11 +663,11 @@ bool direct(const void *p, int64_t ld, int64_t along, size_t size) {
     return aligned(p, ld, size) && along * (int64_t)size % 16 == 0 && 256 * ld * (int64_t)size < kReach;
 }
 
-template <typename T, int AK, int EPI, typename C, bool DIRECT>
+template <typename T, int AK, int EPI, typename C, int WAY>
 hipError_t rows_shape(const ExpertArgs &a, hipStream_t stream) {
     const int tiles_m = tiles(a.M, EPI == E_HIDDEN ? C::BM / 2 : C::BM);
     const int64_t n = ((int64_t)a.R / C::BN + std::min(a.E, a.R)) * tiles_m;
-    return launch(k_rows<T, AK, EPI, C, DIRECT>, dim3((unsigned)((n + 7) / 8 * 8)), dim3(C::THREADS), stream, nullptr, nullptr, a, tiles_m);
+    return launch(k_rows<T, AK, EPI, C, WAY>, dim3((unsigned)((n + 7) / 8 * 8)), dim3(C::THREADS), stream, nullptr, nullptr, a, tiles_m);
 }
 
 template <typename T, int AK, int EPI>
@@ -642,35 +676,41 @@ hipError_t rows_launch(const ExpertArgs &a, hipStream_t stream) {
     const int64_t ld = AK == KC ? a.K : a.M;
     bool d = direct(a.w, ld, ld, sizeof(T)) && direct(a.x.p, a.x.ld, a.K, sizeof(T));
     if (EPI == E_HIDDEN) d = d && ((int64_t)a.M + 256) * a.K * (int64_t)sizeof(T) < kReach;   // from a gate row to its up row
-    if (!d) return rows_shape<T, AK, EPI, Mid, false>(a, stream);
-    const int64_t wide = (int64_t)tiles(a.R, Wide::BN) * tiles(a.M, EPI == E_HIDDEN ? Wide::BM / 2 : Wide::BM);
-    if (wide < MID_BELOW) return rows_shape<T, AK, EPI, Mid, true>(a, stream);
-    return rows_shape<T, AK, EPI, Wide, true>(a, stream);
+    if (!d && std::min(ld, (int64_t)a.K) < kVec<T>) return rows_shape<T, AK, EPI, Small, ELEMENTS>(a, stream);
+    const auto columns = [&](int bm) { return (int64_t)tiles(a.M, EPI == E_HIDDEN ? bm / 2 : bm); };
+    const bool small = std::max(tiles(a.R, Mid::BN), std::min(a.E, a.R)) * columns(Mid::BM) < SMALL_BELOW;
+    if (!d) return small ? rows_shape<T, AK, EPI, Small, PIECES>(a, stream) : rows_shape<T, AK, EPI, Mid, PIECES>(a, stream);
+    if (small) return rows_shape<T, AK, EPI, Small, DIRECT>(a, stream);
+    if (tiles(a.R, Wide::BN) * columns(Wide::BM) < MID_BELOW) return rows_shape<T, AK, EPI, Mid, DIRECT>(a, stream);
+    return rows_shape<T, AK, EPI, Wide, DIRECT>(a, stream);
 }
 
-template <typename T, int AK, typename C, bool DIRECT>
+template <typename T, int AK, typename C, int WAY>
 hipError_t grad_shape(const ExpertGradArgs &a, int splits, float *parts, hipStream_t stream) {
     const int tiles_m = tiles(a.M, C::BM), tiles_n = tiles(a.N, C::BN);
     const int64_t n = (int64_t)tiles_m * tiles_n * a.E * splits;
-    return launch(k_grad<T, AK, C, DIRECT>, dim3((unsigned)((n + 7) / 8 * 8)), dim3(C::THREADS), stream, nullptr, nullptr, a, tiles_m,
+    return launch(k_grad<T, AK, C, WAY>, dim3((unsigned)((n + 7) / 8 * 8)), dim3(C::THREADS), stream, nullptr, nullptr, a, tiles_m,
                   tiles_n, splits, parts);
 }
 
 template <typename T>
 hipError_t grad_launch(const ExpertGradArgs &a, const GradPlan &plan, float *parts, hipStream_t stream) {
     bool d = direct(a.d_out.p, a.d_out.ld, a.N, sizeof(T));
+    const bool tiny = std::min(a.M, a.N) < kVec<T>;
     hipError_t e;
     if (a.x.p) {
         d = d && direct(a.x.p, a.x.ld, a.M, sizeof(T));
-        e = !d          ? grad_shape<T, KR, Mid, false>(a, plan.splits, parts, stream)
-            : plan.wide ? grad_shape<T, KR, Wide, true>(a, plan.splits, parts, stream)
-                        : grad_shape<T, KR, Mid, true>(a, plan.splits, parts, stream);
+        e = d && plan.wide ? grad_shape<T, KR, Wide, DIRECT>(a, plan.splits, parts, stream)
+            : d            ? grad_shape<T, KR, Mid, DIRECT>(a, plan.splits, parts, stream)
+            : tiny         ? grad_shape<T, KR, Mid, ELEMENTS>(a, plan.splits, parts, stream)
+                           : grad_shape<T, KR, Mid, PIECES>(a, plan.splits, parts, stream);
     } else {
         // pieces of 8 codes (4 beside fp32) are whole and aligned
         d = d && !(((uintptr_t)a.codes.q | (uintptr_t)a.codes.ld | (uintptr_t)a.M) & 7) && 256 * std::max(a.codes.ld, a.codes.ld_s) < kReach;
-        e = !d          ? grad_shape<T, KR_CODES, Mid, false>(a, plan.splits, parts, stream)
-            : plan.wide ? grad_shape<T, KR_CODES, Wide, true>(a, plan.splits, parts, stream)
-                        : grad_shape<T, KR_CODES, Mid, true>(a, plan.splits, parts, stream);
+        e = d && plan.wide ? grad_shape<T, KR_CODES, Wide, DIRECT>(a, plan.splits, parts, stream)
+            : d            ? grad_shape<T, KR_CODES, Mid, DIRECT>(a, plan.splits, parts, stream)
+            : tiny         ? grad_shape<T, KR_CODES, Mid, ELEMENTS>(a, plan.splits, parts, stream)
+                           : grad_shape<T, KR_CODES, Mid, PIECES>(a, plan.splits, parts, stream);
     }
     return e;
 }

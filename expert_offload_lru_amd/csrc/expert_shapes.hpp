@@ -3,18 +3,25 @@
 
 namespace moe {
 
-// A workgroup's tile: 2 waves along m and NW along n, each FM x FN pieces of 32 x 32; S steps in LDS at a time.
-template <int FM_, int FN_, int NW, int S>
+// A workgroup's tile: MW waves along m and NW along n, each FM x FN pieces of 32 x 32; S steps in LDS at a time.
+template <int FM_, int FN_, int MW_, int NW, int S>
 struct Shape {
-    static constexpr int FM = FM_, FN = FN_, STAGES = S, WM = FM * 32, WN = FN * 32;   // WM, WN: a wave's columns and rows
-    static constexpr int BM = 2 * WM, BN = NW * WN, WAVES = 2 * NW, THREADS = WAVES * 64;
+    static constexpr int FM = FM_, FN = FN_, MW = MW_, STAGES = S, WM = FM * 32, WN = FN * 32;   // WM, WN: a wave's columns, rows
+    static constexpr int BM = MW * WM, BN = NW * WN, WAVES = MW * NW, THREADS = WAVES * 64;
 };
 // 256 x 256: 8 waves, 128 KB of LDS, one workgroup a CU.
-using Wide = Shape<4, 2, 4, 4>;
+using Wide = Shape<4, 2, 2, 4, 4>;
 // 128 x 128: 4 waves, 64 KB, two workgroups a CU; for few tiles, and for loads through registers.
-using Mid = Shape<2, 2, 2, 4>;
+using Mid = Shape<2, 2, 2, 2, 4>;
+// 64 x 64: 2 waves, 64 KB; for few rows and small products, where there are not enough of the others for every CU, and
+// what counts are the loads on their way: seven steps of them.
+using Small = Shape<2, 1, 1, 2, 8>;
+
 #ifndef MID_BELOW
 #define MID_BELOW 128
+#endif
+#ifndef SMALL_BELOW
+#define SMALL_BELOW 256
 #endif
 
 inline int tiles(int n, int per) { return (n + per - 1) / per; }

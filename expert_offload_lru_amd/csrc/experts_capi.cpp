@@ -26,9 +26,9 @@ int check_experts(int dtype, int n_rows, int inner, int outer, int n_experts) {
     if (n_experts < 1) return invalid("sizes must be positive");
     MOE_TRY(check_size(n_rows, {inner, outer}));
     if (n_experts > kMaxSegments) return unsupported("n_experts > 1024");
-    const int64_t cols = (std::max(inner, outer) + 127) / 128;   // tiles of 128 columns and of 256 rows, at most
-    if ((n_rows / 256 + std::min(n_rows, n_experts)) * cols >= kMaxTiles ||
-        (int64_t)((inner + 255) / 256) * ((outer + 255) / 256) * n_experts >= kMaxTiles)
+    // tiles of 256 rows and 128 columns (hidden), and of the weights' gradients: the smaller shapes are for fewer
+    const int64_t cols = (std::max(inner, outer) + 127) / 128;
+    if ((n_rows / 256 + std::min(n_rows, n_experts)) * cols >= kMaxTiles || cols * cols * n_experts >= kMaxTiles)
         return unsupported("more rows times columns than one launch holds");
     return MOE_OK;
 }
