@@ -37,7 +37,8 @@ __global__ __launch_bounds__(256) void k_grad_join(const float *parts, float *d_
 // smaller ones); a run's partial sums are written and read once more.
 GradPlan grad_plan(int R, int M, int N, int E) {
     const int64_t wide = (int64_t)tiles(M, Wide::BM) * tiles(N, Wide::BN) * E, mid = (int64_t)tiles(M, Mid::BM) * tiles(N, Mid::BN) * E;
-    const bool use = wide * (R / E / 256 + 1) >= MID_BELOW;
+    // widths that are not whole pieces go through registers, in the smaller shape
+    const bool use = M % 8 == 0 && N % 8 == 0 && wide * (R / E / 256 + 1) >= MID_BELOW;
     const int64_t s = std::min<int64_t>({use ? 256 / wide : 512 / mid, R / (use ? 512 : 256), 16});
     return {use, (int)std::max<int64_t>(1, s)};
 }

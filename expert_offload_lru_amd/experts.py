@@ -26,8 +26,8 @@ def _maybe_matrix(name, t, rows, cols, dtype, gpu):
     return (None, cols) if t is None else _matrix(name, t, rows, cols, dtype, gpu)
 
 
-def _maybe_array(name, t, shape, gpu):
-    return None if t is None else _array(name, t, shape, _F32, gpu)
+def _vector(name, t, H, gpu):
+    return None if t is None else _array(name, t, (H,), _F32, gpu)
 
 
 def _codes(codes, scales, rows, cols, blocks, gpu):
@@ -53,7 +53,7 @@ def _experts(offsets, gpu):
 
 
 def _outputs(*tensors):
-    return tuple(t for t in tensors if t is not None)
+    return [t for t in tensors if t is not None]
 
 
 def rows_encode(x, codes, scales, stream=None):
@@ -142,7 +142,7 @@ def experts_product_backward(d_out, offsets, w, x=None, codes=None, scales=None,
     px, ldx = _maybe_matrix("x", x, R, K, d_out.dtype, gpu)
     kept = _codes(codes, scales, R, K, _blocks(K), gpu)
     pg, ldg = _maybe_matrix("d_x", d_x, R, K, d_out.dtype, gpu)
-    p_dw = _maybe_array("d_w", d_w, (E, M, K), gpu)
+    p_dw = None if d_w is None else _array("d_w", d_w, (E, M, K), _F32, gpu)
     if d_x is None and d_w is None:
         return
     need = _needed("moe_experts_product_workspace", R, K, M, E) if d_w is not None else 0
@@ -152,9 +152,7 @@ def experts_product_backward(d_out, offsets, w, x=None, codes=None, scales=None,
 
 
 def _gates(gate, rows_per_gate, R, H, gpu):
-    if gate is None:
-        return None, 1
-    if not 1 <= rows_per_gate:
+    if rows_per_gate < 1:
         _refuse("rows_per_gate must be positive")
     return _array("gate", gate, (-(-R // rows_per_gate), H), _F32, gpu), min(rows_per_gate, max(R, 1))
 
@@ -170,15 +168,16 @@ def block_norm(x, y, out, w_post=None, gate=None, rows_per_gate=1, alpha=None, w
     """
     dtype, gpu = _type("x", x)
     R, H = _dims("x", x, 2)
-    px, ldx = _matrix("x", x, R, H, x.dtype, gpu)
-    py, ldy = _maybe_matrix("y", y, R, H, x.dtype, gpu)
-    po, ldo = _maybe_matrix("out", out, R, H, x.dtype, gpu)
-    pn, ldn = _maybe_matrix("normed", normed, R, H, x.dtype, gpu)
-    pg, per = _gates(gate, rows_per_gate, R, H, gpu)
-    post, a, pre = (_maybe_array(n, t, (H,), gpu) for n, t in (("w_post", w_post), ("alpha", alpha), ("w_pre", w_pre)))
-    p_stats = _maybe_array("stats", stats, (R, 2), gpu)
-    _call(gpu_lib().moe_block_norm, _outputs(out, normed, stats), gpu, stream, px, ldx, py, ldy, dtype, R, H, post, pg, per, a,
-          pre, eps, po, ldo, pn, ldn, p_stats)
+    t = x.dtype
+    px, ldx = _matrix("x", x, R, H, t, gpu)
+    py, ldy = (None, H) if y is None else _matrix("y", y, R, H, t, gpu)
+    po, ldo = (None, H) if out is None else _matrix("out", out, R, H, t, gpu)
+    pn, ldn = (None, H) if normed is None else _matrix("normed", normed, R, H, t, gpu)
+    pg, per = (None, 1) if gate is None else _gates(gate, rows_per_gate, R, H, gpu)
+    p_stats = None if stats is None else _array("stats", stats, (R, 2), _F32, gpu)
+    _call(gpu_lib().moe_block_norm, _outputs(out, normed, stats), gpu, stream, px, ldx, py, ldy, dtype, R, H,
+          _vector("w_post", w_post, H, gpu), pg, per, _vector("alpha", alpha, H, gpu), _vector("w_pre", w_pre, H, gpu), eps,
+          po, ldo, pn, ldn, p_stats)
 
 
 def block_norm_backward(d_out, x, y, stats, d_x, d_y, d_normed=None, w_post=None, gate=None, rows_per_gate=1, alpha=None,
@@ -189,20 +188,26 @@ def block_norm_backward(d_out, x, y, stats, d_x, d_y, d_normed=None, w_post=None
     lib = gpu_lib()
     dtype, gpu = _type("x", x)
     R, H = _dims("x", x, 2)
-    rows = [_maybe_matrix(n, t, R, H, x.dtype, gpu) for n, t in (("d_out", d_out), ("d_normed", d_normed), ("x", x), ("y", y))]
-    grads = [_maybe_matrix(n, t, R, H, x.dtype, gpu) for n, t in (("d_x", d_x), ("d_y", d_y))]
-    pg, per = _gates(gate, rows_per_gate, R, H, gpu)
-    post, a, pre = (_maybe_array(n, t, (H,), gpu) for n, t in (("w_post", w_post), ("alpha", alpha), ("w_pre", w_pre)))
-    p_stats = _maybe_array("stats", stats, (R, 2), gpu)
-    params = d_w_post, d_gate, d_alpha, d_w_pre
-    d_post, d_a, d_pre = (_maybe_array(n, t, (H,), gpu) for n, t in (("d_w_post", d_w_post), ("d_alpha", d_alpha),
-                                                                     ("d_w_pre", d_w_pre)))
-    p_dgate = _maybe_array("d_gate", d_gate, gate.shape if gate is not None else (0, H), gpu)
-    outputs = _outputs(d_x, d_y, *params)
+    t = x.dtype
+    pd, ldd = (None, H) if d_out is None else _matrix("d_out", d_out, R, H, t, gpu)
+    pn, ldn = (None, H) if d_normed is None else _matrix("d_normed", d_normed, R, H, t, gpu)
+    px, ldx = _matrix("x", x, R, H, t, gpu)
+    py, ldy = (None, H) if y is None else _matrix("y", y, R, H, t, gpu)
+    pdx, lddx = (None, H) if d_x is None else _matrix("d_x", d_x, R, H, t, gpu)
+    pdy, lddy = (None, H) if d_y is None else _matrix("d_y", d_y, R, H, t, gpu)
+    pg, per = (None, 1) if gate is None else _gates(gate, rows_per_gate, R, H, gpu)
+    p_stats = None if stats is None else _array("stats", stats, (R, 2), _F32, gpu)
+    outputs = _outputs(d_x, d_y, d_w_post, d_gate, d_alpha, d_w_pre)
     if not outputs:
         return
-    need = _needed("moe_block_norm_workspace", R, H, per) if _outputs(*params) else 0
-    ws = _workspace(need, workspace, gpu, stream) if need else None
-    _call(lib.moe_block_norm_backward, outputs, gpu, stream, *rows[0], *rows[1], *rows[2], *rows[3], dtype, R, H, post, pg, per,
-          a, pre, p_stats, *grads[0], *grads[1], d_post, p_dgate, d_a, d_pre, ws.data_ptr() if need else None,
-          ws.numel() * ws.element_size() if need else 0)
+    p_dgate = None
+    if d_gate is not None:
+        p_dgate = _array("d_gate", d_gate, (0, H) if gate is None else gate.shape, _F32, gpu)
+    pw, wbytes = None, 0
+    if d_w_post is not None or d_gate is not None or d_alpha is not None or d_w_pre is not None:
+        ws = _workspace(_needed("moe_block_norm_workspace", R, H, per), workspace, gpu, stream)
+        pw, wbytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(lib.moe_block_norm_backward, outputs, gpu, stream, pd, ldd, pn, ldn, px, ldx, py, ldy, dtype, R, H,
+          _vector("w_post", w_post, H, gpu), pg, per, _vector("alpha", alpha, H, gpu), _vector("w_pre", w_pre, H, gpu), p_stats,
+          pdx, lddx, pdy, lddy, _vector("d_w_post", d_w_post, H, gpu), p_dgate, _vector("d_alpha", d_alpha, H, gpu),
+          _vector("d_w_pre", d_w_pre, H, gpu), pw, wbytes)
