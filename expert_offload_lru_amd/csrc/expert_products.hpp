@@ -52,10 +52,11 @@ __device__ inline int4v make_rsrc(const void *base) {
 }
 // 16 bytes per lane straight into LDS: lane l's bytes land at lds + 16 l (lds uniform).  In assembly, since the
 // compiler waits for all of its own loads into LDS before it reads any of LDS (it tells 8 of them apart, a tile has
-// 32), so that none could be a step ahead; wait_and_meet waits for these.  No register is written.
+// 32), so that none could be a step ahead; wait_and_meet waits for these.  No register is written.  The s_nop:
+// a vector instruction may just have written a scalar register that the load reads (5 wait states), and M0 wants one.
 __device__ inline void dma16(int4v r, uint4 *lds, int voff) {
     const int at = __builtin_amdgcn_readfirstlane((int)reinterpret_cast<uintptr_t>((lds_void *)lds));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(r)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(r)
                  : "memory", "m0");
 }
 // All but the last N of this wave's loads and stores have landed (N = 63: nothing is asked of them), and its LDS

@@ -10,7 +10,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxHidden = 16384;              // of a block norm
-constexpr int64_t kMaxTiles = 1 << 23;         // workgroups of 512 threads: a launch holds fewer than 2^32 threads
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 4096;   // a launch holds fewer than 2^32; grids are rounded up by 7 workgroups
 
 int check_size(int n_rows, std::initializer_list<int> widths) {
     if (n_rows < 0) return invalid("n_rows is negative");
@@ -26,10 +26,13 @@ int check_experts(int dtype, int n_rows, int inner, int outer, int n_experts) {
     if (n_experts < 1) return invalid("sizes must be positive");
     MOE_TRY(check_size(n_rows, {inner, outer}));
     if (n_experts > kMaxSegments) return unsupported("n_experts > 1024");
-    // tiles of 256 rows and 128 columns (hidden), and of the weights' gradients: the smaller shapes are for fewer
-    const int64_t cols = (std::max(inner, outer) + 127) / 128;
-    if ((n_rows / 256 + std::min(n_rows, n_experts)) * cols >= kMaxTiles || cols * cols * n_experts >= kMaxTiles)
-        return unsupported("more rows times columns than one launch holds");
+    // Workgroups of the smallest tiles that such widths meet: 128 rows x 64 columns by 256 threads (hidden's), or 64 x 32 by
+    // 128; the weights' gradients 128 x 128 by 256.
+    const bool tiny = std::min(inner, outer) < 8;
+    const int64_t br = tiny ? 64 : 128, bc = tiny ? 32 : 64, threads = tiny ? 128 : 256, c = std::max(inner, outer);
+    const int64_t rows = (n_rows / br + std::min(n_rows, n_experts)) * ((c + bc - 1) / bc);
+    const int64_t grads = (int64_t)((inner + 127) / 128) * ((outer + 127) / 128) * n_experts;
+    if (rows * threads >= kMaxThreads || grads * 256 >= kMaxThreads) return unsupported("more than one launch holds");
     return MOE_OK;
 }
 

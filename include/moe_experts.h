@@ -22,7 +22,8 @@
  *    shared power of two.  The scale is the least (of 0 .. 254) for which the block's largest
  *    size becomes 127 or less when rounded, so a value is off by at most 1/127 of that size; scale 255
  *    marks a block that held an infinity or NaN: its codes are 0 and all its values are read as NaN.
- *  - Limits: n_experts <= 1024; n_rows and every width below 2^24.
+ *  - Limits: n_experts <= 1024; n_rows and every width below 2^24; n_rows times a width below 2^36 (one launch's
+ *    workgroups), and so n_experts * inner * outer below 2^37.
  */
 #ifndef MOE_EXPERTS_H
 #define MOE_EXPERTS_H

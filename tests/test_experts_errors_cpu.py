@@ -142,6 +142,16 @@ def test_workspaces():
     assert lib.moe_block_norm_workspace(100, 20000, 1) == 0
 
 
+@pytest.mark.parametrize("n_rows,width,rc", [((1 << 24) - 1, 1 << 12, INV), ((1 << 24) - 1, 1 << 13, UNS), (1 << 20, 1 << 16, INV),
+                                             (1 << 20, 1 << 17, UNS), ((1 << 24) - 1, 7, INV)])
+def test_more_than_a_launch_holds(n_rows, width, rc):
+    """Refused before the tensors are looked at (they are NULL here)."""
+    none = dict(x=None, ld_x=width, dtype=2, n_rows=n_rows, inner=64, outer=width, offsets=None, n_experts=4, w=None, out=None,
+                ld_out=width, stream=None)
+    assert moe.gpu_lib().moe_experts_product(*none.values()) == rc
+    assert moe.gpu_lib().moe_experts_product(*{**none, "inner": width, "outer": 64}.values()) == rc
+
+
 def test_activation_names():
     from expert_offload_lru_amd import experts
     assert experts._activation("silu") == 0 and experts._activation("gelu") == 1

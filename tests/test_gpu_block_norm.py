@@ -210,3 +210,35 @@ def test_same_bits_again():
         moe.block_norm_backward(d, x, y, stats, d_x, d_y, d_normed=d, **p, **g)
         runs.append([d_x, d_y, *g.values()])
     assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(r, runs[0]))
+
+
+@pytest.mark.parametrize("H", [200, 9000])
+def test_without_out_or_stats(H):
+    """normed alone, stats alone, out alone: the same bits as together."""
+    R = 9
+    x, y = randn(1, R, H, dtype=torch.bfloat16), randn(2, R, H, dtype=torch.bfloat16)
+    p = params(H, R, 1, 1, 1, 1, 4)
+    out, normed, stats = forward(x, y, p)
+    a, b, c = torch.empty_like(x), torch.empty(R, 2, device="cuda"), torch.empty_like(x)
+    moe.block_norm(x, y, None, normed=a, **p)
+    moe.block_norm(x, y, None, stats=b, **{**p, "w_pre": None})
+    moe.block_norm(x, y, c, **{**p, "w_pre": None})
+    assert torch.equal(a, normed) and torch.equal(c, out) and torch.equal(b[:, 0], stats[:, 0]) and not b[:, 1].any()
+
+
+def test_rows_far_apart():
+    """Offsets past 31 bits between rows."""
+    H, ld = 72, (1 << 30) + 3
+    x, y = randn(1, 3, H, dtype=torch.float16), randn(2, 3, H, dtype=torch.float16)
+    p = params(H, 3, 1, 0, 0, 1, 1)
+    out, normed, stats = forward(x, y, p)
+    # a buffer each: column ranges of one matrix count as overlapping
+    far = [torch.empty(3 * ld, dtype=torch.float16, device="cuda").view(3, ld)[:, :H] for _ in range(4)]
+    far[0].copy_(x), far[1].copy_(y)
+    moe.block_norm(far[0], far[1], far[0], normed=far[1], **p)
+    assert torch.equal(far[0], out) and torch.equal(far[1], normed)
+    far[0].copy_(x), far[1].copy_(y), far[2].copy_(out), far[3].copy_(normed)
+    d_x, d_y = torch.empty_like(x), torch.empty_like(x)
+    moe.block_norm_backward(out, x, y, stats, d_x, d_y, d_normed=normed, **p)
+    moe.block_norm_backward(far[2], far[0], far[1], stats, far[2], far[3], d_normed=far[3], **p)
+    assert torch.equal(far[2], d_x) and torch.equal(far[3], d_y)
