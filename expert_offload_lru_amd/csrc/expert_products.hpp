@@ -389,6 +389,13 @@ __device__ inline void activation(float g, int act, float &a, float &slope) {
     slope = p + a * (1.f - p) * (silu ? 1.f : c * (1.f + 3.f * q));
 }
 
+// 8 values of a row; in fp32 through the caches, since a lane's 32 bytes take two stores that each leave half lines.
+template <typename T>
+__device__ inline void put8(T *p, const float (&f)[8], int n) {
+    if constexpr (sizeof(T) == 4) store8(p, f, n);
+    else stream8(p, f, n);
+}
+
 // 8 columns of a row of hidden, and what is kept of it.  Every lane of a block of 32 takes part.
 template <typename T>
 __device__ inline void put_hidden(const ExpertArgs &g, int row, int col, bool there, const float (&gv)[8],
@@ -412,8 +419,8 @@ __device__ inline void put_hidden(const ExpertArgs &g, int row, int col, bool th
     if (n <= 0) return;
     if (g.pre.p) {
         T *p = static_cast<T *>(g.pre.p) + row * g.pre.ld + col;
-        stream8(p, gv, n);
-        stream8(p + g.M, uv, n);
+        put8(p, gv, n);
+        put8(p + g.M, uv, n);
     }
     float h[8];
 #pragma unroll
@@ -422,7 +429,7 @@ __device__ inline void put_hidden(const ExpertArgs &g, int row, int col, bool th
         activation<T>(gv[i], g.act, h[i], slope);
         h[i] *= uv[i];
     }
-    stream8(static_cast<T *>(g.out.p) + row * g.out.ld + col, h, n);
+    put8(static_cast<T *>(g.out.p) + row * g.out.ld + col, h, n);
 }
 
 // What the activation's gradient needs of 8 columns of a row, as it lies in memory.
@@ -484,9 +491,9 @@ __device__ inline void put_hidden_back(const ExpertArgs &g, int row, int col, co
         h[i] = a * uv[i];
     }
     T *p = static_cast<T *>(g.pre.p) + row * g.pre.ld + col;
-    stream8(p, dg, n);
-    stream8(p + g.M, du, n);
-    if (g.out.p) stream8(static_cast<T *>(g.out.p) + row * g.out.ld + col, h, n);
+    put8(p, dg, n);
+    put8(p + g.M, du, n);
+    if (g.out.p) put8(static_cast<T *>(g.out.p) + row * g.out.ld + col, h, n);
 }
 
 // LDS operations of one wave are done in order; this keeps the compiler from reordering them.
@@ -499,15 +506,16 @@ __device__ inline void wave_fence() {
 // to each other, so that global stores are whole lines.  Piece p holds columns 8p .. 8p+7; with PAIR the first half of
 // the pieces come with the second half.  fetch(row, p) gives what put(row, p, f, g, fetched) needs from memory; it is
 // called BATCH pieces ahead.
-template <typename C, bool PAIR, int BATCH, typename Fetch, typename Put>
+template <typename C, bool PAIR, bool APART, int BATCH, typename Fetch, typename Put>
 __device__ inline void spill(uint4 *stage, const float16v (&acc)[C::FM][C::FN], Fetch fetch, Put put) {
     constexpr int UNITS = C::FM * 8, PP = UNITS / (PAIR ? 4 : 2), ITS = 32 * PP / 64, ALL = C::FN * ITS;
     static_assert(ITS % BATCH == 0, "batches within 32 rows");
     const int lane = threadIdx.x & 63, half = lane >> 5, r = lane & 31, p = lane % PP, row0 = lane / PP;
     decltype(fetch(0, 0)) ahead[2][BATCH];
     auto get = [&](int row, int piece, float (&f)[8]) {
-        const float4 a = __builtin_bit_cast(float4, stage[row * UNITS + ((2 * piece) ^ (row % UNITS))]);
-        const float4 b = __builtin_bit_cast(float4, stage[row * UNITS + ((2 * piece + 1) ^ (row % UNITS))]);
+        const int u = APART ? piece : 2 * piece, w = APART ? piece + UNITS / 2 : 2 * piece + 1;
+        const float4 a = __builtin_bit_cast(float4, stage[row * UNITS + (u ^ (row % UNITS))]);
+        const float4 b = __builtin_bit_cast(float4, stage[row * UNITS + (w ^ (row % UNITS))]);
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
     };
     auto row_of = [&](int it) { return it / ITS * 32 + it % ITS * (64 / PP) + row0; };
@@ -541,6 +549,19 @@ __device__ inline void spill(uint4 *stage, const float16v (&acc)[C::FM][C::FN], 
     }
 }
 struct Nothing {};
+
+// Piece p of a row of M columns, from column col0 on, as spill gives it.
+template <typename C, typename T>
+__device__ inline void put_plain(T *row, int col0, int p, int M, const float (&f)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        const int a = col0 + 4 * p, b = a + C::FM * 16;
+        stream4(row + a, f[0], f[1], f[2], f[3], M - a);
+        stream4(row + b, f[4], f[5], f[6], f[7], M - b);
+    } else {
+        const int col = col0 + 8 * p;
+        if (col < M) stream8(row + col, f, M - col);
+    }
+}
 
 #define MOE_TILES                                                                                                  \
     __shared__ __align__(16) uint4 steps[C::STAGES * (C::BM + C::BN) * 4];                                           \
@@ -595,19 +616,18 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
     const int row0 = t.row + wn * C::WN, col0 = m0 + wm * MINE;
     const auto nothing = [](int, int) { return Nothing{}; };
     if constexpr (EPI == E_HIDDEN) {
-        spill<C, true, 2>(stage, acc, nothing, [&](int r, int p, const float(&gv)[8], const float(&uv)[8], Nothing) {
+        spill<C, true, false, 2>(stage, acc, nothing, [&](int r, int p, const float(&gv)[8], const float(&uv)[8], Nothing) {
             put_hidden<T>(g, row0 + r, col0 + 8 * p, row0 + r < t.end, gv, uv);
         });
     } else if constexpr (EPI == E_HIDDEN_BACK) {
         const auto fetch = [&](int r, int p) { return get_kept<T>(g, row0 + r, col0 + 8 * p, row0 + r < t.end); };
-        spill<C, false, sizeof(T) == 4 ? 2 : 4>(stage, acc, fetch, [&](int r, int p, const float(&f)[8], const float(&)[8], const Kept<T> &k) {
+        spill<C, false, false, sizeof(T) == 4 ? 2 : 4>(stage, acc, fetch, [&](int r, int p, const float(&f)[8], const float(&)[8], const Kept<T> &k) {
             const int row = row0 + r, col = col0 + 8 * p;
             if (row < t.end && col < g.M) put_hidden_back<T>(g, row, col, f, k);
         });
     } else {
-        spill<C, false, 2>(stage, acc, nothing, [&](int r, int p, const float(&f)[8], const float(&)[8], Nothing) {
-            const int row = row0 + r, col = col0 + 8 * p;
-            if (row < t.end && col < g.M) stream8(static_cast<T *>(g.out.p) + row * g.out.ld + col, f, g.M - col);
+        spill<C, false, sizeof(T) == 4, 2>(stage, acc, nothing, [&](int r, int p, const float(&f)[8], const float(&)[8], Nothing) {
+            if (row0 + r < t.end) put_plain<C>(static_cast<T *>(g.out.p) + (row0 + r) * g.out.ld, col0, p, g.M, f);
         });
     }
 }
@@ -649,9 +669,9 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
                                  (end - begin + KE<T> - 1) / KE<T>, l, acc);
     if (!active) return;
     float *out = (splits > 1 ? parts + (int64_t)sp * g.E * g.N * g.M : g.d_w) + (int64_t)e * g.N * g.M;
-    spill<C, false, 2>(stage, acc, [](int, int) { return Nothing{}; }, [&](int r, int p, const float(&f)[8], const float(&)[8], Nothing) {
-        const int row = n0 + wn * C::WN + r, col = m0 + wm * C::WM + 8 * p;
-        if (row < g.N && col < g.M) stream8(out + (int64_t)row * g.M + col, f, g.M - col);
+    spill<C, false, true, 2>(stage, acc, [](int, int) { return Nothing{}; }, [&](int r, int p, const float(&f)[8], const float(&)[8], Nothing) {
+        const int row = n0 + wn * C::WN + r;
+        if (row < g.N) put_plain<C>(out + (int64_t)row * g.M, m0 + wm * C::WM, p, g.M, f);
     });
 }
 
@@ -678,11 +698,15 @@ hipError_t rows_launch(const ExpertArgs &a, hipStream_t stream) {
     bool d = direct(a.w, ld, ld, sizeof(T)) && direct(a.x.p, a.x.ld, a.K, sizeof(T));
     if (EPI == E_HIDDEN) d = d && ((int64_t)a.M + 256) * a.K * (int64_t)sizeof(T) < kReach;   // from a gate row to its up row
     if (!d && std::min(ld, (int64_t)a.K) < kVec<T>) return rows_shape<T, AK, EPI, Small, ELEMENTS>(a, stream);
+    // Small where the middle one has fewer tiles than there are CUs (8 rows of 8 experts, hidden 2048 to 768: 13.0 us against 16.0;
+    // 999 odd rows of 16 experts 28 / 36).  The larger one from 160 rows an expert and 192 tiles on (128 experts, 768 to 2048: 128 rows each
+    // 108 us against the middle one's 110, 192 rows 123 / 159, 512 rows 257 / 339; 16 experts, 2048 to 2048: 64 rows 35 / 24, 256 rows
+    // and 128 tiles 46 / 46, 512 rows 61 / 85; hidden of 8192 rows of one expert, 192 tiles, 54 / 65).
     const auto columns = [&](int bm) { return (int64_t)tiles(a.M, EPI == E_HIDDEN ? bm / 2 : bm); };
-    const bool small = std::max(tiles(a.R, Mid::BN), std::min(a.E, a.R)) * columns(Mid::BM) < SMALL_BELOW;
+    const bool small = std::max(tiles(a.R, Mid::BN), std::min(a.E, a.R)) * columns(Mid::BM) < 256;
     if (!d) return small ? rows_shape<T, AK, EPI, Small, PIECES>(a, stream) : rows_shape<T, AK, EPI, Mid, PIECES>(a, stream);
     if (small) return rows_shape<T, AK, EPI, Small, DIRECT>(a, stream);
-    if (tiles(a.R, Wide::BN) * columns(Wide::BM) < MID_BELOW) return rows_shape<T, AK, EPI, Mid, DIRECT>(a, stream);
+    if (a.R / a.E < 160 || tiles(a.R, Wide::BN) * columns(Wide::BM) < 192) return rows_shape<T, AK, EPI, Mid, DIRECT>(a, stream);
     return rows_shape<T, AK, EPI, Wide, DIRECT>(a, stream);
 }
 

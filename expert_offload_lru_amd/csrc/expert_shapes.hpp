@@ -17,13 +17,6 @@ using Mid = Shape<2, 2, 2, 2, 4>;
 // what counts are the loads on their way: seven steps of them.
 using Small = Shape<2, 1, 1, 2, 8>;
 
-#ifndef MID_BELOW
-#define MID_BELOW 128
-#endif
-#ifndef SMALL_BELOW
-#define SMALL_BELOW 256
-#endif
-
 inline int tiles(int n, int per) { return (n + per - 1) / per; }
 
 // A weights' gradient: its tile, and runs of an expert's rows that are summed apart.

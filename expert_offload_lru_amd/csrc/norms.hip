@@ -101,17 +101,54 @@ __device__ inline void row_sum(float (&v)[N], float *s, int wave_in_row, int fir
     }
 }
 
-// A row's results: past the caches (8192 rows of 2048: 32 -> 28 us); in fp32, where a lane's 32 bytes take two
-// instructions that each leave half lines, through them (40 against 42 us).
+// A lane's 8 columns of a row: next to each other in the 16-bit types; in fp32 4 and, 256 columns on, 4 more, so that each
+// load and store of 16 bytes a lane is whole lines (8192 rows: 3.3 TB/s otherwise).  Column of element i, behind the first:
 template <typename T>
-__device__ inline void put8(T *p, const float (&f)[8], int n) {
-    if constexpr (sizeof(T) == 4) store8(p, f, n);
-    else stream8(p, f, n);
+__device__ constexpr int column(int i) { return sizeof(T) == 4 ? (i & 3) + (i >> 2) * 256 : i; }
+// The first column of piece v of V, of wave w of W a row.
+template <typename T>
+__device__ inline int first_column(int v, int W, int w) {
+    return (v * W + w) * 512 + (threadIdx.x & 63) * (sizeof(T) == 4 ? 4 : 8);
+}
+// n: columns from the first on that there are.
+template <typename T, typename U>
+__device__ inline void load_columns(const U *p, float (&f)[8], int n) {
+    if constexpr (sizeof(T) == 4) {
+        float a[4], b[4];
+        unpack<float>(load_piece(p, n), a);
+        unpack<float>(load_piece(p + 256, n - 256), b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+    } else {
+        load8(p, f, n);
+    }
+}
+// A row's results, past the caches (8192 rows of 2048, bf16: 32 -> 28 us).
+template <typename T>
+__device__ inline void put_columns(T *p, const float (&f)[8], int n) {
+    if constexpr (sizeof(T) == 4) {
+        stream4(p, f[0], f[1], f[2], f[3], n);
+        stream4(p + 256, f[4], f[5], f[6], f[7], n - 256);
+    } else {
+        stream8(p, f, n);
+    }
+}
+// Sums in fp32, beside rows of T.
+template <typename T>
+__device__ inline void put_sums(float *p, const float (&f)[8], int n) {
+    if constexpr (sizeof(T) == 4) {
+        store_piece(p, pack<float>({f[0], f[1], f[2], f[3]}), n);
+        store_piece(p + 256, pack<float>({f[4], f[5], f[6], f[7]}), n - 256);
+    } else {
+        store8(p, f, n);
+    }
 }
 
+// A parameter's columns; `other` where it is not there.
+template <typename T>
 __device__ inline void load_vector(const float *p, int col, int n, float (&f)[8], float other) {
     if (p) {
-        load8(p + col, f, n);
+        load_columns<T>(p + col, f, n);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = other;
@@ -127,8 +164,8 @@ struct Raw {
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int j = 0; j < (int)sizeof(T) / 2; ++j)
-                v[i][j] = load_piece(static_cast<const T *>(m.p) + row * m.ld + col[i] + j * kVec<T>,
-                                     there && m.p ? n[i] - j * kVec<T> : 0);
+                v[i][j] = load_piece(static_cast<const T *>(m.p) + row * m.ld + col[i] + column<T>(j * kVec<T>),
+                                     there && m.p ? n[i] - column<T>(j * kVec<T>) : 0);
     }
     __device__ void get(int i, float (&f)[8]) const {
 #pragma unroll
@@ -153,12 +190,12 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void k_norm(NormArgs 
     float post[V][8], pre[V][8], alpha[V][8], gate[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        col[v] = ((v * WAVES + w) * 64 + lane) * 8;
+        col[v] = first_column<T>(v, WAVES, w);
         n[v] = g.H - col[v];
-        load_vector(g.w_post, col[v], n[v], post[v], 1.f);
-        load_vector(g.w_pre, col[v], n[v], pre[v], 1.f);
-        load_vector(g.alpha, col[v], n[v], alpha[v], 1.f);
-        load_vector(nullptr, col[v], n[v], gate[v], 1.f);
+        load_vector<T>(g.w_post, col[v], n[v], post[v], 1.f);
+        load_vector<T>(g.w_pre, col[v], n[v], pre[v], 1.f);
+        load_vector<T>(g.alpha, col[v], n[v], alpha[v], 1.f);
+        load_vector<T>(nullptr, col[v], n[v], gate[v], 1.f);
     }
     const int64_t step = (int64_t)gridDim.x * GROUPS;
     const int steps = (int)((g.T + step - 1) / step);
@@ -174,7 +211,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void k_norm(NormArgs 
         if (g.gate && there && row / g.per_gate != gate_row) {
             gate_row = row / g.per_gate;
 #pragma unroll
-            for (int v = 0; v < V; ++v) load_vector(g.gate + gate_row * g.H, col[v], n[v], gate[v], 1.f);
+            for (int v = 0; v < V; ++v) load_vector<T>(g.gate + gate_row * g.H, col[v], n[v], gate[v], 1.f);
         }
         float x[V][8], y[V][8], r_y = 0.f, r_o = 0.f;
 #pragma unroll
@@ -195,7 +232,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void k_norm(NormArgs 
             for (int v = 0; v < V; ++v) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[v][i] = alpha[v][i] * x[v][i] + gate[v][i] * (post[v][i] * (y[v][i] * r));
-                if (g.out.p && there && n[v] > 0) put8(static_cast<T *>(g.out.p) + row * g.out.ld + col[v], x[v], n[v]);
+                if (g.out.p && there && n[v] > 0) put_columns(static_cast<T *>(g.out.p) + row * g.out.ld + col[v], x[v], n[v]);
             }
         }
         if (g.w_pre) {
@@ -203,7 +240,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void k_norm(NormArgs 
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[0] += n[v] > i ? x[v][i] * x[v][i] : 0.f;
+                for (int i = 0; i < 8; ++i) s[0] += n[v] > column<T>(i) ? x[v][i] * x[v][i] : 0.f;
             row_sum<WAVES, 1>(s, s_o[it & 1], w, group * WAVES);
             r_o = 1.f / sqrtf(s[0] * inv + g.eps);
 #pragma unroll
@@ -211,7 +248,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void k_norm(NormArgs 
                 float p[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) p[i] = pre[v][i] * (x[v][i] * r_o);
-                if (there && n[v] > 0) put8(static_cast<T *>(g.normed.p) + row * g.normed.ld + col[v], p, n[v]);
+                if (there && n[v] > 0) put_columns(static_cast<T *>(g.normed.p) + row * g.normed.ld + col[v], p, n[v]);
             }
         }
         if (g.stats && lane == 0 && w == 0 && there) {
@@ -236,9 +273,10 @@ struct Deal {
 constexpr int kBackWaves = 4;   // waves of a workgroup, at least
 
 // Waves along a row and columns (x8) of a lane for a width.
-inline int back_waves(int H) { return H <= 512 ? 1 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 8192 ? 8 : 16; }
+inline int back_waves(int H) { return H <= 512 ? 1 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 6 * 512 ? 6 : H <= 8192 ? 8 : 16; }
 inline int back_groups(int H) { return std::max(1, kBackWaves / back_waves(H)); }
-// One round of workgroups: two waves a SIMD, as the registers allow (a row more ahead or three waves were slower).
+// One round of workgroups: two waves a SIMD, as the registers allow (16384 rows of 2048: 97 us; two rows
+// ahead 105, three waves 130).
 inline int back_chunks(int H) { return std::max(256, 2048 / std::max(kBackWaves, back_waves(H))); }
 
 Deal deal(int T, int H, int per_gate, bool gate) {
@@ -278,12 +316,12 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
     int col[V], n[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        col[v] = ((v * WAVES + w) * 64 + lane) * 8;
+        col[v] = first_column<T>(v, WAVES, w);
         n[v] = g.H - col[v];
-        load_vector(g.w_post, col[v], n[v], post[v], 1.f);
-        load_vector(g.w_pre, col[v], n[v], pre[v], 0.f);
-        load_vector(g.alpha, col[v], n[v], alpha[v], 1.f);
-        load_vector(g.gate && begin < end && d.unit == 0 ? g.gate + begin / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
+        load_vector<T>(g.w_post, col[v], n[v], post[v], 1.f);
+        load_vector<T>(g.w_pre, col[v], n[v], pre[v], 0.f);
+        load_vector<T>(g.alpha, col[v], n[v], alpha[v], 1.f);
+        load_vector<T>(g.gate && begin < end && d.unit == 0 ? g.gate + begin / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
     }
     const float inv = 1.f / (float)g.H;
     // a row of step `it`; last: of its gate
@@ -312,32 +350,30 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
         f.r_y = there && g.w_post ? g.stats[2 * row] : 1.f;
         f.r_o = there && g.w_pre ? g.stats[2 * row + 1] : 0.f;
     };
-    Four ahead;
-    fetch(ahead, 0);
-    for (int it = 0; it < steps; ++it) {
+    auto one = [&](Four &at, int it) {
         bool first, last;
         const int64_t row = row_of(it, first, last);
         if (first)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                load_vector(row < end ? g.gate + row / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
+                load_vector<T>(row < end ? g.gate + row / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
         const bool there = row < end;
         float x[V][8], y[V][8], dd[V][8], t[V][8], o[V][8];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            ahead.x.get(v, x[v]);
-            ahead.y.get(v, y[v]);
-            ahead.d.get(v, dd[v]);
-            ahead.n.get(v, t[v]);
+            at.x.get(v, x[v]);
+            at.y.get(v, y[v]);
+            at.d.get(v, dd[v]);
+            at.n.get(v, t[v]);
         }
-        const float r_y = ahead.r_y, r_o = ahead.r_o;
-        if (ROOM) fetch(ahead, it + 1);
+        const float r_y = at.r_y, r_o = at.r_o;
+        if (ROOM) fetch(at, it + 1);
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (n[v] > i && there) {
+                if (n[v] > column<T>(i) && there) {
                     const float k = gate[v][i] * post[v][i];
                     o[v][i] = alpha[v][i] * x[v][i] + (g.y.p ? gate[v][i] * (post[v][i] * (y[v][i] * r_y)) : 0.f);
                     if (g.d_normed.p) {
@@ -369,22 +405,27 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
                 a_post[v][i] += gate[v][i] * D * z;
                 a_gate[v][i] += post[v][i] * D * z;
             }
-            if (g.d_x.p) put8(static_cast<T *>(g.d_x.p) + row * g.d_x.ld + col[v], dx, n[v]);
-            if (g.d_y.p) put8(static_cast<T *>(g.d_y.p) + row * g.d_y.ld + col[v], dy, n[v]);
+            if (g.d_x.p) put_columns(static_cast<T *>(g.d_x.p) + row * g.d_x.ld + col[v], dx, n[v]);
+            if (g.d_y.p) put_columns(static_cast<T *>(g.d_y.p) + row * g.d_y.ld + col[v], dy, n[v]);
         }
         if (last && g.d_gate) {   // this gate's rows are all this group's
             const int64_t q = (begin + (int64_t)((it / d.unit) * GROUPS + group) * d.unit) / g.per_gate;
             if (q * g.per_gate < end)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    if (n[v] > 0) store8(g.d_gate + q * g.H + col[v], a_gate[v], n[v]);
+                    if (n[v] > 0) put_sums<T>(g.d_gate + q * g.H + col[v], a_gate[v], n[v]);
         }
         if (last)
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) a_gate[v][i] = 0.f;
-        if (!ROOM) fetch(ahead, it + 1);
+    };
+    Four row;
+    fetch(row, 0);
+    for (int it = 0; it < steps; ++it) {
+        one(row, it);
+        if (!ROOM) fetch(row, it + 1);
     }
     if (!parts) return;
     // the groups' sums, in order, then the chunk's row of each parameter's partial sums
@@ -408,7 +449,7 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
         if (group == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (n[v] > 0) store8(parts + ((int64_t)which * d.chunks + blockIdx.x) * g.H + col[v], a[v], n[v]);
+                if (n[v] > 0) put_sums<T>(parts + ((int64_t)which * d.chunks + blockIdx.x) * g.H + col[v], a[v], n[v]);
     };
     if (g.d_w_post) put(a_post, 0);
     if (g.d_alpha) put(a_alpha, 1);
@@ -451,6 +492,7 @@ hipError_t norm_launch(const NormArgs &a, hipStream_t stream) {
     if (a.H <= 512) return launch(k_norm<T, 1, 1>, grid(4, 2048), dim3(256), stream, nullptr, nullptr, a);
     if (a.H <= 1024) return launch(k_norm<T, 2, 1>, grid(2, 2048), dim3(256), stream, nullptr, nullptr, a);
     if (a.H <= 2048) return launch(k_norm<T, 4, 1>, grid(1, 1024), dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 6 * 512) return launch(k_norm<T, 6, 1>, grid(1, 1024), dim3(384), stream, nullptr, nullptr, a);
     if (a.H <= 4096) return launch(k_norm<T, 8, 1>, grid(1, 1024), dim3(512), stream, nullptr, nullptr, a);
     if (a.H <= 8192) return launch(k_norm<T, 16, 1>, grid(1, 512), dim3(1024), stream, nullptr, nullptr, a);
     return launch(k_norm<T, 16, 2>, grid(1, 256), dim3(1024), stream, nullptr, nullptr, a);
@@ -463,10 +505,11 @@ hipError_t norm_back_launch(const NormBackArgs &a, float *parts, hipStream_t str
     hipError_t e = hipSuccess;
     if (a.T > 0) {
         const int w = back_waves(a.H);
-        const dim3 block((unsigned)(std::max(w, kBackWaves) * 64));
+        const dim3 block((unsigned)(back_groups(a.H) * w * 64));
         if (w == 1) e = launch(k_norm_back<T, 1, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else if (w == 2) e = launch(k_norm_back<T, 2, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else if (w == 4) e = launch(k_norm_back<T, 4, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
+        else if (w == 6) e = launch(k_norm_back<T, 6, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else if (a.H <= 4096) e = launch(k_norm_back<T, 8, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else if (w == 8) e = launch(k_norm_back<T, 8, 2>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else e = launch(k_norm_back<T, 16, 2>, grid, block, stream, nullptr, nullptr, a, d, parts);

@@ -7,20 +7,22 @@
 
 namespace moe {
 
-// 8 values at p, the first n of them, past the caches where they are whole: what a product writes is as large as
-// what it reads, and would push that out of L2 (gradients of 65536 rows 745 -> 700 us, with fp32 d_w 1540 -> 1330).
+// Values at p, the first n of them, past the caches where they are whole: what a product writes is as large as what it
+// reads, and would push that out of L2 (gradients of 65536 rows 745 -> 700 us).
+template <typename T>
+__device__ inline void stream_piece(T *p, uint4 v, int n) {
+    typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
+    if (n >= kVec<T>) __builtin_nontemporal_store(words{v.x, v.y, v.z, v.w}, reinterpret_cast<words *>(p));
+    else store_piece(p, v, n);
+}
+__device__ inline void stream4(float *p, float a, float b, float c, float d, int n) { stream_piece(p, pack<float>({a, b, c, d}), n); }
 template <typename T>
 __device__ inline void stream8(T *p, const float (&f)[8], int n) {
-    typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
-    auto put = [](T *q, uint4 v, int m) {
-        if (m >= kVec<T>) __builtin_nontemporal_store(words{v.x, v.y, v.z, v.w}, reinterpret_cast<words *>(q));
-        else store_piece(q, v, m);
-    };
     if constexpr (sizeof(T) == 4) {
-        put(p, pack<T>({f[0], f[1], f[2], f[3]}), min(n, 4));
-        put(p + 4, pack<T>({f[4], f[5], f[6], f[7]}), min(n - 4, 4));
+        stream4(p, f[0], f[1], f[2], f[3], n);
+        stream4(p + 4, f[4], f[5], f[6], f[7], n - 4);
     } else {
-        put(p, pack<T>(f), n);
+        stream_piece(p, pack<T>(f), n);
     }
 }
 

@@ -10,8 +10,8 @@ from token_harness import DTYPES, assert_near, f64, randn
 
 pytestmark = pytest.mark.gpu
 
-# 128 tiles of 256 x 256 and more, with reductions of 1 to 9 steps; 127 of them; odd widths in tiles of 128 x 128
-LARGE = [(4096, 96, 2048, 5), (8200, 32, 1024, 3), (3900, 288, 2304, 1), (3840, 40, 2032, 2), (4100, 71, 1001, 6), (1000, 9, 4001, 2)]
+# 192 tiles of 256 x 256 and more, and fewer, with reductions of 1 to 9 steps; odd widths in tiles of 128 x 128
+LARGE = [(6200, 96, 2048, 5), (16500, 40, 776, 3), (4096, 96, 2048, 5), (8200, 32, 1024, 3), (3900, 288, 2304, 1), (3840, 40, 2032, 2), (4100, 71, 1001, 6), (1000, 9, 4001, 2)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -33,7 +33,7 @@ def test_products(R, K, M, E, dtype):
 
 @pytest.mark.parametrize("keep", ["none", "type", "8 bits"])
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("R,K,I,E", [(4096, 64, 1024, 5), (7900, 104, 520, 2), (4100, 71, 501, 6)])
+@pytest.mark.parametrize("R,K,I,E", [(6200, 64, 1024, 5), (12600, 104, 520, 2), (4096, 64, 1024, 5), (7900, 104, 520, 2), (4100, 71, 501, 6)])
 def test_hidden(R, K, I, E, dtype, keep):
     t, nb = DTYPES[dtype], -(-I // 32)
     x, w, off = randn(1, R, K, dtype=t), randn(2, E, 2 * I, K, dtype=t, std=K ** -0.5), offsets_of(3, R, E, 1, 2)
@@ -59,7 +59,7 @@ def test_hidden(R, K, I, E, dtype, keep):
 
 @pytest.mark.parametrize("keep", ["type", "8 bits"])
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("R,H,I,E", [(4096, 64, 2048, 5), (7900, 104, 1032, 2), (4100, 71, 1001, 3)])
+@pytest.mark.parametrize("R,H,I,E", [(6200, 64, 2048, 5), (12600, 104, 1032, 2), (4096, 64, 2048, 5), (7900, 104, 1032, 2), (4100, 71, 1001, 3)])
 def test_hidden_backward(R, H, I, E, dtype, keep):
     t, nb = DTYPES[dtype], -(-I // 32)
     d_out, w, off = randn(1, R, H, dtype=t), randn(2, E, H, I, dtype=t, std=H ** -0.5), offsets_of(3, R, E, 1, 2)
@@ -89,7 +89,7 @@ def magnitude_t(d_out, off, w):
 
 @pytest.mark.parametrize("codes", [False, True])
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("R,M,N,E", [(5000, 1024, 768, 3), (600, 1024, 2048, 4), (9000, 96, 160, 1), (2100, 203, 301, 2)])
+@pytest.mark.parametrize("R,M,N,E", [(17000, 520, 776, 130), (5000, 1024, 768, 3), (600, 1024, 2048, 4), (9000, 96, 160, 1), (2100, 203, 301, 2)])
 def test_weight_gradients(R, M, N, E, dtype, codes):
     """Whole experts and runs of rows; values that add without a rounding, so that every row counts exactly."""
     t = DTYPES[dtype]
