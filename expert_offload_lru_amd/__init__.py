@@ -1,7 +1,7 @@
 """MI355X offloaded mixture-of-experts layer with an LRU expert cache.
 
-Thin ctypes binding over the C ABI of ``include/moe_offload.h`` and
-``include/moe_tokens.h`` (GPU library ``libmoe_offload.so``) and
+Thin ctypes binding over the C ABI of ``include/moe_offload.h``,
+``include/moe_tokens.h`` and ``include/moe_experts.h`` (GPU library ``libmoe_offload.so``) and
 ``include/moe_planner.h`` (host slot table, also built alone as
 ``libmoe_planner.so`` without HIP).  The binding only
 marshals arguments: every step of the layer runs in the native library.
@@ -32,7 +32,7 @@ POOL_SHARED, SHARED_EXPERT, PREFETCH, WAVES_UNION, POLICY_LFU, ADAPTIVE_CAPACITY
 # forward flags
 FWD_RESIDUAL = 0x1
 DECODE_MAX_TOKENS = 32
-# element types of the token and adapter operators
+# element types of the token, adapter and expert operators
 T_F32, T_F16, T_BF16 = 0, 1, 2
 # timing mask
 TIME_ROUTER, TIME_GATE_UP, TIME_DOWN, TIME_COMBINE, TIME_PREFILL, TIME_FUSED = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
