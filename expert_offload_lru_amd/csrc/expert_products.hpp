@@ -196,6 +196,15 @@ struct Loader {
     __device__ static __amdgpu_buffer_rsrc_t codes_rsrc(const void *p) {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)kReach, kRsrcWord3);
     }
+    // Takes every register as read, so that no load is left out where a tile ends: the waits count them.
+    __device__ void use() const {
+        if constexpr (WAY == DIRECT && KIND == KR_CODES) {
+#pragma unroll
+            for (int k = 0; k < C::STAGES; ++k)
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i) asm volatile("" ::"v"(r[k][i].x), "v"(r[k][i].y), "v"(r[k][i].z));
+        }
+    }
     // and from there to LDS
     __device__ void store(int step, int stage, uint4 *buf) {
         if constexpr (TO_LDS) return;
@@ -304,8 +313,9 @@ __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da,
             }
     };
     constexpr int FIRST = (BEHIND * ALL + GROUPS - 1) / GROUPS;   // loads of order < BEHIND
-    // loads that may still be on their way when the next step's have to be there: those of the S - 2 steps behind
-    // it.  Codes are two loads each.  Loads to registers alone: the compiler waits for them.
+    // Loads that may still be on their way when the next step's have to be there: those of the S - 2 steps behind
+    // it.  Codes are two loads each, in every step, past the last one too (Loader::use).  Loads to registers alone: the
+    // compiler waits for them.
     constexpr int CODES = WAY == DIRECT && AK == KR_CODES ? 2 * LA::LOADS : 0;
     constexpr int LEFT = ALL ? (S - 2) * (ALL + CODES) : 63;
     const Reader<T, AK == KR_CODES ? KR : AK, C::BM> ra(fa);
@@ -367,6 +377,7 @@ __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da,
     };
     if (active) run(std::true_type{});
     else run(std::false_type{});
+    la.use();
     wait_and_meet<0>();   // the LDS is free for the results
 }
 
@@ -382,11 +393,11 @@ __device__ inline float sigmoid(float g) {
 // (1 + tanh(z/2)) / 2 = sigmoid(z) (gelu).
 template <typename T>
 __device__ inline void activation(float g, int act, float &a, float &slope) {
-    const float c = 1.5957691216057308f, q = 0.044715f * g * g;
+    const float c = 1.5957691216057308f, q = fminf(0.044715f * g * g, 1e10f);
     const bool silu = act == MOE_ACT_SILU;
     const float p = sigmoid<T>(silu ? g : c * (g + q * g));
     a = g * p;
-    slope = p + a * (1.f - p) * (silu ? 1.f : c * (1.f + 3.f * q));
+    slope = p + a * (1.f - p) * (silu ? 1.f : c * (1.f + 3.f * q));   // p is 0 or 1 long before q is cut
 }
 
 // 8 values of a row; in fp32 through the caches, since a lane's 32 bytes take two stores that each leave half lines.

@@ -339,7 +339,7 @@ def test_activations_at_large_arguments():
         d_pre = torch.empty(1, 2 * I, device="cuda")
         moe.experts_hidden_backward(torch.ones(1, I, device="cuda"), off, torch.eye(I, device="cuda").reshape(1, I, I), d_pre,
                                     activation=act, pre=x)
-        assert torch.equal(d_pre[0, 4:7], torch.ones(3, device="cuda")) and (d_pre[0, 1:3].abs() < 1e-30).all()
+        assert torch.equal(d_pre[0, 4:8], torch.ones(4, device="cuda")) and (d_pre[0, :3].abs() < 1e-30).all()
 
 
 def test_empty_calls():
