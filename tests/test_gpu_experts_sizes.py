@@ -160,3 +160,46 @@ def test_many_experts():
     mx, mw = o.product_backward(np.abs(f64(d)), np.abs(f64(x)), off.tolist(), np.abs(f64(w)), np.zeros((R, K)))
     assert_near(d_x, rx, t, (M + 1) * ULP * mx)
     assert_near(d_w, rw, torch.float32, 8 * ULP * mw)
+
+
+def whole(seed, *shape, dtype, most=8):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,M,E", [(40, 64, 1), (700, 2432, 2), (6200, 2048, 5)])
+def test_every_number_of_steps(R, M, E, dtype):
+    """Reductions of 1 to 20 steps and their remainders by the steps held at a time, in each tile; sums of whole numbers are exact,
+    so a load that came late or a step too many shows in any bit."""
+    t = DTYPES[dtype]
+    off = offsets_of(3, R, E, 1, 2)
+    piece = 16 // torch.empty((), dtype=t).element_size()
+    lengths = [n * 4 * piece - cut for n in range(1, 20 if R < 1000 else 10) for cut in (0, piece)]
+    for K in lengths:
+        x, w = whole(K, R, K, dtype=t), whole(K + 1, E, M, K, dtype=t)
+        v = w.transpose(1, 2).contiguous()
+        out, d_x = sevens(R, M, t), sevens(R, M, t)
+        moe.experts_product(x, off, w, out)
+        moe.experts_product_backward(x, off, v, d_x=d_x)
+        want = torch.full((R, M), 7.0, dtype=t, device="cuda")
+        for e, a, b in o.segments(off.tolist(), R):
+            want[a:b] = (x[a:b].float() @ v[e].float()).to(t)   # exact in fp32
+        assert torch.equal(out, want) and torch.equal(d_x, want), K
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,E", [(64, 72, 1), (1024, 768, 3)])
+def test_weight_gradients_of_every_number_of_steps(M, N, E, dtype):
+    t = DTYPES[dtype]
+    for rows in [*range(1, 7), *range(15, 330, 21), *((1100, 1130, 1160, 1190) if E > 1 else ())]:
+        R = E * rows
+        off = torch.arange(0, R + 1, rows, dtype=torch.int32).cuda()
+        x, d, w = whole(rows, R, M, dtype=t), whole(rows + 1, R, N, dtype=t), torch.empty(E, N, M, dtype=t, device="cuda")
+        q, s = torch.empty(R, M, dtype=torch.int8, device="cuda"), torch.empty(R, M // 32, dtype=torch.uint8, device="cuda")
+        moe.rows_encode(x, q, s)
+        a, b = torch.empty(E, N, M, device="cuda"), torch.empty(E, N, M, device="cuda")
+        moe.experts_product_backward(d, off, w, x=x, d_w=a)
+        moe.experts_product_backward(d, off, w, codes=q, scales=s, d_w=b)
+        want = torch.stack([d[i * rows:(i + 1) * rows].double().T.contiguous() @ x[i * rows:(i + 1) * rows].double() for i in range(E)])
+        assert torch.equal(a.double(), want) and torch.equal(b, a), rows
