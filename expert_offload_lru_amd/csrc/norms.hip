@@ -358,11 +358,14 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
             for (int v = 0; v < V; ++v)
                 load_vector<T>(row < end ? g.gate + row / g.per_gate * g.H : nullptr, col[v], n[v], gate[v], 1.f);
         const bool there = row < end;
-        float x[V][8], y[V][8], dd[V][8], t[V][8], o[V][8];
+        // Sums are of y r_y and out r_out, numbers of size 1, so that no row's size leaves fp32's range in them:
+        //   D = d_out + r_out (t - o mean(t o)), o = out r_out;   d_y = r_y (c - z mean(c z)), z = y r_y,
+        // and mean(c z) from sums that need no D, made together with mean(t o): one exchange between the waves a row.
+        float x[V][8], z[V][8], dd[V][8], t[V][8], o[V][8];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             at.x.get(v, x[v]);
-            at.y.get(v, y[v]);
+            at.y.get(v, z[v]);
             at.d.get(v, dd[v]);
             at.n.get(v, t[v]);
         }
@@ -374,23 +377,22 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (n[v] > column<T>(i) && there) {
-                    const float k = gate[v][i] * post[v][i];
-                    o[v][i] = alpha[v][i] * x[v][i] + (g.y.p ? gate[v][i] * (post[v][i] * (y[v][i] * r_y)) : 0.f);
+                    z[v][i] *= r_y;
+                    o[v][i] = (alpha[v][i] * x[v][i] + (g.y.p ? gate[v][i] * (post[v][i] * z[v][i]) : 0.f)) * r_o;
                     if (g.d_normed.p) {
-                        a_pre[v][i] += t[v][i] * (o[v][i] * r_o);
+                        a_pre[v][i] += t[v][i] * o[v][i];
                         t[v][i] *= pre[v][i];
                         s[0] += t[v][i] * o[v][i];
                         dd[v][i] += r_o * t[v][i];
                     }
-                    const float ky = k * y[v][i];
-                    s[1] += ky * dd[v][i];
-                    s[2] += ky * o[v][i];
+                    const float kz = gate[v][i] * post[v][i] * z[v][i];
+                    s[1] += kz * dd[v][i];
+                    s[2] += kz * o[v][i];
                 }
             }
         row_sum<WAVES, 3>(s, sums[it & 1], w, group * WAVES);
-        const float c1 = g.d_normed.p ? r_o * r_o * r_o * (s[0] * inv) : 0.f;
-        // mean of c y, c = k D: its parts' sums are made with S1's
-        const float c2 = g.w_post ? r_y * r_y * r_y * ((s[1] - c1 * s[2]) * inv) : 0.f;
+        const float c1 = g.d_normed.p ? r_o * (s[0] * inv) : 0.f;
+        const float c2 = g.w_post ? (s[1] - c1 * s[2]) * inv : 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (!there || n[v] <= 0) continue;
@@ -398,12 +400,11 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float D = g.d_normed.p ? dd[v][i] - c1 * o[v][i] : dd[v][i];
-                const float z = y[v][i] * r_y, c = gate[v][i] * post[v][i] * D;
                 dx[i] = alpha[v][i] * D;
-                dy[i] = r_y * c - c2 * y[v][i];
+                dy[i] = r_y * (gate[v][i] * post[v][i] * D - c2 * z[v][i]);
                 a_alpha[v][i] += D * x[v][i];
-                a_post[v][i] += gate[v][i] * D * z;
-                a_gate[v][i] += post[v][i] * D * z;
+                a_post[v][i] += gate[v][i] * D * z[v][i];
+                a_gate[v][i] += post[v][i] * D * z[v][i];
             }
             if (g.d_x.p) put_columns(static_cast<T *>(g.d_x.p) + row * g.d_x.ld + col[v], dx, n[v]);
             if (g.d_y.p) put_columns(static_cast<T *>(g.d_y.p) + row * g.d_y.ld + col[v], dy, n[v]);

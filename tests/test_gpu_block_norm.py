@@ -242,3 +242,12 @@ def test_rows_far_apart():
     moe.block_norm_backward(out, x, y, stats, d_x, d_y, d_normed=normed, **p)
     moe.block_norm_backward(far[2], far[0], far[1], stats, far[2], far[3], d_normed=far[3], **p)
     assert torch.equal(far[2], d_x) and torch.equal(far[3], d_y)
+
+
+@pytest.mark.parametrize("size", [1e15, 1e-15, 1e18])
+def test_backward_of_rows_of_any_size(size):
+    """r^3 of such rows is outside fp32's range."""
+    R, H = 7, 200
+    x, y = randn(1, R, H) * size, randn(2, R, H) * size
+    check_backward(x, y, params(H, R, 1, 1, 1, 1, 3), R, H)
+    check_backward(x, None, params(H, R, 0, 0, 0, 1, 1), R, H)
