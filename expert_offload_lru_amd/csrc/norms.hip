@@ -281,10 +281,12 @@ inline int back_chunks(int H) { return std::max(256, 2048 / std::max(kBackWaves,
 
 Deal deal(int T, int H, int per_gate, bool gate) {
     const int groups = back_groups(H), n = std::max(1, gate ? std::min(per_gate, T) : T);
-    int each = std::max(groups, (T + back_chunks(H) - 1) / back_chunks(H));
-    if (!gate || n >= each) {
-        const int parts = (n + each - 1) / each, gates = (T + n - 1) / n;
-        return {parts * gates, each, parts, 0};
+    const int most = back_chunks(H), gates = std::max(1, (T + n - 1) / n);
+    int each = std::max(groups, (T + most - 1) / most);
+    if (!gate || n >= each) {   // as many whole parts a gate as still make one round
+        each = std::max(groups, (n + std::max(1, most / gates) - 1) / std::max(1, most / gates));
+        const int parts = (n + each - 1) / each;
+        return {T > 0 ? parts * gates : 0, each, parts, 0};
     }
     each = (each + n - 1) / n * n;   // whole gates
     each = std::max(each, n * groups);
