@@ -74,10 +74,20 @@ unsigned row_blocks(int R, int lanes) {
 
 // --------------------------------------------------------------------------------------------- norms
 
+// v plus the value that a lane gets by `CTRL` (0 in rows of 16 lanes outside MASK).
+template <int CTRL, int MASK>
+__device__ inline float plus_from(float v) {
+    return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, MASK, 0xf, false));
+}
+// The wave's sum: by moves between lanes within the vector unit (through LDS: 2048 rows of 8192 forward 28.5 us, so 26.1).
 __device__ inline float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+    v = plus_from<0x111, 0xf>(v);   // row_shr:1 .. 8: lane 15 of each 16 has their sum
+    v = plus_from<0x112, 0xf>(v);
+    v = plus_from<0x114, 0xf>(v);
+    v = plus_from<0x118, 0xf>(v);
+    v = plus_from<0x142, 0xa>(v);   // row_bcast:15
+    v = plus_from<0x143, 0xc>(v);   // row_bcast:31: lane 63 has all
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
 // Sums over the waves of a row; the buffer `s` has a place for each wave and is not written again before
