@@ -317,9 +317,11 @@ int moe_block_norm_backward(const void *d_out, int64_t ld_d_out, const void *d_n
     MOE_TRY(check_ld("d_y", d_y, ld_d_y, hidden));
     const size_t z = elem_size(dtype);
     const bool params = d_w_post || d_gate || d_alpha || d_w_pre;
-    const size_t need = params ? norm_workspace(n_rows, hidden, gate ? rows_per_gate : 1) : 0;
+    // the kernel finds a row's gate by this: a gate of more rows than there are is one of all rows
+    const int per_gate = gate ? std::min(rows_per_gate, std::max(n_rows, 1)) : 1;
+    const size_t need = params ? norm_workspace(n_rows, hidden, per_gate) : 0;
     MOE_TRY(check_workspace(workspace, workspace_bytes, need));
-    const int64_t gates = gate ? (n_rows + (int64_t)rows_per_gate - 1) / rows_per_gate : 0;
+    const int64_t gates = gate ? (n_rows + (int64_t)per_gate - 1) / per_gate : 0;
     const Span none{};
     const Span s_dx = matrix("d_x", d_x, n_rows, hidden, ld_d_x, z), s_dy = matrix("d_y", d_y, n_rows, hidden, ld_d_y, z);
     const Span rows[] = {matrix("d_out", d_out, n_rows, hidden, ld_d_out, z), matrix("d_normed", d_normed, n_rows, hidden, ld_d_normed, z),
@@ -336,7 +338,7 @@ int moe_block_norm_backward(const void *d_out, int64_t ld_d_out, const void *d_n
         MOE_TRY(check_overlap({s_dy}, {same(d_y, ld_d_y, rows[i].p, lds[i]) ? none : rows[i]}));
     }
     NormBackArgs a{{d_out, ld_d_out}, {d_normed, ld_d_normed}, {x, ld_x}, {y, ld_y}, w_post, gate, alpha, w_pre, stats,
-                   n_rows, hidden, gate ? rows_per_gate : 1, {d_x, ld_d_x}, {d_y, ld_d_y}, d_w_post, d_gate, d_alpha, d_w_pre};
+                   n_rows, hidden, per_gate, {d_x, ld_d_x}, {d_y, ld_d_y}, d_w_post, d_gate, d_alpha, d_w_pre};
     if (n_rows == 0 && !params) return MOE_OK;
     return finish(launch_norm_back(dtype, a, workspace, static_cast<hipStream_t>(stream)));
 }
