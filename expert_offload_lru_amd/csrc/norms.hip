@@ -111,6 +111,39 @@ __device__ inline void row_sum(float (&v)[N], float *s, int wave_in_row, int fir
     }
 }
 
+// 1 / sqrt(mean square + eps) of a row; sum: a lane's part of the sum of squares, squares(k): the same of k times the
+// values.  A sum of squares leaves fp32's range where a row's root mean square is 2^64 / sqrt(columns) and more, and loses
+// squares below 2^-126 where eps does not outweigh them; such a row is summed once more, from its values times 2^-80 or
+// 2^80 (exact, and enough for every row whose inverse root is an fp32 number).  Other rows pay a comparison: 2048 rows of
+// 8192 columns 27.5 -> 28.6 us, 6000 of 2560 29.3 -> 30.6, the other widths the same or less.  s, again: a place for each
+// of the ALL waves, as row_sum wants them.
+template <int WAVES, int ALL, typename Squares>
+__device__ inline float inverse_root(float sum, Squares squares, float inv, float eps, float *s, float *again,
+                                     int wave_in_row, int first_wave) {
+    constexpr float kFar = 1.2089258196146292e24f, kNear = 7.888609052210118e-31f;   // 2^80, 2^-100
+    const auto far = [&](float m) { return m == __builtin_inff() || m < kNear; };
+    float v[1] = {sum};
+    row_sum<WAVES, 1>(v, s, wave_in_row, first_wave);
+    const float mean = v[0] * inv + eps;
+    bool any = far(mean);
+    if constexpr (WAVES > 1 && ALL > WAVES) {   // of the workgroup's rows: the sums below meet at a barrier
+#pragma unroll
+        for (int g = 0; g < ALL; g += WAVES) {
+            float m = 0.f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) m += s[g + w];
+            any |= far(m * inv + eps);
+        }
+    }
+    if (__builtin_expect(any, 0)) {
+        const float k = mean < 1.f ? kFar : 1.f / kFar;
+        v[0] = squares(k);
+        row_sum<WAVES, 1>(v, again, wave_in_row, first_wave);
+        if (far(mean)) return k / sqrtf(v[0] * inv + eps * k * k);
+    }
+    return 1.f / sqrtf(mean);
+}
+
 // A lane's 8 columns of a row: next to each other in the 16-bit types; in fp32 4 and, 256 columns on, 4 more, so that each
 // load and store of 16 bytes a lane is whole lines (8192 rows: 3.3 TB/s otherwise).  Column of element i, behind the first:
 template <typename T>
@@ -194,7 +227,7 @@ struct Raw {
 template <typename T, int WAVES, int V>
 __global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void k_norm(NormArgs g) {
     constexpr int GROUPS = WAVES < 4 ? 4 / WAVES : 1, ALL = GROUPS * WAVES;
-    __shared__ float s_y[2][ALL], s_o[2][ALL];
+    __shared__ float s_y[2][ALL], s_o[2][ALL], again[ALL];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = wave / WAVES, w = wave % WAVES;
     int col[V], n[V];
     float post[V][8], pre[V][8], alpha[V][8], gate[V][8];
@@ -224,35 +257,51 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void k_norm(NormArgs 
             for (int v = 0; v < V; ++v) load_vector<T>(g.gate + gate_row * g.H, col[v], n[v], gate[v], 1.f);
         }
         float x[V][8], y[V][8], r_y = 0.f, r_o = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) nx.get(v, x[v]);
         if (g.y.p) {
-            float s[1] = {0.f}, r = 1.f;
+            float s = 0.f, r = 1.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 ny.get(v, y[v]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[0] += y[v][i] * y[v][i];
+                for (int i = 0; i < 8; ++i) s = fmaf(y[v][i], y[v][i], s);
             }
             if (g.w_post) {
-                row_sum<WAVES, 1>(s, s_y[it & 1], w, group * WAVES);
-                r = r_y = 1.f / sqrtf(s[0] * inv + g.eps);
+                const auto squares = [&](float k) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s += (k * y[v][i]) * (k * y[v][i]);
+                    return s;
+                };
+                r = r_y = inverse_root<WAVES, ALL>(s, squares, inv, g.eps, s_y[it & 1], again, w, group * WAVES);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                nx.get(v, x[v]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[v][i] = alpha[v][i] * x[v][i] + gate[v][i] * (post[v][i] * (y[v][i] * r));
                 if (g.out.p && there && n[v] > 0) put_columns(static_cast<T *>(g.out.p) + row * g.out.ld + col[v], x[v], n[v]);
             }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) nx.get(v, x[v]);
         }
         if (g.w_pre) {
-            float s[1] = {0.f};
+            float s = 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[0] += n[v] > column<T>(i) ? x[v][i] * x[v][i] : 0.f;
-            row_sum<WAVES, 1>(s, s_o[it & 1], w, group * WAVES);
-            r_o = 1.f / sqrtf(s[0] * inv + g.eps);
+                for (int i = 0; i < 8; ++i) s += n[v] > column<T>(i) ? x[v][i] * x[v][i] : 0.f;
+            const auto squares = [&](float k) {
+                float s = 0.f;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s += n[v] > column<T>(i) ? (k * x[v][i]) * (k * x[v][i]) : 0.f;
+                return s;
+            };
+            r_o = inverse_root<WAVES, ALL>(s, squares, inv, g.eps, s_o[it & 1], again, w, group * WAVES);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float p[8];

@@ -99,7 +99,9 @@ int moe_experts_product_backward(const void *d_out, int64_t ld_d_out, int dtype,
  * ceil(n_rows / rows_per_gate) rows (n_rows or more a gate: one row for all; 1: a row each), contiguous.
  * NULL: w_post no norm of y (out = alpha x + gate y); gate, alpha 1; w_pre and normed (together) no second
  * norm.  y NULL: the first norm alone, normed = w_pre * (x r_out) (then w_post, gate, alpha and out are NULL).
- * out may be NULL otherwise too.  stats [n_rows x 2] gets r_y and r_out (0 for a norm that is not there);
+ * Mean squares may leave fp32's range, above or below: r_y and r_out are right wherever they are fp32 numbers
+ * themselves and out is finite in fp32.
+ * out may be NULL with y too.  stats [n_rows x 2] gets r_y and r_out (0 for a norm that is not there);
  * NULL: not wanted.  out and normed may each be x or y (the same pointer and ld), but not both the same.
  * Limits: hidden <= 16384; n_rows below 2^23 where hidden > 8192. */
 int moe_block_norm(const void *x, int64_t ld_x, const void *y, int64_t ld_y, int dtype, int n_rows, int hidden,
