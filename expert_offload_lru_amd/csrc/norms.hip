@@ -453,7 +453,9 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
             }
         row_sum<WAVES, 3>(s, sums[it & 1], w, group * WAVES);
         const float c1 = g.d_normed.p ? r_o * (s[0] * inv) : 0.f;
-        const float c2 = g.w_post ? (s[1] - c1 * s[2]) * inv : 0.f;
+        // what is not part of a formula stays out of it, not times 0: out and y may be infinite (6000 rows of 2560 columns
+        // 102.5 -> 105 us, the other widths within 1 %)
+        const float c2 = (g.d_normed.p ? s[1] - c1 * s[2] : s[1]) * inv;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (!there || n[v] <= 0) continue;
@@ -462,7 +464,7 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
             for (int i = 0; i < 8; ++i) {
                 const float D = g.d_normed.p ? dd[v][i] - c1 * o[v][i] : dd[v][i];
                 dx[i] = alpha[v][i] * D;
-                dy[i] = r_y * (gate[v][i] * post[v][i] * D - c2 * z[v][i]);
+                dy[i] = r_y * (gate[v][i] * post[v][i] * D - (g.w_post ? c2 * z[v][i] : 0.f));
                 a_alpha[v][i] += D * x[v][i];
                 a_post[v][i] += gate[v][i] * D * z[v][i];
                 a_gate[v][i] += post[v][i] * D * z[v][i];

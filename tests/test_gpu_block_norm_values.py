@@ -91,3 +91,30 @@ def test_rows_beside_infinite_ones(H):
     for a, b in zip(got, want):
         assert torch.equal(a[same], b[same])
     assert (got[2][[1, 7], 1] == 0).all() and torch.isnan(got[2][4]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H", [96, 1000, 2100, 9000])
+@pytest.mark.parametrize("pre", ["no second norm", "its gradient not given"])
+def test_infinities_that_a_gradient_does_not_depend_on(H, dtype, pre):
+    """Without the second norm's gradient D = d_out: d_y does not see x, d_x sees neither, and without w_post d_y does not
+    see y."""
+    t, R = DTYPES[dtype], 9
+    x, y, d_out = (randn(i, R, H, dtype=t) for i in (1, 2, 21))
+    u, v = x.clone(), y.clone()
+    u[2, 5], u[4], u[6, H - 1] = float("inf"), float("-inf"), float("nan")
+    v[1, 0], v[4, 7], v[8] = float("nan"), float("inf"), float("-inf")
+    for post, gate, alpha in ((1, 1, 1), (1, 0, 0), (0, 1, 1), (0, 0, 1), (0, 0, 0)):
+        p = params(H, R, post, gate, alpha, pre != "no second norm", 4)
+
+        def grads(x, y):
+            d_x, d_y = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+            moe.block_norm_backward(d_out, x, y, forward(x, y, p)[2], d_x, d_y, **p)
+            return d_x, d_y
+
+        want = grads(x, y)
+        for given in ((u, y), (x, v), (u, v)):
+            d_x, d_y = grads(*given)
+            assert torch.equal(d_x, want[0])
+            rows = [0, 2, 3, 5, 6, 7] if post and given[1] is v else list(range(R))
+            assert torch.equal(d_y[rows], want[1][rows])
