@@ -45,8 +45,9 @@ __device__ inline void decode8(uint2 q, int scale, float (&f)[8]) {
     for (int i = 0; i < 8; ++i) {
         const uint32_t w = i < 4 ? q.x : q.y;
         const float v = __builtin_ldexpf((float)(int8_t)(w >> (8 * (i & 3))), scale - kScaleBias);
-        // 127 * 2^121 is within the other types' range
-        f[i] = scale == kScaleNaN ? __builtin_nanf("") : std::is_same_v<T, f16> ? fminf(fmaxf(v, -65504.f), 65504.f) : v;
+        // beyond the other types' range there is one value, -128 * 2^121 (rows that were encoded hold no -128)
+        constexpr float kMost = std::is_same_v<T, f16> ? 65504.f : std::is_same_v<T, bf16> ? 3.3895313892515355e38f : 3.4028234663852886e38f;
+        f[i] = scale == kScaleNaN ? __builtin_nanf("") : fminf(fmaxf(v, -kMost), kMost);
     }
 }
 
