@@ -22,8 +22,12 @@
  *    shared power of two.  The scale is the least (of 0 .. 254) for which the block's largest
  *    size becomes 127 or less when rounded, so a value is off by at most 1/127 of that size; scale 255
  *    marks a block that held an infinity or NaN: its codes are 0 and all its values are read as NaN.
- *  - Limits: n_experts <= 1024; n_rows and every width below 2^24; n_rows times a width below 2^36 (one launch's
- *    workgroups), and so n_experts * inner * outer below 2^37.
+ *  - Limits: n_experts <= 1024; n_rows and every width (2 * inter too) below 2^24; and what the workgroups of one
+ *    launch can be.  With a and b a call's two widths (inner, outer, inter) and w the larger one, quotients by n_rows
+ *    rounded down and the others up:
+ *      (n_rows / 128 + min(n_rows, n_experts)) * (w / 64)  below 2^24 - 16,
+ *      or, if a or b is under 8, (n_rows / 64 + min(n_rows, n_experts)) * (w / 32)  below 2^25 - 32;
+ *      n_experts * (a / 128) * (b / 128)  below 2^24 - 16.
  */
 #ifndef MOE_EXPERTS_H
 #define MOE_EXPERTS_H

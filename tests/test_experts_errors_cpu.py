@@ -152,6 +152,26 @@ def test_more_than_a_launch_holds(n_rows, width, rc):
     assert moe.gpu_lib().moe_experts_product(*{**none, "inner": width, "outer": 64}.values()) == rc
 
 
+@pytest.mark.parametrize("n_rows,E,inner,outer,rc", [
+    # (n_rows / 128 + min(n_rows, E)) * ceil(w / 64) < 2^24 - 16
+    (1024, 1024, 8, 64 * 16256, INV), (1024, 1024, 8, 64 * 16256 + 1, UNS), (1151, 1024, 8, 64 * 16256, INV), (1152, 1024, 8, 64 * 16256, UNS),
+    (1024, 1024, 8, 1 << 22, UNS), (1, 1024, 8, 1 << 20, INV), ((1 << 24) - 1, 1, 64, 64 * 127, INV), ((1 << 24) - 1, 1, 64, 64 * 128, UNS),
+    # widths under 8: (n_rows / 64 + min(n_rows, E)) * ceil(w / 32) < 2^25 - 32
+    (65280, 4, 7, 32 * 32767, INV), (65280, 4, 7, 32 * 32767 + 1, UNS), (65343, 4, 7, 32 * 32767, INV), (65344, 4, 7, 32 * 32767, UNS),
+    # E * ceil(inner / 128) * ceil(outer / 128) < 2^24 - 16
+    (1, 1024, 127 * 128, 129 * 128, INV), (1, 1024, 127 * 128, 129 * 128 + 1, UNS), (1, 1024, 128 * 128, 128 * 128, UNS),
+])
+def test_what_the_workgroups_of_one_launch_can_be(n_rows, E, inner, outer, rc):
+    """The documented limits, on either side; refused before the tensors are looked at (they are NULL here)."""
+    lib = moe.gpu_lib()
+    for a, b in ((inner, outer), (outer, inner)):
+        none = dict(x=None, ld_x=a, dtype=1, n_rows=n_rows, inner=a, outer=b, offsets=None, n_experts=E, w=None)
+        assert lib.moe_experts_product(*none.values(), None, b, None) == rc
+        assert lib.moe_experts_hidden(*none.values(), 0, None, b, None, 0, None, 0, None, 0, None) == rc
+        assert lib.moe_experts_hidden_backward(*none.values(), 0, None, 0, None, 0, None, 0, None, 0, None, 0, None) == rc
+        assert lib.moe_experts_product_backward(*none.values(), None, 0, None, 0, None, 0, None, a, 64, None, 0, None) == rc
+
+
 def test_activation_names():
     from expert_offload_lru_amd import experts
     assert experts._activation("silu") == 0 and experts._activation("gelu") == 1
