@@ -1,9 +1,11 @@
 // Rows kept in 8 bits: blocks of 32 columns, int8 codes and a shared power of two.
 //
-// value = code * 2^e, e = scale - 133.  e is the least exponent for which the block's largest size, over
-// 2^e and rounded, is 127 or less, so the largest code is 64 .. 127 and a value is off by at most 2^(e-1).
-// A power of two makes the codes exact values of the 16-bit types: code * 2^e has 7 bits, so reading a row
-// back rounds nothing (a product with a scale of 24 bits would round again), and x / 2^e is exact.
+// value = code * 2^e, e = scale - 133 from -133 to 121.  e is the least of these for which the block's largest size, over
+// 2^e and rounded, is 127 or less (121 where none is), so from a largest size of 2^-127 on the largest code is 64 .. 127
+// and a value is off by at most 2^(e-1) (2^e at 121); blocks below have e = -133 and smaller codes.
+// A power of two makes the codes exact values of fp32 and bf16: code * 2^e has 7 bits and is no less than bf16's least
+// step, so reading a row back rounds nothing (a product with a scale of 24 bits would round again), and x / 2^e is
+// exact.  fp16 takes the values that are within its range and not below its least step as they are.
 #pragma once
 
 #include <type_traits>

@@ -19,9 +19,10 @@
  *  - Weights are contiguous [n_experts x outer x inner], of dtype.
  *  - Rows kept in 8 bits: codes int8 [rows x cols], scales uint8 [rows x ceil(cols / 32)], with ld of their
  *    own.  Column c of a row has the value codes[c] * 2^(scales[c / 32] - 133): an int8 block of 32 with a
- *    shared power of two.  The scale is the least (of 0 .. 254) for which the block's largest
- *    size becomes 127 or less when rounded, so a value is off by at most 1/127 of that size; scale 255
- *    marks a block that held an infinity or NaN: its codes are 0 and all its values are read as NaN.
+ *    shared power of two.  The scale is the least (of 0 .. 254) for which the block's largest size becomes 127 or
+ *    less when rounded (254 where that takes more), so a value is off by at most 1/127 of that size, or by 2^-134 where
+ *    that size is under 2^-127.  Scale 255 marks a block that held an infinity or NaN: its codes are 0 and all its
+ *    values are read as NaN.  Reading rounds nothing in fp32 and bf16; fp16 has its own range and subnormal steps.
  *  - Limits: n_experts <= 1024; n_rows and every width (2 * inter too) below 2^24; and what the workgroups of one
  *    launch can be.  With a and b a call's two widths (inner, outer, inter) and w the larger one, quotients by n_rows
  *    rounded down and the others up:

@@ -38,3 +38,25 @@ def test_least_code_in_a_weight_gradient(M, dtype):
     moe.experts_product_backward(d, off, w, codes=codes, scales=scales, d_w=a)
     moe.experts_product_backward(d, off, w, x=back, d_w=b)
     assert torch.equal(a, b) and torch.isfinite(a).all() and (a == torch.finfo(t).max / 4).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_how_far_values_are_off(dtype):
+    """By 1/127 of the block's largest size; by 2^-134 where that is under 2^-127."""
+    t = DTYPES[dtype]
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(300, 96, generator=g, dtype=torch.float64)
+    tops = torch.randint(-149, 128, (300, 3), generator=g).double()
+    tops[:40], tops[40:80] = torch.arange(-149, -109)[:, None].double(), torch.arange(88, 128)[:, None].double()
+    x = (x.view(300, 3, 32) / x.view(300, 3, 32).abs().amax(-1, keepdim=True) * 1.99 * 2.0 ** tops[..., None]).reshape(300, 96).to(t)
+    x[250:, ::32] = torch.finfo(t).max
+    assert torch.isfinite(x).all()
+    codes, scales = torch.empty(300, 96, dtype=torch.int8, device="cuda"), torch.empty(300, 3, dtype=torch.uint8, device="cuda")
+    back = torch.empty(300, 96, dtype=t, device="cuda")
+    moe.rows_encode(x.cuda(), codes, scales)
+    moe.rows_decode(codes, scales, back)
+    v = x.double().view(300, 3, 32)
+    off, top = (back.cpu().double().view(300, 3, 32) - v).abs().amax(-1), v.abs().amax(-1)
+    assert (off <= torch.where(top >= 2.0 ** -127, top / 127, torch.full_like(top, 2.0 ** -134))).all()
+    largest = codes.cpu().view(300, 3, 32).abs().amax(-1)
+    assert ((largest >= 64) | (top < 2.0 ** -127)).all()
