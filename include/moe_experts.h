@@ -5,9 +5,11 @@
  * (library: expert_offload_lru_amd/libmoe_offload.so).
  *
  * moe_layer_forward (moe_offload.h) runs frozen 4-bit experts; these entry points are for experts that a
- * caller trains, or serves in its own types, on the rows of moe_tokens_dispatch (moe_tokens.h), with or
- * without adapters beside them.  A training step is: moe_block_norm, moe_tokens_dispatch,
- * moe_experts_hidden, moe_experts_product, moe_tokens_combine, and back through the same.
+ * caller trains, or serves in its own types, on the rows of moe_tokens_dispatch (moe_tokens.h).  A training
+ * step is: moe_block_norm, moe_tokens_dispatch, moe_experts_hidden, moe_experts_product,
+ * moe_tokens_combine, and back through the same.  Adapters (moe_adapters_forward with the product as its base)
+ * go beside moe_experts_product; moe_experts_hidden takes none beside its projections, which it joins before
+ * anything is written.
  *
  * Conventions: those of moe_tokens.h (streams, captured graphs, strides, overlaps, errors, indexes checked
  * on the device, the same bits from the same inputs), and
