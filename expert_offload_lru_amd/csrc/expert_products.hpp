@@ -381,8 +381,10 @@ __device__ inline void reduce(const Source &sa, const Source &sb, int fa, Da da,
     wait_and_meet<0>();   // the LDS is free for the results
 }
 
-// 1 / (1 + exp(-g)); the 16-bit types take the hardware's exponential and reciprocal (off by 2^-20 at most, a
-// sixteenth of their rounding and less; half the time of a tile's activations).
+// 1 / (1 + exp(-g)); the 16-bit types take the hardware's exponential and reciprocal (half the time of a tile's
+// activations).  Off by (|g| + 5) 2^-23 of itself at most: two roundings of the exponential's argument, 1 unit in the last
+// place each of the two instructions, and 0 from about g = -87 down, where it is no normal number.  An activation that is
+// a normal number of its type has g > -13 in f16 and, above that cut, g > -88 in bf16: under a hundredth of its rounding.
 template <typename T>
 __device__ inline float sigmoid(float g) {
     if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-g));

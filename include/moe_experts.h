@@ -44,7 +44,9 @@
 extern "C" {
 #endif
 
-/* ---------------------------------------------------------------- activations of the gate */
+/* ---------------------------------------------------------------- activations of the gate
+ * Evaluated in fp32, with their slopes: 0 where the exponential leaves fp32 (silu from about g = -87 down), infinity or NaN
+ * as the formulas give it at an infinite g (its slope: NaN). */
 #define MOE_ACT_SILU  0   /* g / (1 + exp(-g)) */
 #define MOE_ACT_GELU  1   /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
 
