@@ -31,7 +31,7 @@ enum Kind { KC, KR, KR_CODES };
 // bits; the loads write LDS (codes: registers, by as many instructions whatever is asked for).  Otherwise through
 // registers, STAGES steps of them: PIECES, 16 bytes at any element; ELEMENTS, where a row is shorter than a piece.
 enum Way { DIRECT, PIECES, ELEMENTS };
-enum Epi { E_HIDDEN, E_PLAIN, E_HIDDEN_BACK, E_GRAD };
+enum Epi { E_HIDDEN, E_PLAIN, E_HIDDEN_BACK };
 
 constexpr int kRsrcWord3 = 0x00020000;    // buffer resource flags of the gfx9 family (raw, untyped)
 constexpr int kOut = (int)0x80000000;     // a buffer offset past every range: the load gives zeros
