@@ -453,8 +453,9 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
             }
         row_sum<WAVES, 3>(s, sums[it & 1], w, group * WAVES);
         const float c1 = g.d_normed.p ? r_o * (s[0] * inv) : 0.f;
-        // what is not part of a formula stays out of it, not times 0: out and y may be infinite (6000 rows of 2560 columns
-        // 102.5 -> 105 us, the other widths within 1 %)
+        // What is not part of a formula stays out of it, not times 0: out and y may be infinite.  The selection in the loop
+        // costs 6000 rows of 2560 columns 102.5 -> 105 us and 1024 of 16384 306 -> 320, up to 2 % elsewhere; the loop twice, with
+        // and without w_post, takes 30 registers more.
         const float c2 = (g.d_normed.p ? s[1] - c1 * s[2] : s[1]) * inv;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
