@@ -114,14 +114,15 @@ __device__ inline void row_sum(float (&v)[N], float *s, int wave_in_row, int fir
 // 1 / sqrt(mean square + eps) of a row; sum: a lane's part of the sum of squares, squares(k): the same of k times the
 // values.  A sum of squares leaves fp32's range where a row's root mean square is 2^64 / sqrt(columns) and more, and loses
 // squares below 2^-126 where eps does not outweigh them; such a row is summed once more, from its values times 2^-80 or
-// 2^80 (exact, and enough for every row whose inverse root is an fp32 number).  Other rows pay a comparison: 2048 rows of
-// 8192 columns 27.5 -> 28.6 us, 6000 of 2560 29.3 -> 30.6, the other widths the same or less.  s, again: a place for each
-// of the ALL waves, as row_sum wants them.
+// 2^80 (exact, and enough for every row whose inverse root is an fp32 number).  Other rows pay a comparison (65536 rows of
+// 64 columns 37.8 -> 39.6 us; nothing to 2 % from 512 columns on).  s, again: a place for each of the ALL waves, as row_sum
+// wants them.
 template <int WAVES, int ALL, typename Squares>
 __device__ inline float inverse_root(float sum, Squares squares, float inv, float eps, float *s, float *again,
                                      int wave_in_row, int first_wave) {
-    constexpr float kFar = 1.2089258196146292e24f, kNear = 7.888609052210118e-31f;   // 2^80, 2^-100
-    const auto far = [&](float m) { return m == __builtin_inff() || m < kNear; };
+    constexpr float kFar = 1.2089258196146292e24f;   // 2^80
+    constexpr uint32_t kLeast = (127 - 100) << 23, kInf = 0x7F800000u;   // 2^-100; a mean below it, infinite or NaN is far
+    const auto far = [](float m) { return __float_as_uint(m) - kLeast >= kInf - kLeast; };
     float v[1] = {sum};
     row_sum<WAVES, 1>(v, s, wave_in_row, first_wave);
     const float mean = v[0] * inv + eps;
@@ -331,8 +332,10 @@ struct Deal {
 
 constexpr int kBackWaves = 4;   // waves of a workgroup, at least
 
-// Waves along a row and columns (x8) of a lane for a width.
-inline int back_waves(int H) { return H <= 512 ? 1 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 6 * 512 ? 6 : H <= 8192 ? 8 : 16; }
+// Waves along a row; a lane has 8 columns, 16 above 4096 (bf16: 16384 rows of 500 columns, 1 wave 45 us, 2 72; of 1000, 2 waves 76,
+// 4 121, one with 16 columns a lane 66; 8192 of 2048, 4 waves 56, 8 82, 2 with 16 55; 6000 of 2560, 8 waves 74, 6 105, 4 with 16 79;
+// 4096 of 4096, 8 waves 64, 16 275, 4 with 16 62; 2048 of 8192, 8 with 16 71, 16 waves 218).
+inline int back_waves(int H) { return H <= 512 ? 1 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 8192 ? 8 : 16; }
 inline int back_groups(int H) { return std::max(1, kBackWaves / back_waves(H)); }
 // One round of workgroups: two waves a SIMD, as the registers allow (16384 rows of 2048: 97 us; two rows
 // ahead 105, three waves 130).
@@ -454,8 +457,8 @@ __global__ __launch_bounds__(WAVES > kBackWaves ? WAVES * 64 : kBackWaves * 64) 
         row_sum<WAVES, 3>(s, sums[it & 1], w, group * WAVES);
         const float c1 = g.d_normed.p ? r_o * (s[0] * inv) : 0.f;
         // What is not part of a formula stays out of it, not times 0: out and y may be infinite.  The selection in the loop
-        // costs 6000 rows of 2560 columns 102.5 -> 105 us and 1024 of 16384 306 -> 320, up to 2 % elsewhere; the loop twice, with
-        // and without w_post, takes 30 registers more.
+        // costs 1024 rows of 16384 columns 306 -> 320 us and up to 2 % elsewhere; the loop twice, with and without w_post, takes 30
+        // registers more.
         const float c2 = (g.d_normed.p ? s[1] - c1 * s[2] : s[1]) * inv;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -552,14 +555,18 @@ __global__ __launch_bounds__(1024) void k_norm_join(NormBackArgs g, Deal d, cons
 
 template <typename T>
 hipError_t norm_launch(const NormArgs &a, hipStream_t stream) {
-    // about as many workgroups as run at a time: more rows each keep the parameters longer
+    // Waves a row: 8 columns a lane, 16 above 8192 columns (bf16: 16384 rows of 500 columns, 1 wave 18 us, 2 30; of 1000, 2 waves 27,
+    // 4 40, one with 16 columns a lane 28; 8192 of 2048, 4 waves 25, 8 37, 2 with 16 28; 6000 of 2560, 6 waves 29, 8 30, 4 with 16 34;
+    // 4096 of 4096, 8 waves 25, 16 40, 4 with 16 26; 2048 of 8192, 16 waves 26, 8 with 16 28).
+    // Workgroups: as many as run at a time, since more rows each keep the parameters longer (the same cases with 256, 512, 1024 and
+    // 2048: 40 26 18 19 us; 65 38 27 27; 48 30 25 25; 43 29 30 35; 32 25 26 28; 26 29 33 39; 1024 of 16384 columns 54 68 89 89).
     const auto grid = [&](int rows, int most) { return dim3((unsigned)std::min((a.T + rows - 1) / rows, most)); };
     if (a.H <= 512) return launch(k_norm<T, 1, 1>, grid(4, 2048), dim3(256), stream, nullptr, nullptr, a);
-    if (a.H <= 1024) return launch(k_norm<T, 2, 1>, grid(2, 2048), dim3(256), stream, nullptr, nullptr, a);
+    if (a.H <= 1024) return launch(k_norm<T, 2, 1>, grid(2, 1024), dim3(256), stream, nullptr, nullptr, a);
     if (a.H <= 2048) return launch(k_norm<T, 4, 1>, grid(1, 1024), dim3(256), stream, nullptr, nullptr, a);
-    if (a.H <= 6 * 512) return launch(k_norm<T, 6, 1>, grid(1, 1024), dim3(384), stream, nullptr, nullptr, a);
-    if (a.H <= 4096) return launch(k_norm<T, 8, 1>, grid(1, 1024), dim3(512), stream, nullptr, nullptr, a);
-    if (a.H <= 8192) return launch(k_norm<T, 16, 1>, grid(1, 512), dim3(1024), stream, nullptr, nullptr, a);
+    if (a.H <= 6 * 512) return launch(k_norm<T, 6, 1>, grid(1, 512), dim3(384), stream, nullptr, nullptr, a);
+    if (a.H <= 4096) return launch(k_norm<T, 8, 1>, grid(1, 512), dim3(512), stream, nullptr, nullptr, a);
+    if (a.H <= 8192) return launch(k_norm<T, 16, 1>, grid(1, 256), dim3(1024), stream, nullptr, nullptr, a);
     return launch(k_norm<T, 16, 2>, grid(1, 256), dim3(1024), stream, nullptr, nullptr, a);
 }
 
@@ -574,7 +581,6 @@ hipError_t norm_back_launch(const NormBackArgs &a, float *parts, hipStream_t str
         if (w == 1) e = launch(k_norm_back<T, 1, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else if (w == 2) e = launch(k_norm_back<T, 2, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else if (w == 4) e = launch(k_norm_back<T, 4, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
-        else if (w == 6) e = launch(k_norm_back<T, 6, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else if (a.H <= 4096) e = launch(k_norm_back<T, 8, 1>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else if (w == 8) e = launch(k_norm_back<T, 8, 2>, grid, block, stream, nullptr, nullptr, a, d, parts);
         else e = launch(k_norm_back<T, 16, 2>, grid, block, stream, nullptr, nullptr, a, d, parts);
