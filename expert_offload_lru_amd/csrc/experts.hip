@@ -36,7 +36,8 @@ __global__ __launch_bounds__(256) void k_grad_join(const float *parts, float *d_
 // The larger tile from 128 rows an expert on where there are at least four rounds of it, or from 1024 rows on (128 experts,
 // 768 x 2048: 64 rows each 144 us against the smaller's 139, 128 rows 174 / 214, 512 rows 309 / 400; 8 experts, 2048 x 1536,
 // one and a half rounds: 512 rows 46 / 40, 2048 rows 113 / 133).  Widths that are not whole pieces go through
-// registers, in the smaller one.  Runs of an expert's rows, 512 and more, until there is a workgroup a CU (two of the
+// registers, in the smaller one (so do rows at other addresses, with the runs of the larger one if it was chosen: the plan
+// and the workspace go by sizes).  Runs of an expert's rows, 512 and more, until there is a workgroup a CU (two of the
 // smaller ones): a run's partial sums are written and read once more.
 GradPlan grad_plan(int R, int M, int N, int E) {
     const int64_t wide = (int64_t)tiles(M, Wide::BM) * tiles(N, Wide::BN) * E, mid = (int64_t)tiles(M, Mid::BM) * tiles(N, Mid::BN) * E;
