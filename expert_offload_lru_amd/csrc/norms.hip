@@ -126,8 +126,8 @@ __device__ inline float inverse_root(float sum, Squares squares, float inv, floa
     float v[1] = {sum};
     row_sum<WAVES, 1>(v, s, wave_in_row, first_wave);
     const float mean = v[0] * inv + eps;
-    bool any = far(mean);
-    if constexpr (WAVES > 1 && ALL > WAVES) {   // of the workgroup's rows: the sums below meet at a barrier
+    bool any = false;   // the same in all waves that meet at the sums' barrier: of all their rows, from the same numbers
+    if constexpr (WAVES > 1 && ALL > WAVES) {
 #pragma unroll
         for (int g = 0; g < ALL; g += WAVES) {
             float m = 0.f;
@@ -135,6 +135,8 @@ __device__ inline float inverse_root(float sum, Squares squares, float inv, floa
             for (int w = 0; w < WAVES; ++w) m += s[g + w];
             any |= far(m * inv + eps);
         }
+    } else {
+        any = far(mean);
     }
     if (__builtin_expect(any, 0)) {
         const float k = mean < 1.f ? kFar : 1.f / kFar;
